@@ -2,7 +2,10 @@
  * moefp8.h -- C ABI of libmoefp8.so: the forward of one fused routed-expert FP8 MoE layer on
  * NVIDIA B200 (sm_100a): the whole layer on one GPU (moe_forward), the gate in front of its
  * router (moe_gate), and the device steps of expert parallelism over the GPUs of a node
- * (moe_ep_dispatch, moe_forward_rows, moe_combine_rows), around an all-to-all the caller runs.
+ * (moe_ep_dispatch, moe_forward_rows, moe_combine_rows), around an all-to-all the caller runs;
+ * and the operators around the layer: the residual RMS norm with an 8-bit output
+ * (moe_add_rms_norm), the dense FP8 product (moe_linear), and the router's balance loss and
+ * gradients (moe_balance_loss, moe_route_backward).
  *
  * The layer (sources are web pages, cited by title and section):
  *   "MindIE-SD Fused MoE" -- function signature and parameter table (hidden_states,
@@ -336,6 +339,122 @@ int moe_forward_rows(const moe_config_t *cfg, const void *rows, const int32_t *e
                      size_t workspace_bytes, void *stream);
 int moe_combine_rows(const moe_config_t *cfg, const float *o_rows, int32_t num_rows, const int32_t *slot_pos,
                      const float *topk_weights, void *y, int32_t *status, void *stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * Around the layer.  These entry points have no counterpart on the pages; they are what a user of
+ * the layer calls next to it: the residual addition and RMS norm in front of it, the dense FP8
+ * products of the same block, and what its router is trained with.  They follow the conventions
+ * above; a row's output does not depend on the other rows' values.
+ *
+ * Quantized rows: E4M3 codes [rows, cols] and K-block-major scales, one 4-byte word per (128-column
+ * block, row), [cols/128][scale_rows]: the fp32 scale (recipe 0), or the block's four UE8M0 bytes,
+ * lowest 32 columns in the lowest byte (recipes 1, 2).  scale_rows is rows + 132 rounded up to 4;
+ * words past `rows` are never written and never affect a result.
+ *
+ * moe_quantized_size: bytes of both buffers, and the row stride (host call; NULL outputs are skipped). */
+int moe_quantized_size(int32_t rows, int32_t cols, size_t *codes_bytes, size_t *scales_bytes, size_t *scale_rows);
+
+/* The residual addition, the RMS norm of its result, and the norm's 8-bit form, in one pass:
+ *   h = x + residual (fp32),  y = h / sqrt(mean_h h^2 + rms_eps) * norm_weight
+ * cfg: num_tokens, hidden (at most 32768) and recipe are used.
+ *   x              device bf16 [T, H]
+ *   residual       device [T, H], bf16 (residual_fp32 = 0) or fp32 (1), or NULL: h = x
+ *   norm_weight    device fp32 [H]
+ *   residual_out   device, type of residual; out: h (rounded once for bf16); NULL: not stored.
+ *                  NULL when residual is NULL.
+ *   y              device bf16 [T, H] or NULL; out
+ *   codes, scales  device, quantized rows of the unrounded y, or both NULL; out
+ * At least one output.  residual_out may be the residual or (bf16) x buffer itself, and y the x
+ * buffer or (bf16) the residual buffer; buffers may not overlap in any other way.  Every buffer
+ * 16-byte aligned.  One launch.  Inf or NaN in a row makes y, or the values its codes stand for,
+ * non-finite in that row only. */
+int moe_add_rms_norm(const moe_config_t *cfg, const void *x, const void *residual, int residual_fp32,
+                     const float *norm_weight, float rms_eps, void *residual_out, void *y, void *codes,
+                     void *scales, void *stream);
+
+/* A dense FP8 product: y = act(x W + bias) + residual, summed and finished in fp32, rounded once to
+ * bf16.  recipe as in moe_config_t (0, 1, 2); activation one of MOE_ACT_*.
+ * Limits (MOE_ERR_UNSUPPORTED): in_features % 128; out_features even for recipe 2. */
+#define MOE_ACT_NONE 0
+#define MOE_ACT_RELU 1
+#define MOE_ACT_SILU 2
+#define MOE_ACT_GELU 3        /* 0.5 v (1 + erf(v / sqrt 2)) */
+#define MOE_ACT_GELU_TANH 4   /* 0.5 v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) */
+typedef struct {
+    int32_t num_tokens, in_features, out_features;   /* T, K, N */
+    int32_t recipe, activation;
+} moe_linear_config_t;
+
+/* Weights, laid out once: w [K, N] E4M3 codes (recipe 2: E2M1 pairs, [K, N/2] bytes, the even column
+ * in the low nibble), w_scale fp32 [K/128, N] (recipe 0) or UE8M0 bytes [K/32, N], as
+ * moe_transform_weights takes them for one expert.  Outputs: sizes from
+ * moe_transformed_linear_size; w_t 32-byte, ws_t 16-byte aligned.  num_tokens is not used. */
+int moe_transformed_linear_size(const moe_linear_config_t *cfg, size_t *w_bytes, size_t *ws_bytes);
+int moe_transform_linear_weights(const moe_linear_config_t *cfg, const void *w, const void *w_scale, void *w_t,
+                                 void *ws_t, void *stream);
+
+/* Workspace bytes of moe_linear for cfg->num_tokens bf16 rows; with quantized rows the first
+ * MOE_LINEAR_STATUS_BYTES are enough.  moe_read_status reads its status word. */
+#define MOE_LINEAR_STATUS_BYTES 1024
+int moe_linear_workspace_size(const moe_linear_config_t *cfg, size_t *bytes);
+
+/*   x              device bf16 [T, K], quantized by the call (two launches), or NULL
+ *   codes, scales  device, quantized rows [T, K] (one launch), or NULL; exactly one of x and codes
+ *   w_t, ws_t      device, from moe_transform_linear_weights
+ *   bias           device bf16 [N] or NULL
+ *   residual       device bf16 [T, N] or NULL (may be y itself)
+ *   y              device bf16 [T, N]; out
+ *   workspace      device, 256-byte aligned; not shared by calls in flight at the same time
+ * Alignment: x, codes, scales, bias, residual, y 16 bytes.  A row's bits depend on num_tokens only
+ * through the kernel it selects. */
+int moe_linear(const moe_linear_config_t *cfg, const void *x, const void *codes, const void *scales, const void *w_t,
+               const void *ws_t, const void *bias, const void *residual, void *y, void *workspace,
+               size_t workspace_bytes, void *stream);
+
+/* The router's balance loss, from the logits and ids of moe_route or moe_gate.  Sequence s holds the
+ * tokens seq_offsets[s] .. seq_offsets[s+1] - 1; a token counts when it lies in a sequence and its
+ * token_mask is not zero (the logits and ids of other tokens are not read).  With n_s counted tokens,
+ *   p[t, e] = softmax(logits[t])                              (routing 0)
+ *           = sigmoid(logits[t, e]) / sum_j sigmoid(logits[t, j])   (routing 1)
+ *   loss = coef / S' * sum_s sum_e  E / (k n_s) counts[s, e] * mean_t p[t, e],  S' sequences have n_s > 0
+ * (0 when none has).  cfg: num_tokens, num_experts, top_k and routing are used.
+ *   router_logits  device fp32 [T, E];  topk_idx  device int32 [T, k]
+ *   token_mask     device uint8 [T] or NULL (every token counts)
+ *   seq_offsets    device int32 [num_seqs + 1], ascending, in [0, T], or NULL: one sequence of all
+ *                  tokens (num_seqs 1)
+ *   expert_counts  device int32 [num_seqs, E] out: routed slots per expert
+ *   seq_tokens     device int32 [num_seqs + 1] out: n_s, and S' last
+ *   mean_probs     device fp32 [num_seqs, E] out: mean p (0 for a sequence without counted tokens)
+ *   loss           device fp32 [1] out
+ *   workspace      device, moe_balance_workspace_size bytes, 256-byte aligned; not shared by calls in
+ *                  flight at the same time.  An id outside [0, E) is not counted, offsets that
+ *                  descend or leave [0, T] make the sums undefined; both set the workspace's status
+ *                  word to MOE_ERR_BOUNDS.
+ * Two launches; the result is the same on every run (no atomics on floats). */
+int moe_balance_workspace_size(const moe_config_t *cfg, int32_t num_seqs, size_t *bytes);
+int moe_balance_loss(const moe_config_t *cfg, const float *router_logits, const int32_t *topk_idx,
+                     const uint8_t *token_mask, const int32_t *seq_offsets, int32_t num_seqs, float coef,
+                     int32_t *expert_counts, int32_t *seq_tokens, float *mean_probs, float *loss, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/* The gradient of the router's logits: from the routing weights of moe_route (routing, renormalize,
+ * per_expert_scale, routed_scaling_factor; the choice of experts and groups is piecewise constant),
+ * and from the balance loss (the counts are constants).
+ *   d_topk_weights  device fp32 [T, k] or NULL
+ *   d_loss          device fp32 [1] or NULL (no balance loss: the arguments from coef to num_seqs
+ *                   are not used), the gradient of moe_balance_loss's loss
+ *   expert_counts, seq_tokens  as moe_balance_loss wrote them; token_mask, seq_offsets as given to it
+ *   d_logits        device fp32 [T, E] out, every row written; a row with neither gradient is zero,
+ *                   whatever its logits are
+ *   d_per_expert_scale  device fp32 [E] or NULL; out (needs per_expert_scale)
+ *   workspace       as for moe_balance_loss with the same num_seqs; only used (and may be NULL
+ *                   otherwise) when d_per_expert_scale is wanted
+ * An id outside [0, E) adds nothing.  One launch, two with d_per_expert_scale. */
+int moe_route_backward(const moe_config_t *cfg, const float *router_logits, const float *per_expert_scale,
+                       const int32_t *topk_idx, const float *d_topk_weights, const float *d_loss, float coef,
+                       const int32_t *expert_counts, const int32_t *seq_tokens, const uint8_t *token_mask,
+                       const int32_t *seq_offsets, int32_t num_seqs, float *d_logits, float *d_per_expert_scale,
+                       void *workspace, size_t workspace_bytes, void *stream);
 
 /* Create / destroy a stage profiler (creates CUDA events on the current device). */
 int moe_profile_create(moe_profile_t **prof);

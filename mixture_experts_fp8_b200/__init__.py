@@ -9,7 +9,9 @@ Entry points (same names as the C ABI):
     check_config, transformed_weights_size, transform_weights, workspace_size,
     workspace_layout, route, forward, forward_profiled, forward_static_workspace, read_status,
     selftest_bounded_wait,
-    Profile (moe_profile_create / read / reset / destroy).
+    Profile (moe_profile_create / read / reset / destroy);
+around the layer:
+    add_rms_norm, transform_linear_weights, linear, balance_loss, route_backward.
 """
 from __future__ import annotations
 
@@ -38,7 +40,11 @@ EXPORTED = (
     "moe_debug_unfused_gate_up",
     "moe_debug_inject_fault", "moe_gate", "moe_gate_weights_size", "moe_transform_gate_weights",
     "moe_ep_dispatch", "moe_forward_rows", "moe_combine_rows",
+    "moe_quantized_size", "moe_add_rms_norm", "moe_transformed_linear_size", "moe_transform_linear_weights",
+    "moe_linear_workspace_size", "moe_linear", "moe_balance_workspace_size", "moe_balance_loss", "moe_route_backward",
 )
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = range(5)
+MOE_LINEAR_STATUS_BYTES = 1024
 MOE_FAULT_NONE = 0
 MOE_FAULT_SKIP_STAGE = 1
 
@@ -55,6 +61,10 @@ class _Cfg(ctypes.Structure):
                  "renormalize", "group_count", "k_group", "group_select_mode")] + \
                [("routed_scaling_factor", ctypes.c_float), ("recipe", ctypes.c_int32),
                 ("shared_experts", ctypes.c_int32)]
+
+
+class _LinearCfg(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_tokens", "in_features", "out_features", "recipe", "activation")]
 
 
 _LAYOUT_FIELDS = ("status", "topk_idx", "topk_weights", "counts", "offsets", "tile_start",
@@ -97,6 +107,19 @@ class Config:
         return 128 if self.recipe == 0 else 32
 
 
+@dataclass
+class LinearConfig:
+    """One dense product (moe_linear_config_t): recipe as Config's, activation one of ACT_*."""
+    num_tokens: int
+    in_features: int
+    out_features: int
+    recipe: int = 0
+    activation: int = ACT_NONE
+
+    def c(self) -> _LinearCfg:
+        return _LinearCfg(self.num_tokens, self.in_features, self.out_features, self.recipe, self.activation)
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -113,7 +136,7 @@ def _load():
             raise ImportError("libmoefp8.so is missing and could not be built")
         lib = ctypes.CDLL(LIB_PATH)
         P, I, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
-        CP = ctypes.POINTER(_Cfg)
+        CP, LP = ctypes.POINTER(_Cfg), ctypes.POINTER(_LinearCfg)
         lib.moe_last_error.restype = ctypes.c_char_p
         lib.moe_last_error.argtypes = []
         sig = {
@@ -142,6 +165,15 @@ def _load():
             "moe_ep_dispatch": [CP, I, P, P, P, P, P, P, P, S, P],
             "moe_forward_rows": [CP] + [P] * 10 + [S, P],
             "moe_combine_rows": [CP, P, ctypes.c_int32, P, P, P, P, P],
+            "moe_quantized_size": [ctypes.c_int32, ctypes.c_int32] + [ctypes.POINTER(S)] * 3,
+            "moe_add_rms_norm": [CP, P, P, I, P, ctypes.c_float] + [P] * 5,
+            "moe_transformed_linear_size": [LP, ctypes.POINTER(S), ctypes.POINTER(S)],
+            "moe_transform_linear_weights": [LP] + [P] * 5,
+            "moe_linear_workspace_size": [LP, ctypes.POINTER(S)],
+            "moe_linear": [LP] + [P] * 9 + [S, P],
+            "moe_balance_workspace_size": [CP, ctypes.c_int32, ctypes.POINTER(S)],
+            "moe_balance_loss": [CP] + [P] * 4 + [ctypes.c_int32, ctypes.c_float] + [P] * 5 + [S, P],
+            "moe_route_backward": [CP] + [P] * 5 + [ctypes.c_float] + [P] * 4 + [ctypes.c_int32] + [P] * 3 + [S, P],
         }
         for name, args in sig.items():
             f = getattr(lib, name)
@@ -171,6 +203,12 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _raw_stream(stream, dev):
+    """The stream's handle; the current stream of dev by default."""
+    import torch
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 # --------------------------------------------------------------------------------------------
@@ -394,6 +432,231 @@ def debug_inject_fault(fault: int) -> None:
     """Arm a fault for the next forward on this thread (the debug library only; the release
     library raises MoeError with MOE_ERR_UNSUPPORTED)."""
     _check(_load().moe_debug_inject_fault(int(fault)))
+
+
+# -------------------------------------------------------------------------------------------- around the layer
+def _refuse(msg: str):
+    raise MoeError(MOE_ERR_INVALID_ARG, msg)
+
+
+def _device_of(t, name: str):
+    """The device of a call's first tensor, which has to be the current one (its stream and kernels)."""
+    import torch
+    dev = t.device
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        _refuse(f"{name} is on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _arg(t, name: str, shape, dtype, dev):
+    """Pointer of tensor t (None: NULL); anything but a contiguous tensor of this shape, type and device is refused."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        _refuse(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got "
+                f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+    return t.data_ptr()
+
+
+def _workspace_arg(t, dev):
+    if t.device != dev or not t.is_contiguous():
+        _refuse(f"workspace must be a contiguous tensor on {dev}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def quantized_size(rows: int, cols: int):
+    """(bytes of the codes, bytes of the scales, scale_rows) of quantized rows."""
+    out = [ctypes.c_size_t() for _ in range(3)]
+    _check(_load().moe_quantized_size(rows, cols, *[ctypes.byref(o) for o in out]))
+    return tuple(o.value for o in out)
+
+
+def new_quantized(rows: int, cols: int, device="cuda"):
+    """Buffers for quantized rows: (codes uint8 [rows, cols], scale words int32 [cols/128, scale_rows])."""
+    import torch
+    scale_rows = quantized_size(rows, cols)[2]
+    return (torch.empty((rows, cols), dtype=torch.uint8, device=device),
+            torch.empty((cols // 128, scale_rows), dtype=torch.int32, device=device))
+
+
+def _quantized_args(q, rows, cols, dev):
+    import torch
+    if q is None:
+        return None, None
+    return (_arg(q[0], "codes", (rows, cols), torch.uint8, dev),
+            _arg(q[1], "scales", (cols // 128, (rows + 135) // 4 * 4), torch.int32, dev))
+
+
+def add_rms_norm(cfg: Config, x, norm_weight, rms_eps: float, residual=None, residual_out=None, y=None,
+                 quantized=None, want_y=True, want_quantized=True, stream=None):
+    """h = x + residual; y = h / sqrt(mean h^2 + rms_eps) * norm_weight; quantized = the codes and scales of y.
+    x bf16 [T, H], residual bf16 or fp32 [T, H] or None.  Outputs that are not passed are allocated.
+    -> (h in the residual's type, or x without one; y bf16 or None; (codes, scale words) or None)."""
+    import torch
+    dev = _device_of(x, "x")
+    T, H = cfg.num_tokens, cfg.hidden
+    shape = (T, H)
+    if residual is None:
+        if residual_out is not None:
+            _refuse("residual_out needs a residual")
+    elif residual.dtype not in (torch.bfloat16, torch.float32):
+        _refuse(f"residual must be bfloat16 or float32, got {residual.dtype}")
+    elif residual_out is None:
+        residual_out = torch.empty_like(residual)
+    if y is None and want_y:
+        y = torch.empty_like(x)
+    if quantized is None and want_quantized:
+        quantized = (torch.empty(shape, dtype=torch.uint8, device=dev),
+                     torch.empty((H // 128, (T + 135) // 4 * 4), dtype=torch.int32, device=dev))
+    rt = None if residual is None else residual.dtype
+    c = cfg.c()
+    _check(_load().moe_add_rms_norm(
+        ctypes.byref(c), _arg(x, "x", shape, torch.bfloat16, dev), _arg(residual, "residual", shape, rt, dev),
+        1 if rt == torch.float32 else 0, _arg(norm_weight, "norm_weight", (H,), torch.float32, dev), rms_eps,
+        _arg(residual_out, "residual_out", shape, rt, dev), _arg(y, "y", shape, torch.bfloat16, dev),
+        *_quantized_args(quantized, T, H, dev), _raw_stream(stream, dev)))
+    return (x if residual is None else residual_out), y, quantized
+
+
+def transformed_linear_size(cfg: LinearConfig):
+    c = cfg.c()
+    out = [ctypes.c_size_t() for _ in range(2)]
+    _check(_load().moe_transformed_linear_size(ctypes.byref(c), *[ctypes.byref(o) for o in out]))
+    return tuple(o.value for o in out)
+
+
+def transform_linear_weights(cfg: LinearConfig, w, w_scale, stream=None):
+    """w [K, N] codes (recipe 2: [K, N/2] bytes of pairs) and w_scale (fp32 [K/128, N], or UE8M0 bytes
+    [K/32, N]) -> (w_t, ws_t) uint8 device tensors, for any num_tokens."""
+    import torch
+    dev = _device_of(w, "w")
+    K, N, g = cfg.in_features, cfg.out_features, 128 if cfg.recipe == 0 else 32
+    outs = [torch.empty(n, dtype=torch.uint8, device=dev) for n in transformed_linear_size(cfg)]
+    c = cfg.c()
+    _check(_load().moe_transform_linear_weights(
+        ctypes.byref(c), _arg(w, "w", (K, N // 2 if cfg.recipe == 2 else N), torch.uint8, dev),
+        _arg(w_scale, "w_scale", (K // g, N), torch.float32 if cfg.recipe == 0 else torch.uint8, dev),
+        *[o.data_ptr() for o in outs], _raw_stream(stream, dev)))
+    return tuple(outs)
+
+
+def linear_workspace_size(cfg: LinearConfig) -> int:
+    c = cfg.c()
+    n = ctypes.c_size_t()
+    _check(_load().moe_linear_workspace_size(ctypes.byref(c), ctypes.byref(n)))
+    return n.value
+
+
+def new_linear_workspace(cfg: LinearConfig, device="cuda"):
+    """A workspace for linear() on bf16 rows (quantized rows need its first MOE_LINEAR_STATUS_BYTES only)."""
+    import torch
+    return torch.empty(linear_workspace_size(cfg), dtype=torch.uint8, device=device)
+
+
+def linear(cfg: LinearConfig, weights, x=None, quantized=None, bias=None, residual=None, y=None, workspace=None,
+           stream=None):
+    """y = act(x W + bias) + residual, bf16 [T, N].  Exactly one of x (bf16 [T, K], quantized by the call) and
+    quantized (codes and scale words, as add_rms_norm returns them); weights from transform_linear_weights."""
+    import torch
+    if (x is None) == (quantized is None):
+        _refuse("pass exactly one of x and quantized")
+    dev = _device_of(x if quantized is None else quantized[0], "x")
+    T, K, N = cfg.num_tokens, cfg.in_features, cfg.out_features
+    if y is None:
+        y = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+    if workspace is None:
+        n = linear_workspace_size(cfg) if quantized is None else MOE_LINEAR_STATUS_BYTES
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    c = cfg.c()
+    w_t, ws_t = weights
+    sizes = transformed_linear_size(cfg)
+    bf16 = torch.bfloat16
+    _check(_load().moe_linear(
+        ctypes.byref(c), _arg(x, "x", (T, K), bf16, dev), *_quantized_args(quantized, T, K, dev),
+        _arg(w_t, "w_t", (sizes[0],), torch.uint8, dev), _arg(ws_t, "ws_t", (sizes[1],), torch.uint8, dev),
+        _arg(bias, "bias", (N,), bf16, dev), _arg(residual, "residual", (T, N), bf16, dev),
+        _arg(y, "y", (T, N), bf16, dev), *_workspace_arg(workspace, dev), _raw_stream(stream, dev)))
+    return y
+
+
+def balance_workspace_size(cfg: Config, num_seqs: int = 1) -> int:
+    c = cfg.c()
+    n = ctypes.c_size_t()
+    _check(_load().moe_balance_workspace_size(ctypes.byref(c), num_seqs, ctypes.byref(n)))
+    return n.value
+
+
+def new_balance_workspace(cfg: Config, num_seqs: int = 1, device="cuda"):
+    import torch
+    return torch.empty(balance_workspace_size(cfg, num_seqs), dtype=torch.uint8, device=device)
+
+
+def _seq_args(cfg, token_mask, seq_offsets, dev):
+    """(mask pointer, offsets pointer, number of sequences)."""
+    import torch
+    n = 1
+    if seq_offsets is not None:
+        n = seq_offsets.numel() - 1
+        if n < 1:
+            _refuse("seq_offsets must hold at least two offsets")
+    if token_mask is not None and token_mask.dtype == torch.bool:
+        token_mask = token_mask.view(torch.uint8)
+    return (_arg(token_mask, "token_mask", (cfg.num_tokens,), torch.uint8, dev),
+            _arg(seq_offsets, "seq_offsets", (n + 1,), torch.int32, dev), n)
+
+
+def balance_loss(cfg: Config, router_logits, topk_idx, coef: float, seq_offsets=None, token_mask=None,
+                 workspace=None, stream=None):
+    """The router's balance loss over the sequences of seq_offsets (int32 [S + 1]; None: one sequence),
+    of the tokens whose token_mask (uint8 or bool [T]) is set.
+    -> (loss fp32 [1], expert_counts int32 [S, E], seq_tokens int32 [S + 1], mean_probs fp32 [S, E])."""
+    import torch
+    dev = _device_of(router_logits, "router_logits")
+    T, E = cfg.num_tokens, cfg.num_experts
+    mask, off, S = _seq_args(cfg, token_mask, seq_offsets, dev)
+    counts = torch.empty((S, E), dtype=torch.int32, device=dev)
+    tokens = torch.empty(S + 1, dtype=torch.int32, device=dev)
+    mean = torch.empty((S, E), dtype=torch.float32, device=dev)
+    loss = torch.empty(1, dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = new_balance_workspace(cfg, S, dev)
+    c = cfg.c()
+    _check(_load().moe_balance_loss(
+        ctypes.byref(c), _arg(router_logits, "router_logits", (T, E), torch.float32, dev),
+        _arg(topk_idx, "topk_idx", (T, cfg.top_k), torch.int32, dev), mask, off, S, coef, counts.data_ptr(),
+        tokens.data_ptr(), mean.data_ptr(), loss.data_ptr(), *_workspace_arg(workspace, dev), _raw_stream(stream, dev)))
+    return loss, counts, tokens, mean
+
+
+def route_backward(cfg: Config, router_logits, topk_idx, d_topk_weights=None, per_expert_scale=None, d_loss=None,
+                   coef: float = 0.0, expert_counts=None, seq_tokens=None, seq_offsets=None, token_mask=None,
+                   d_logits=None, workspace=None, stream=None):
+    """The gradient of the router logits from the routing weights (d_topk_weights fp32 [T, k]) and from the
+    balance loss (d_loss fp32 [1], with balance_loss's arguments and its expert_counts and seq_tokens).
+    -> (d_logits fp32 [T, E], d_per_expert_scale fp32 [E] or None without per_expert_scale)."""
+    import torch
+    dev = _device_of(router_logits, "router_logits")
+    T, E, k = cfg.num_tokens, cfg.num_experts, cfg.top_k
+    f32 = torch.float32
+    mask, off, S = _seq_args(cfg, token_mask, seq_offsets, dev)
+    if d_logits is None:
+        d_logits = torch.empty((T, E), dtype=f32, device=dev)
+    d_scale, ws = None, (None, 0)
+    if per_expert_scale is not None:
+        d_scale = torch.empty(E, dtype=f32, device=dev)
+        if workspace is None:
+            workspace = new_balance_workspace(cfg, S, dev)
+        ws = _workspace_arg(workspace, dev)
+    c = cfg.c()
+    _check(_load().moe_route_backward(
+        ctypes.byref(c), _arg(router_logits, "router_logits", (T, E), f32, dev),
+        _arg(per_expert_scale, "per_expert_scale", (E,), f32, dev),
+        _arg(topk_idx, "topk_idx", (T, k), torch.int32, dev), _arg(d_topk_weights, "d_topk_weights", (T, k), f32, dev),
+        _arg(d_loss, "d_loss", (1,), f32, dev), coef, _arg(expert_counts, "expert_counts", (S, E), torch.int32, dev),
+        _arg(seq_tokens, "seq_tokens", (S + 1,), torch.int32, dev), mask, off, S,
+        _arg(d_logits, "d_logits", (T, E), f32, dev), None if d_scale is None else d_scale.data_ptr(), *ws,
+        _raw_stream(stream, dev)))
+    return d_logits, d_scale
 
 
 class Profile:

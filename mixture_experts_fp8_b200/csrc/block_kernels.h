@@ -1,0 +1,119 @@
+// block_kernels.h -- host-side launchers of the kernels around the layer (internal header): the
+// residual RMS norm, the dense FP8 product, the balance loss and the router's gradients.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace moe {
+
+struct NormArgs {
+    const __nv_bfloat16* x;     // [T, H]
+    const void* res;            // [T, H] bf16 or fp32, or null
+    const float* w;             // [H]
+    void* res_out;              // as res, or null
+    __nv_bfloat16* y;           // [T, H] or null
+    uint8_t* xq;                // [T, H] or null
+    uint32_t* xs;               // [H/128][a_pad] words
+    int T, H, recipe, a_pad, res_fp32;
+    float eps;
+    int tpr;                    // threads per row (set by the launcher)
+};
+
+struct QuantRowsArgs {
+    const __nv_bfloat16* x;     // [T, K]
+    uint8_t* xq;                // [T, K]
+    uint32_t* xs;               // [K/128][a_pad] words
+    int32_t* status;            // cleared to MOE_OK
+    int T, K, recipe, a_pad;
+};
+
+// Weight transform of one dense product: w [K, N] -> K-major rows, scales re-laid.
+struct LinearTransformArgs {
+    const uint8_t* w;
+    const void* ws;
+    uint8_t* w_t;
+    void* ws_t;
+    int K, N, recipe;
+};
+
+struct LinearArgs {
+    int T, N, K, recipe, act;
+    int a_pad;                  // row stride of the activation scales
+    const void* a_scale;        // [K/128][a_pad] words
+    const void* w_scale;        // recipe 0: fp32 [K/128][n_pad]; else 512-byte atoms [n_pad/128][K/128]
+    const __nv_bfloat16* bias;  // [N] or null
+    const __nv_bfloat16* res;   // [T, N] or null
+    __nv_bfloat16* y;           // [T, N]
+    int32_t* status;
+    int clear;                  // the kernel clears the status word (it is the call's first)
+};
+
+// Output columns are padded to this in the transformed scales.
+constexpr int kLinearPad = 256;
+inline int linear_n_pad(int N) { return (N + kLinearPad - 1) / kLinearPad * kLinearPad; }
+
+cudaError_t launch_add_rms_norm(NormArgs a, cudaStream_t s);
+cudaError_t launch_quant_rows(const QuantRowsArgs& a, cudaStream_t s);
+cudaError_t launch_linear_transform(const LinearTransformArgs& a, cudaStream_t s);
+// tmX: codes [T, K], tmW: codes [N, K] (box rows as the two functions say).
+uint32_t linear_token_box(const LinearArgs& a);
+uint32_t linear_weight_box(const LinearArgs& a);
+cudaError_t launch_linear(const LinearArgs& a, const CUtensorMap& tmX, const CUtensorMap& tmW, int num_sms,
+                          cudaStream_t s);
+cudaError_t launch_linear_fp32(const LinearArgs& a, const CUtensorMap& tmX, const CUtensorMap& tmW, int num_sms,
+                               cudaStream_t s);
+cudaError_t launch_linear_mx(const LinearArgs& a, const CUtensorMap& tmX, const CUtensorMap& tmW, int num_sms,
+                             cudaStream_t s);
+
+// Tokens are taken in chunks; chunk c and sequence s that meet have the partial sums of slot c + s:
+// walking the tokens in order raises c or s at every step, so no two pairs share a slot.
+constexpr int kBalanceChunks = 148;
+inline int balance_chunk(int T) {
+    const int c = (T + kBalanceChunks - 1) / kBalanceChunks;
+    return c < 32 ? 32 : c;
+}
+inline int balance_chunks(int T) { return (T + balance_chunk(T) - 1) / balance_chunk(T); }
+
+struct BalanceArgs {
+    const float* logits;        // [T, E]
+    const int32_t* idx;         // [T, K]
+    const uint8_t* mask;        // [T] or null: 0 = not counted
+    const int32_t* off;         // [S + 1] or null (one sequence of all tokens)
+    float* part_p;              // [chunks + S][E]
+    int32_t* part_n;            // [chunks + S][E + 2] counts, counted tokens, ids out of range
+    float* seq_loss;            // [S]
+    int32_t* ticket;
+    int32_t* counts;            // [S, E]
+    int32_t* tokens;            // [S + 1]
+    float* mean;                // [S, E]
+    float* loss;                // [1]
+    int32_t* status;
+    int T, E, K, S, routing, chunk, chunks;
+    float coef;
+};
+
+struct RouteBackwardArgs {
+    const float* logits;        // [T, E]
+    const int32_t* idx;         // [T, K]
+    const float* dw;            // [T, K] or null
+    const float* pes;           // [E] or null
+    const float* dloss;         // [1] or null (no balance loss)
+    const int32_t* counts;      // [S, E]
+    const int32_t* tokens;      // [S + 1]
+    const uint8_t* mask;
+    const int32_t* off;
+    float* dl;                  // [T, E]
+    float* dpes;                // [E] or null
+    float* part;                // [chunks][E] partial sums of dpes
+    int T, E, K, S, routing, renorm, chunk, chunks;
+    float rsf, coef;
+};
+
+cudaError_t launch_balance(const BalanceArgs& a, cudaStream_t s);
+cudaError_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t s);
+
+}  // namespace moe

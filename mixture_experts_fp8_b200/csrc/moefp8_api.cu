@@ -16,6 +16,7 @@
 #include <string>
 #include <vector>
 
+#include "block_kernels.h"
 #include "moe_common.cuh"
 #include "moe_kernels.h"
 
@@ -671,6 +672,257 @@ int moe_forward(const moe_config_t* cfg, const void* hidden_states, const float*
     return moe_forward_profiled(cfg, hidden_states, router_logits, per_expert_scale, topk_idx, topk_weights, w13_t,
                                 w13s_t, w2_t, w2s_t, w13_bias, w2_bias, y, expert_counts, workspace, workspace_bytes,
                                 nullptr, stream);
+}
+
+// ============================================================================ around the layer
+namespace {
+
+// Regions of the balance workspace.
+struct BalanceLayout {
+    size_t ticket, seq_loss, part_p, part_n, total;
+};
+
+int balance_layout(const moe_config_t* c, int32_t num_seqs, const char* who, BalanceLayout* L) {
+    if (num_seqs < 1 || num_seqs > (1 << 24))
+        return fail(MOE_ERR_INVALID_ARG, "%s: num_seqs must be in [1, 2^24], got %d", who, num_seqs);
+    const size_t slots = static_cast<size_t>(moe::balance_chunks(c->num_tokens)) + num_seqs, E = c->num_experts;
+    L->ticket = 256;                                    // the status word comes first
+    L->seq_loss = 512;
+    L->part_p = align_up(L->seq_loss + 4 * static_cast<size_t>(num_seqs), 256);
+    L->part_n = align_up(L->part_p + 4 * slots * E, 256);
+    L->total = align_up(L->part_n + 4 * slots * (E + 2), 256);
+    return MOE_OK;
+}
+
+int check_linear(const moe_linear_config_t* c) {
+    if (!c) return fail(MOE_ERR_INVALID_ARG, "linear config is NULL");
+    if (c->num_tokens <= 0 || c->in_features <= 0 || c->out_features <= 0)
+        return fail(MOE_ERR_INVALID_ARG, "num_tokens (%d), in_features (%d) and out_features (%d) must be > 0",
+                    c->num_tokens, c->in_features, c->out_features);
+    if (c->recipe < 0 || c->recipe > 2)
+        return fail(MOE_ERR_INVALID_ARG, "recipe must be 0 (fp32 per 128), 1 (MXFP8) or 2 (W4A8), got %d", c->recipe);
+    if (c->activation < MOE_ACT_NONE || c->activation > MOE_ACT_GELU_TANH)
+        return fail(MOE_ERR_INVALID_ARG, "activation must be one of MOE_ACT_*, got %d", c->activation);
+    if (c->in_features % 128)
+        return fail(MOE_ERR_UNSUPPORTED, "in_features (%d) must be a multiple of 128", c->in_features);
+    if (c->recipe == 2 && c->out_features % 2)
+        return fail(MOE_ERR_UNSUPPORTED, "out_features (%d) must be even for recipe 2 (codes in pairs)", c->out_features);
+    if (c->num_tokens > (1 << 24) || c->in_features > (1 << 20) || c->out_features > (1 << 20))
+        return fail(MOE_ERR_UNSUPPORTED, "problem too large: at most 2^24 tokens and 2^20 features");
+    return MOE_OK;
+}
+
+size_t linear_scale_bytes(int32_t rows, int32_t cols) { return static_cast<size_t>(cols / 128) * scale_rows_of(rows) * 4; }
+
+}  // namespace
+
+int moe_quantized_size(int32_t rows, int32_t cols, size_t* codes_bytes, size_t* scales_bytes, size_t* scale_rows) {
+    if (rows <= 0 || cols <= 0) return fail(MOE_ERR_INVALID_ARG, "rows (%d) and cols (%d) must be > 0", rows, cols);
+    if (cols % 128) return fail(MOE_ERR_UNSUPPORTED, "cols (%d) must be a multiple of 128", cols);
+    if (codes_bytes) *codes_bytes = static_cast<size_t>(rows) * cols;
+    if (scales_bytes) *scales_bytes = linear_scale_bytes(rows, cols);
+    if (scale_rows) *scale_rows = scale_rows_of(rows);
+    return ok();
+}
+
+int moe_add_rms_norm(const moe_config_t* cfg, const void* x, const void* residual, int residual_fp32,
+                     const float* norm_weight, float rms_eps, void* residual_out, void* y, void* codes, void* scales,
+                     void* stream) {
+    int rc = check_config(cfg);
+    if (rc) return rc;
+    if (!x || !norm_weight) return fail(MOE_ERR_INVALID_ARG, "moe_add_rms_norm: NULL pointer");
+    if ((codes == nullptr) != (scales == nullptr))
+        return fail(MOE_ERR_INVALID_ARG, "moe_add_rms_norm: pass both codes and scales, or neither");
+    if (!residual_out && !y && !codes) return fail(MOE_ERR_INVALID_ARG, "moe_add_rms_norm: no output");
+    if (residual_out && !residual)
+        return fail(MOE_ERR_INVALID_ARG, "moe_add_rms_norm: residual_out needs a residual");
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(norm_weight, 16) || !aligned(residual_out, 16) ||
+        !aligned(y, 16) || !aligned(codes, 16) || !aligned(scales, 16))
+        return fail(MOE_ERR_INVALID_ARG, "moe_add_rms_norm: buffers need 16-byte alignment");
+    if (!(rms_eps >= 0.0f)) return fail(MOE_ERR_INVALID_ARG, "moe_add_rms_norm: rms_eps must be >= 0");
+    if (cfg->hidden > 32768)
+        return fail(MOE_ERR_UNSUPPORTED, "moe_add_rms_norm: hidden (%d) exceeds 32768", cfg->hidden);
+    DeviceInfo di;
+    if ((rc = device_info(&di))) return rc;
+    moe::NormArgs a{};
+    a.x = static_cast<const __nv_bfloat16*>(x);
+    a.res = residual;
+    a.w = norm_weight;
+    a.res_out = residual_out;
+    a.y = static_cast<__nv_bfloat16*>(y);
+    a.xq = static_cast<uint8_t*>(codes);
+    a.xs = static_cast<uint32_t*>(scales);
+    a.T = cfg->num_tokens;
+    a.H = cfg->hidden;
+    a.recipe = cfg->recipe;
+    a.a_pad = static_cast<int>(scale_rows_of(cfg->num_tokens));
+    a.res_fp32 = residual_fp32 != 0;
+    a.eps = rms_eps;
+    MOE_CUDA_TRY(moe::launch_add_rms_norm(a, static_cast<cudaStream_t>(stream)));
+    return ok();
+}
+
+int moe_transformed_linear_size(const moe_linear_config_t* cfg, size_t* w_bytes, size_t* ws_bytes) {
+    int rc = check_linear(cfg);
+    if (rc) return rc;
+    if (!w_bytes || !ws_bytes) return fail(MOE_ERR_INVALID_ARG, "NULL size pointer");
+    *w_bytes = static_cast<size_t>(cfg->out_features) * cfg->in_features / (cfg->recipe == 2 ? 2 : 1);
+    *ws_bytes = static_cast<size_t>(cfg->in_features / 128) * moe::linear_n_pad(cfg->out_features) * 4;
+    return ok();
+}
+
+int moe_transform_linear_weights(const moe_linear_config_t* cfg, const void* w, const void* w_scale, void* w_t,
+                                 void* ws_t, void* stream) {
+    int rc = check_linear(cfg);
+    if (rc) return rc;
+    if (!w || !w_scale || !w_t || !ws_t) return fail(MOE_ERR_INVALID_ARG, "moe_transform_linear_weights: NULL pointer");
+    if (!aligned(w_scale, cfg->recipe == 0 ? 4 : 1) || !aligned(w_t, 32) || !aligned(ws_t, 16))
+        return fail(MOE_ERR_INVALID_ARG,
+                    "moe_transform_linear_weights: misaligned buffer (w_t needs 32 bytes, ws_t 16)");
+    DeviceInfo di;
+    if ((rc = device_info(&di))) return rc;
+    moe::LinearTransformArgs a{static_cast<const uint8_t*>(w), w_scale, static_cast<uint8_t*>(w_t), ws_t,
+                               cfg->in_features, cfg->out_features, cfg->recipe};
+    MOE_CUDA_TRY(moe::launch_linear_transform(a, static_cast<cudaStream_t>(stream)));
+    return ok();
+}
+
+int moe_linear_workspace_size(const moe_linear_config_t* cfg, size_t* bytes) {
+    int rc = check_linear(cfg);
+    if (rc) return rc;
+    if (!bytes) return fail(MOE_ERR_INVALID_ARG, "NULL bytes pointer");
+    *bytes = MOE_LINEAR_STATUS_BYTES + align_up(static_cast<size_t>(cfg->num_tokens) * cfg->in_features, 1024) +
+             linear_scale_bytes(cfg->num_tokens, cfg->in_features);
+    return ok();
+}
+
+int moe_linear(const moe_linear_config_t* cfg, const void* x, const void* codes, const void* scales, const void* w_t,
+               const void* ws_t, const void* bias, const void* residual, void* y, void* workspace,
+               size_t workspace_bytes, void* stream_) {
+    int rc = check_linear(cfg);
+    if (rc) return rc;
+    if (!w_t || !ws_t || !y || !workspace) return fail(MOE_ERR_INVALID_ARG, "moe_linear: NULL pointer");
+    if ((x == nullptr) == (codes == nullptr) || (codes == nullptr) != (scales == nullptr))
+        return fail(MOE_ERR_INVALID_ARG, "moe_linear: pass exactly one of x, and codes with scales");
+    if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 16) || !aligned(w_t, 32) || !aligned(ws_t, 16) ||
+        !aligned(bias, 16) || !aligned(residual, 16) || !aligned(y, 16) || !aligned(workspace, 256))
+        return fail(MOE_ERR_INVALID_ARG,
+                    "moe_linear: misaligned buffer (rows, scales and bias need 16 bytes, w_t 32, workspace 256)");
+    const int T = cfg->num_tokens, K = cfg->in_features, N = cfg->out_features;
+    const size_t q_at = MOE_LINEAR_STATUS_BYTES, s_at = q_at + align_up(static_cast<size_t>(T) * K, 1024);
+    const size_t need = x ? s_at + linear_scale_bytes(T, K) : static_cast<size_t>(MOE_LINEAR_STATUS_BYTES);
+    if (workspace_bytes < need)
+        return fail(MOE_ERR_INVALID_ARG, "moe_linear: workspace has %zu bytes, needs %zu", workspace_bytes, need);
+    DeviceInfo di;
+    if ((rc = device_info(&di))) return rc;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    cudaStream_t s = static_cast<cudaStream_t>(stream_);
+    moe::LinearArgs a{};
+    a.T = T;
+    a.N = N;
+    a.K = K;
+    a.recipe = cfg->recipe;
+    a.act = cfg->activation;
+    a.a_pad = static_cast<int>(scale_rows_of(T));
+    a.a_scale = x ? ws + s_at : scales;
+    a.w_scale = ws_t;
+    a.bias = static_cast<const __nv_bfloat16*>(bias);
+    a.res = static_cast<const __nv_bfloat16*>(residual);
+    a.y = static_cast<__nv_bfloat16*>(y);
+    a.status = static_cast<int32_t*>(workspace);
+    a.clear = x == nullptr;
+    CUtensorMap tm_x, tm_w;
+    if ((rc = make_kmajor_map(&tm_x, x ? ws + q_at : codes, T, K, moe::linear_token_box(a)))) return rc;
+    if ((rc = make_kmajor_map(&tm_w, w_t, N, K, moe::linear_weight_box(a), cfg->recipe == 2))) return rc;
+    if (x) {
+        moe::QuantRowsArgs q{static_cast<const __nv_bfloat16*>(x), ws + q_at, reinterpret_cast<uint32_t*>(ws + s_at),
+                             a.status, T, K, cfg->recipe, a.a_pad};
+        MOE_CUDA_TRY(moe::launch_quant_rows(q, s));
+    }
+    MOE_CUDA_TRY(moe::launch_linear(a, tm_x, tm_w, di.sms, s));
+    return ok();
+}
+
+int moe_balance_workspace_size(const moe_config_t* cfg, int32_t num_seqs, size_t* bytes) {
+    int rc = check_config(cfg);
+    if (rc) return rc;
+    if (!bytes) return fail(MOE_ERR_INVALID_ARG, "NULL bytes pointer");
+    BalanceLayout L;
+    if ((rc = balance_layout(cfg, num_seqs, "moe_balance_workspace_size", &L))) return rc;
+    *bytes = L.total;
+    return ok();
+}
+
+int moe_balance_loss(const moe_config_t* cfg, const float* router_logits, const int32_t* topk_idx,
+                     const uint8_t* token_mask, const int32_t* seq_offsets, int32_t num_seqs, float coef,
+                     int32_t* expert_counts, int32_t* seq_tokens, float* mean_probs, float* loss, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+    int rc = check_config(cfg);
+    if (rc) return rc;
+    if (!router_logits || !topk_idx || !expert_counts || !seq_tokens || !mean_probs || !loss || !workspace)
+        return fail(MOE_ERR_INVALID_ARG, "moe_balance_loss: NULL pointer");
+    BalanceLayout L;
+    if ((rc = balance_layout(cfg, num_seqs, "moe_balance_loss", &L))) return rc;
+    if (!seq_offsets && num_seqs != 1)
+        return fail(MOE_ERR_INVALID_ARG, "moe_balance_loss: %d sequences need seq_offsets", num_seqs);
+    if (!aligned(router_logits, 4) || !aligned(topk_idx, 4) || !aligned(seq_offsets, 4) || !aligned(expert_counts, 4) ||
+        !aligned(seq_tokens, 4) || !aligned(mean_probs, 4) || !aligned(loss, 4) || !aligned(workspace, 256))
+        return fail(MOE_ERR_INVALID_ARG, "moe_balance_loss: misaligned buffer (the workspace needs 256 bytes)");
+    if (workspace_bytes < L.total)
+        return fail(MOE_ERR_INVALID_ARG, "moe_balance_loss: workspace has %zu bytes, needs %zu", workspace_bytes,
+                    L.total);
+    DeviceInfo di;
+    if ((rc = device_info(&di))) return rc;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const int T = cfg->num_tokens;
+    moe::BalanceArgs a{router_logits, topk_idx, token_mask, seq_offsets, reinterpret_cast<float*>(ws + L.part_p),
+                       reinterpret_cast<int32_t*>(ws + L.part_n), reinterpret_cast<float*>(ws + L.seq_loss),
+                       reinterpret_cast<int32_t*>(ws + L.ticket), expert_counts, seq_tokens, mean_probs, loss,
+                       reinterpret_cast<int32_t*>(ws), T, cfg->num_experts, cfg->top_k, num_seqs, cfg->routing,
+                       moe::balance_chunk(T), moe::balance_chunks(T), coef};
+    MOE_CUDA_TRY(moe::launch_balance(a, static_cast<cudaStream_t>(stream)));
+    return ok();
+}
+
+int moe_route_backward(const moe_config_t* cfg, const float* router_logits, const float* per_expert_scale,
+                       const int32_t* topk_idx, const float* d_topk_weights, const float* d_loss, float coef,
+                       const int32_t* expert_counts, const int32_t* seq_tokens, const uint8_t* token_mask,
+                       const int32_t* seq_offsets, int32_t num_seqs, float* d_logits, float* d_per_expert_scale,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_config(cfg);
+    if (rc) return rc;
+    if (!router_logits || !topk_idx || !d_logits || (!d_topk_weights && !d_loss))
+        return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: NULL pointer (one of d_topk_weights and d_loss is needed)");
+    if (d_loss && (!expert_counts || !seq_tokens))
+        return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: d_loss needs expert_counts and seq_tokens");
+    if (d_per_expert_scale && (!per_expert_scale || !workspace))
+        return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: d_per_expert_scale needs per_expert_scale and a workspace");
+    if (!d_loss) {
+        num_seqs = 1;
+        seq_offsets = nullptr;
+    }
+    BalanceLayout L;
+    if ((rc = balance_layout(cfg, num_seqs, "moe_route_backward", &L))) return rc;
+    if (!seq_offsets && num_seqs != 1)
+        return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: %d sequences need seq_offsets", num_seqs);
+    if (!aligned(router_logits, 4) || !aligned(topk_idx, 4) || !aligned(seq_offsets, 4) || !aligned(expert_counts, 4) ||
+        !aligned(seq_tokens, 4) || !aligned(d_topk_weights, 4) || !aligned(d_loss, 4) || !aligned(d_logits, 4) ||
+        !aligned(per_expert_scale, 4) || !aligned(d_per_expert_scale, 4) || !aligned(workspace, 256))
+        return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: misaligned buffer (the workspace needs 256 bytes)");
+    if (d_per_expert_scale && workspace_bytes < L.total)
+        return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: workspace has %zu bytes, needs %zu", workspace_bytes,
+                    L.total);
+    DeviceInfo di;
+    if ((rc = device_info(&di))) return rc;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const int T = cfg->num_tokens;
+    moe::RouteBackwardArgs a{router_logits, topk_idx, d_topk_weights, per_expert_scale, d_loss, expert_counts,
+                             seq_tokens, token_mask, seq_offsets, d_logits, d_per_expert_scale,
+                             d_per_expert_scale ? reinterpret_cast<float*>(ws + L.part_p) : nullptr, T,
+                             cfg->num_experts, cfg->top_k, num_seqs, cfg->routing, cfg->renormalize != 0,
+                             moe::balance_chunk(T), moe::balance_chunks(T), cfg->routed_scaling_factor, coef};
+    MOE_CUDA_TRY(moe::launch_route_backward(a, static_cast<cudaStream_t>(stream)));
+    return ok();
 }
 
 int moe_profile_create(moe_profile_t** prof) {

@@ -1,0 +1,219 @@
+// norm.cu -- what stands in front of the layer and of a dense product: the residual addition with
+// the RMS norm, and the 8-bit codes and scales of its result (moe_add_rms_norm); and the codes and
+// scales of bf16 rows as they are (the first launch of moe_linear on bf16 input).
+//
+//   h = x + residual (fp32),  r = 1 / sqrt(mean_h h^2 + eps),  y = h * r * w
+//   recipe 0:    s = amax / 448 per 128 columns, q = e4m3(y / s); amax 0 -> s = 1
+//   recipes 1, 2: s = 2^e per 32 columns, e the smallest with amax <= 448 * 2^e; q = e4m3(y * 2^-e)
+// Scales are stored as every GEMM of the library reads them: [H/128][scale_rows] 4-byte words.
+#include "block_kernels.h"
+#include "moe_common.cuh"
+
+namespace moe {
+
+namespace {
+
+__device__ __forceinline__ void unpack8(uint4 raw, float* v) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float* v) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ float absmax8(const float* v) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+    return m;
+}
+
+__device__ __forceinline__ uint2 codes8(const float* v) {
+    return make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+}
+
+// Sixteen lanes hold the 128 columns of one scale block, eight columns each; their maximum.
+__device__ __forceinline__ float group16_max(float m) {
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+}
+
+// fp32 scale of a block with maximum amax, and its codes by IEEE division (the layer's quantizer).
+__device__ __forceinline__ uint2 quant_fp32(const float* v, float amax, float& s) {
+    s = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(v[i], s);
+    return codes8(q);
+}
+
+// UE8M0 scales: four lanes hold a 32-column group.  Returns the codes; word = the four scale bytes
+// of the lane's 128-column block, lowest group in the lowest byte (equal in its sixteen lanes).
+__device__ __forceinline__ uint2 quant_mx(const float* v, uint32_t& word) {
+    float m = absmax8(v);
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const int e = mx_exponent(m);
+    const float inv = exp2_int(-e);
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = v[i] * inv;
+    const int lane = threadIdx.x & 31;
+    word = static_cast<uint32_t>(e + 127) << (8 * ((lane >> 2) & 3));
+    word |= __shfl_xor_sync(0xffffffffu, word, 4);
+    word |= __shfl_xor_sync(0xffffffffu, word, 8);
+    return codes8(q);
+}
+
+}  // namespace
+
+// ------------------------------------------------------------------------------------------
+// TPR threads a row (a multiple of 32), CH chunks of eight columns a thread, so that the row stays
+// in registers between the sum and the scaling and is read once.  Rows of a block are independent.
+// The thread count and the chunks follow from H alone, and the sum is taken in a fixed order: a
+// row's bits do not depend on the batch.  RES: 0 no residual, 1 bf16, 2 fp32.
+template <int CH, int RES>
+__global__ void __launch_bounds__(1024) k_add_rms_norm(NormArgs a) {
+    __shared__ float s_sum[32];
+    pdl_wait_then_release();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int wpr = a.tpr >> 5;                        // warps per row
+    const int sub = warp / wpr;                        // row of the block
+    const long long t = static_cast<long long>(blockIdx.x) * (blockDim.x / a.tpr) + sub;
+    const int rt = tid - sub * a.tpr;                  // thread of the row
+    const bool row_ok = t < a.T;
+    const size_t base = static_cast<size_t>(row_ok ? t : 0) * a.H;
+
+    float h[CH][8];
+    float ss = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int col = (c * a.tpr + rt) * 8;
+        if (row_ok && col < a.H) {
+            unpack8(*reinterpret_cast<const uint4*>(a.x + base + col), h[c]);
+            if (RES == 1) {
+                float r[8];
+                unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.res) + base + col), r);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[c][i] += r[i];
+            } else if (RES == 2) {
+                const float4* r4 = reinterpret_cast<const float4*>(static_cast<const float*>(a.res) + base + col);
+                const float4 r0 = r4[0], r1 = r4[1];
+                h[c][0] += r0.x, h[c][1] += r0.y, h[c][2] += r0.z, h[c][3] += r0.w;
+                h[c][4] += r1.x, h[c][5] += r1.y, h[c][6] += r1.z, h[c][7] += r1.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[c][i] = 0.0f;
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(h[c][i], h[c][i], ss);
+    ss = warp_sum(ss);
+    if (lane == 0) s_sum[warp] = ss;
+    __syncthreads();
+    float tot = 0.0f;
+    for (int w = 0; w < wpr; ++w) tot += s_sum[sub * wpr + w];
+    const float r = 1.0f / sqrtf(tot / static_cast<float>(a.H) + a.eps);
+
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int col = (c * a.tpr + rt) * 8;
+        const bool ok = row_ok && col < a.H;
+        if (RES == 1 && ok && a.res_out)
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.res_out) + base + col) = pack8(h[c]);
+        if (RES == 2 && ok && a.res_out) {
+            float4* o4 = reinterpret_cast<float4*>(static_cast<float*>(a.res_out) + base + col);
+            o4[0] = make_float4(h[c][0], h[c][1], h[c][2], h[c][3]);
+            o4[1] = make_float4(h[c][4], h[c][5], h[c][6], h[c][7]);
+        }
+        float y[8];
+        float4 w0 = make_float4(0.f, 0.f, 0.f, 0.f), w1 = w0;
+        if (ok) {
+            w0 = __ldg(reinterpret_cast<const float4*>(a.w + col));
+            w1 = __ldg(reinterpret_cast<const float4*>(a.w + col) + 1);
+        }
+        const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = h[c][i] * r * w[i];
+        if (ok && a.y) *reinterpret_cast<uint4*>(a.y + base + col) = pack8(y);
+        if (!a.xq) continue;
+        uint2 q;
+        uint32_t word;
+        if (a.recipe == 0) {
+            float s;
+            q = quant_fp32(y, group16_max(absmax8(y)), s);
+            word = __float_as_uint(s);
+        } else {
+            q = quant_mx(y, word);
+        }
+        if (ok) {
+            *reinterpret_cast<uint2*>(a.xq + base + col) = q;
+            if ((lane & 15) == 0) a.xs[static_cast<size_t>(col >> 7) * a.a_pad + t] = word;
+        }
+    }
+}
+
+// The codes and scales of bf16 rows: a thread per eight columns, the arithmetic of the layer's own
+// quantizer.  Clears the status word of the call (its first kernel).
+__global__ void __launch_bounds__(256) k_quant_rows(QuantRowsArgs a) {
+    pdl_wait_then_release();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = MOE_OK;
+    const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+    const int per_row = a.K >> 3;                      // a multiple of 16: a scale block stays in a half warp
+    const long long t = i / per_row;
+    const int col = static_cast<int>(i - t * per_row) * 8;
+    const bool ok = t < a.T;
+    float v[8];
+    unpack8(ok ? __ldg(reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(t) * a.K + col)) : make_uint4(0, 0, 0, 0), v);
+    uint2 q;
+    uint32_t word;
+    if (a.recipe == 0) {
+        float s;
+        q = quant_fp32(v, group16_max(absmax8(v)), s);
+        word = __float_as_uint(s);
+    } else {
+        q = quant_mx(v, word);
+    }
+    if (!ok) return;
+    *reinterpret_cast<uint2*>(a.xq + static_cast<size_t>(t) * a.K + col) = q;
+    if ((threadIdx.x & 15) == 0) a.xs[static_cast<size_t>(col >> 7) * a.a_pad + t] = word;
+}
+
+template <int CH>
+static cudaError_t launch_norm_ch(const NormArgs& a, int rows, cudaStream_t s) {
+    const dim3 grid(static_cast<unsigned>((a.T + rows - 1) / rows)), block(a.tpr * rows);
+    if (!a.res) return launch_pdl(k_add_rms_norm<CH, 0>, grid, block, 0, s, a);
+    return a.res_fp32 ? launch_pdl(k_add_rms_norm<CH, 2>, grid, block, 0, s, a)
+                      : launch_pdl(k_add_rms_norm<CH, 1>, grid, block, 0, s, a);
+}
+
+cudaError_t launch_add_rms_norm(NormArgs a, cudaStream_t s) {
+    // The fewest chunks a thread that keep a row within 256 threads (1024 for the longest rows).
+    const int chunks = a.H / 8;
+    const int ch = chunks <= 256 ? 1 : chunks <= 512 ? 2 : 4;
+    a.tpr = ((chunks + ch - 1) / ch + 31) / 32 * 32;
+    const int rows = a.tpr >= 256 ? 1 : 256 / a.tpr;
+    return ch == 1 ? launch_norm_ch<1>(a, rows, s) : ch == 2 ? launch_norm_ch<2>(a, rows, s) : launch_norm_ch<4>(a, rows, s);
+}
+
+cudaError_t launch_quant_rows(const QuantRowsArgs& a, cudaStream_t s) {
+    const long long n = static_cast<long long>(a.T) * (a.K >> 3);
+    return launch_pdl(k_quant_rows, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, s, a);
+}
+
+}  // namespace moe
