@@ -18,7 +18,9 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from dataclasses import asdict, dataclass
+from dataclasses import dataclass
+
+import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmoefp8.so")
@@ -96,11 +98,13 @@ class Config:
     shared_experts: int = 0
 
     def c(self) -> _Cfg:
-        d = asdict(self)
-        return _Cfg(*(int(d[n]) for n in ("num_tokens", "hidden", "inter", "num_experts", "top_k",
-                                          "routing", "renormalize", "group_count", "k_group",
-                                          "group_select_mode")),
-                    float(d["routed_scaling_factor"]), int(d["recipe"]), int(d["shared_experts"]))
+        v = (self.num_tokens, self.hidden, self.inter, self.num_experts, self.top_k, self.routing,
+             self.renormalize, self.group_count, self.k_group, self.group_select_mode,
+             self.routed_scaling_factor, self.recipe, self.shared_experts)
+        try:
+            return _Cfg(*v)
+        except TypeError:      # numbers of other types (numpy's, tensors')
+            return _Cfg(*(float(x) if i == 10 else int(x) for i, x in enumerate(v)))
 
     @property
     def group(self) -> int:
@@ -117,7 +121,11 @@ class LinearConfig:
     activation: int = ACT_NONE
 
     def c(self) -> _LinearCfg:
-        return _LinearCfg(self.num_tokens, self.in_features, self.out_features, self.recipe, self.activation)
+        v = (self.num_tokens, self.in_features, self.out_features, self.recipe, self.activation)
+        try:
+            return _LinearCfg(*v)
+        except TypeError:
+            return _LinearCfg(*(int(x) for x in v))
 
 
 _lock = threading.Lock()
@@ -126,6 +134,8 @@ _lib = None
 
 def _load():
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -199,7 +209,6 @@ def _ptr(t):
 
 
 def _stream(stream):
-    import torch
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
@@ -207,7 +216,6 @@ def _stream(stream):
 
 def _raw_stream(stream, dev):
     """The stream's handle; the current stream of dev by default."""
-    import torch
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
 
 
@@ -226,7 +234,6 @@ def transformed_weights_size(cfg: Config):
 
 def transform_weights(cfg: Config, w13, w13_scale, w2, w2_scale, stream=None):
     """Device tensors in the pages' layout -> (w13_t, w13s_t, w2_t, w2s_t) uint8 device tensors."""
-    import torch
     sizes = transformed_weights_size(cfg)
     outs = [torch.empty(n, dtype=torch.uint8, device=w13.device) for n in sizes]
     c = cfg.c()
@@ -250,14 +257,12 @@ def workspace_layout(cfg: Config) -> dict:
 
 
 def new_workspace(cfg: Config, device="cuda"):
-    import torch
     return torch.empty(workspace_size(cfg), dtype=torch.uint8, device=device)
 
 
 def route(cfg: Config, router_logits, per_expert_scale=None, topk_idx=None, topk_weights=None,
           stream=None):
     """-> (topk_idx int32 [T,k], topk_weights fp32 [T,k]) on the logits' device."""
-    import torch
     T, k = cfg.num_tokens, cfg.top_k
     if topk_idx is None:
         topk_idx = torch.empty((T, k), dtype=torch.int32, device=router_logits.device)
@@ -279,7 +284,6 @@ def gate_weights_size(cfg: Config) -> int:
 def transform_gate_weights(cfg: Config, norm_weight, router_weight, stream=None):
     """norm_weight fp32 [H] and router_weight fp32 [E, H] (device) -> the gate's weights: a uint8
     device tensor holding w' = norm_weight * router_weight as three bf16 parts [3, E, H]."""
-    import torch
     out = torch.empty(gate_weights_size(cfg), dtype=torch.uint8, device=router_weight.device)
     c = cfg.c()
     _check(_load().moe_transform_gate_weights(ctypes.byref(c), _ptr(norm_weight), _ptr(router_weight), _ptr(out),
@@ -291,7 +295,6 @@ def gate(cfg: Config, hidden_states, gate_weights, rms_eps: float, per_expert_sc
          topk_idx=None, topk_weights=None, stream=None):
     """RMSNorm + router matmul + router top-k (gate_weights from transform_gate_weights).
     -> (logits fp32 [T, E], topk_idx int32 [T, k], topk_weights fp32 [T, k])."""
-    import torch
     T, E, k = cfg.num_tokens, cfg.num_experts, cfg.top_k
     dev = hidden_states.device
     if logits is None:
@@ -310,7 +313,6 @@ def gate(cfg: Config, hidden_states, gate_weights, rms_eps: float, per_expert_sc
 def ep_dispatch(cfg: Config, ranks: int, hidden_states, topk_idx, workspace, stream=None):
     """Order this rank's routed slots by destination rank (rank r owns experts r*E/R ..) ->
     (send_counts int32 [R], send_x bf16 [T*k, H], send_expert int32 [T*k], slot_pos int32 [T, k])."""
-    import torch
     T, H, k = cfg.num_tokens, cfg.hidden, cfg.top_k
     dev = hidden_states.device
     send_counts = torch.empty(ranks, dtype=torch.int32, device=dev)
@@ -328,7 +330,6 @@ def forward_rows(cfg: Config, rows, expert_of_row, weights, w13_bias=None, w2_bi
                  workspace=None, stream=None):
     """Each row through one local expert with weight 1 (cfg: num_tokens = rows, top_k = 1,
     num_experts = this rank's experts) -> o_rows fp32 [N, H]."""
-    import torch
     N, H = cfg.num_tokens, cfg.hidden
     if o_rows is None:
         o_rows = torch.empty((N, H), dtype=torch.float32, device=rows.device)
@@ -346,7 +347,6 @@ def combine_rows(cfg: Config, o_rows, slot_pos, topk_weights, y=None, status=Non
     """y[t] = bf16(sum_j w[t,j] * o_rows[slot_pos[t,j]]) in slot order -> y bf16 [T, H].  A slot
     whose position is outside o_rows adds nothing and sets `status` (device int32) to
     MOE_ERR_BOUNDS."""
-    import torch
     T, H = cfg.num_tokens, cfg.hidden
     if y is None:
         y = torch.empty((T, H), dtype=torch.bfloat16, device=slot_pos.device)
@@ -362,7 +362,6 @@ def forward(cfg: Config, hidden_states, weights, router_logits=None, per_expert_
             expert_counts=None, workspace=None, stream=None, profile: "Profile | None" = None):
     """The fused layer forward.  `weights` = (w13_t, w13s_t, w2_t, w2s_t) from
     transform_weights.  Returns y (bf16 [T, H])."""
-    import torch
     if y is None:
         y = torch.empty((cfg.num_tokens, cfg.hidden), dtype=torch.bfloat16, device=hidden_states.device)
     if workspace is None:
@@ -385,7 +384,6 @@ def forward_static_workspace(cfg: Config, hidden_states, weights, router_logits=
     """The layer forward with its scratch in the library's fixed device array (no workspace
     argument, nothing allocated by the library).  For callers that may not allocate device
     memory; `y` should be preallocated by such callers."""
-    import torch
     if y is None:
         y = torch.empty((cfg.num_tokens, cfg.hidden), dtype=torch.bfloat16, device=hidden_states.device)
     c = cfg.c()
@@ -406,7 +404,6 @@ def debug_unfused_gate_up(cfg: Config, hidden_states, topk_idx, weights, workspa
     """The gate+up step taken apart (test hook): the GEMM stores the fp32 gate/up sums h, then a
     separate SwiGLU + requantization kernel writes the act codes and scales into `workspace`.
     Returns h [A, 2I] fp32 (columns in the transformed order)."""
-    import torch
     A = cfg.num_tokens * (cfg.top_k + cfg.shared_experts)
     h = torch.empty((A, 2 * cfg.inter), dtype=torch.float32, device=hidden_states.device)
     c = cfg.c()
@@ -441,7 +438,6 @@ def _refuse(msg: str):
 
 def _device_of(t, name: str):
     """The device of a call's first tensor, which has to be the current one (its stream and kernels)."""
-    import torch
     dev = t.device
     if dev.type != "cuda" or dev.index != torch.cuda.current_device():
         _refuse(f"{name} is on {dev}, the current device is cuda:{torch.cuda.current_device()}")
@@ -452,10 +448,10 @@ def _arg(t, name: str, shape, dtype, dev):
     """Pointer of tensor t (None: NULL); anything but a contiguous tensor of this shape, type and device is refused."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
-        _refuse(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got "
-                f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got "
+            f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
 def _workspace_arg(t, dev):
@@ -473,14 +469,12 @@ def quantized_size(rows: int, cols: int):
 
 def new_quantized(rows: int, cols: int, device="cuda"):
     """Buffers for quantized rows: (codes uint8 [rows, cols], scale words int32 [cols/128, scale_rows])."""
-    import torch
     scale_rows = quantized_size(rows, cols)[2]
     return (torch.empty((rows, cols), dtype=torch.uint8, device=device),
             torch.empty((cols // 128, scale_rows), dtype=torch.int32, device=device))
 
 
 def _quantized_args(q, rows, cols, dev):
-    import torch
     if q is None:
         return None, None
     return (_arg(q[0], "codes", (rows, cols), torch.uint8, dev),
@@ -492,7 +486,6 @@ def add_rms_norm(cfg: Config, x, norm_weight, rms_eps: float, residual=None, res
     """h = x + residual; y = h / sqrt(mean h^2 + rms_eps) * norm_weight; quantized = the codes and scales of y.
     x bf16 [T, H], residual bf16 or fp32 [T, H] or None.  Outputs that are not passed are allocated.
     -> (h in the residual's type, or x without one; y bf16 or None; (codes, scale words) or None)."""
-    import torch
     dev = _device_of(x, "x")
     T, H = cfg.num_tokens, cfg.hidden
     shape = (T, H)
@@ -506,8 +499,8 @@ def add_rms_norm(cfg: Config, x, norm_weight, rms_eps: float, residual=None, res
     if y is None and want_y:
         y = torch.empty_like(x)
     if quantized is None and want_quantized:
-        quantized = (torch.empty(shape, dtype=torch.uint8, device=dev),
-                     torch.empty((H // 128, (T + 135) // 4 * 4), dtype=torch.int32, device=dev))
+        quantized = (torch.empty_like(x, dtype=torch.uint8),
+                     norm_weight.new_empty((H // 128, (T + 135) // 4 * 4), dtype=torch.int32))
     rt = None if residual is None else residual.dtype
     c = cfg.c()
     _check(_load().moe_add_rms_norm(
@@ -528,7 +521,6 @@ def transformed_linear_size(cfg: LinearConfig):
 def transform_linear_weights(cfg: LinearConfig, w, w_scale, stream=None):
     """w [K, N] codes (recipe 2: [K, N/2] bytes of pairs) and w_scale (fp32 [K/128, N], or UE8M0 bytes
     [K/32, N]) -> (w_t, ws_t) uint8 device tensors, for any num_tokens."""
-    import torch
     dev = _device_of(w, "w")
     K, N, g = cfg.in_features, cfg.out_features, 128 if cfg.recipe == 0 else 32
     outs = [torch.empty(n, dtype=torch.uint8, device=dev) for n in transformed_linear_size(cfg)]
@@ -549,7 +541,6 @@ def linear_workspace_size(cfg: LinearConfig) -> int:
 
 def new_linear_workspace(cfg: LinearConfig, device="cuda"):
     """A workspace for linear() on bf16 rows (quantized rows need its first MOE_LINEAR_STATUS_BYTES only)."""
-    import torch
     return torch.empty(linear_workspace_size(cfg), dtype=torch.uint8, device=device)
 
 
@@ -557,23 +548,23 @@ def linear(cfg: LinearConfig, weights, x=None, quantized=None, bias=None, residu
            stream=None):
     """y = act(x W + bias) + residual, bf16 [T, N].  Exactly one of x (bf16 [T, K], quantized by the call) and
     quantized (codes and scale words, as add_rms_norm returns them); weights from transform_linear_weights."""
-    import torch
     if (x is None) == (quantized is None):
         _refuse("pass exactly one of x and quantized")
     dev = _device_of(x if quantized is None else quantized[0], "x")
     T, K, N = cfg.num_tokens, cfg.in_features, cfg.out_features
     if y is None:
-        y = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+        y = weights[0].new_empty((T, N), dtype=torch.bfloat16)
     if workspace is None:
         n = linear_workspace_size(cfg) if quantized is None else MOE_LINEAR_STATUS_BYTES
         workspace = torch.empty(n, dtype=torch.uint8, device=dev)
     c = cfg.c()
     w_t, ws_t = weights
-    sizes = transformed_linear_size(cfg)
+    w_bytes = K * N // (2 if cfg.recipe == 2 else 1)
+    ws_bytes = K // 128 * ((N + 255) // 256 * 256) * 4
     bf16 = torch.bfloat16
     _check(_load().moe_linear(
         ctypes.byref(c), _arg(x, "x", (T, K), bf16, dev), *_quantized_args(quantized, T, K, dev),
-        _arg(w_t, "w_t", (sizes[0],), torch.uint8, dev), _arg(ws_t, "ws_t", (sizes[1],), torch.uint8, dev),
+        _arg(w_t, "w_t", (w_bytes,), torch.uint8, dev), _arg(ws_t, "ws_t", (ws_bytes,), torch.uint8, dev),
         _arg(bias, "bias", (N,), bf16, dev), _arg(residual, "residual", (T, N), bf16, dev),
         _arg(y, "y", (T, N), bf16, dev), *_workspace_arg(workspace, dev), _raw_stream(stream, dev)))
     return y
@@ -587,13 +578,11 @@ def balance_workspace_size(cfg: Config, num_seqs: int = 1) -> int:
 
 
 def new_balance_workspace(cfg: Config, num_seqs: int = 1, device="cuda"):
-    import torch
     return torch.empty(balance_workspace_size(cfg, num_seqs), dtype=torch.uint8, device=device)
 
 
 def _seq_args(cfg, token_mask, seq_offsets, dev):
     """(mask pointer, offsets pointer, number of sequences)."""
-    import torch
     n = 1
     if seq_offsets is not None:
         n = seq_offsets.numel() - 1
@@ -610,14 +599,11 @@ def balance_loss(cfg: Config, router_logits, topk_idx, coef: float, seq_offsets=
     """The router's balance loss over the sequences of seq_offsets (int32 [S + 1]; None: one sequence),
     of the tokens whose token_mask (uint8 or bool [T]) is set.
     -> (loss fp32 [1], expert_counts int32 [S, E], seq_tokens int32 [S + 1], mean_probs fp32 [S, E])."""
-    import torch
     dev = _device_of(router_logits, "router_logits")
     T, E = cfg.num_tokens, cfg.num_experts
     mask, off, S = _seq_args(cfg, token_mask, seq_offsets, dev)
-    counts = torch.empty((S, E), dtype=torch.int32, device=dev)
-    tokens = torch.empty(S + 1, dtype=torch.int32, device=dev)
-    mean = torch.empty((S, E), dtype=torch.float32, device=dev)
-    loss = torch.empty(1, dtype=torch.float32, device=dev)
+    counts, tokens = topk_idx.new_empty((S, E)), topk_idx.new_empty(S + 1)
+    mean, loss = router_logits.new_empty((S, E)), router_logits.new_empty(1)
     if workspace is None:
         workspace = new_balance_workspace(cfg, S, dev)
     c = cfg.c()
@@ -634,16 +620,15 @@ def route_backward(cfg: Config, router_logits, topk_idx, d_topk_weights=None, pe
     """The gradient of the router logits from the routing weights (d_topk_weights fp32 [T, k]) and from the
     balance loss (d_loss fp32 [1], with balance_loss's arguments and its expert_counts and seq_tokens).
     -> (d_logits fp32 [T, E], d_per_expert_scale fp32 [E] or None without per_expert_scale)."""
-    import torch
     dev = _device_of(router_logits, "router_logits")
     T, E, k = cfg.num_tokens, cfg.num_experts, cfg.top_k
     f32 = torch.float32
     mask, off, S = _seq_args(cfg, token_mask, seq_offsets, dev)
     if d_logits is None:
-        d_logits = torch.empty((T, E), dtype=f32, device=dev)
+        d_logits = torch.empty_like(router_logits)
     d_scale, ws = None, (None, 0)
     if per_expert_scale is not None:
-        d_scale = torch.empty(E, dtype=f32, device=dev)
+        d_scale = torch.empty_like(per_expert_scale)
         if workspace is None:
             workspace = new_balance_workspace(cfg, S, dev)
         ws = _workspace_arg(workspace, dev)

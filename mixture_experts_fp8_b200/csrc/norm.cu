@@ -3,7 +3,7 @@
 // scales of bf16 rows as they are (the first launch of moe_linear on bf16 input).
 //
 //   h = x + residual (fp32),  r = 1 / sqrt(mean_h h^2 + eps),  y = h * r * w
-//   recipe 0:    s = amax / 448 per 128 columns, q = e4m3(y / s); amax 0 -> s = 1
+//   recipe 0:    s = amax * (1/448) per 128 columns, q = e4m3(y / s); amax 0 -> s = 1
 //   recipes 1, 2: s = 2^e per 32 columns, e the smallest with amax <= 448 * 2^e; q = e4m3(y * 2^-e)
 // Scales are stored as every GEMM of the library reads them: [H/128][scale_rows] 4-byte words.
 #include "block_kernels.h"
@@ -50,9 +50,11 @@ __device__ __forceinline__ float group16_max(float m) {
     return m;
 }
 
-// fp32 scale of a block with maximum amax, and its codes by IEEE division (the layer's quantizer).
+// fp32 scale of a block with maximum amax, and its codes.  The scale is amax times the rounded 1/448,
+// as a torch program on the GPU computes amax / 448.0, so that its codes are these; the layer's own
+// quantizer divides, which can differ by one ulp of the scale.
 __device__ __forceinline__ uint2 quant_fp32(const float* v, float amax, float& s) {
-    s = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+    s = amax > 0.0f ? __fmul_rn(amax, 1.0f / 448.0f) : 1.0f;
     float q[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(v[i], s);
@@ -168,8 +170,7 @@ __global__ void __launch_bounds__(1024) k_add_rms_norm(NormArgs a) {
     }
 }
 
-// The codes and scales of bf16 rows: a thread per eight columns, the arithmetic of the layer's own
-// quantizer.  Clears the status word of the call (its first kernel).
+// The codes and scales of bf16 rows: a thread per eight columns.  Clears the status word of the call (its first kernel).
 __global__ void __launch_bounds__(256) k_quant_rows(QuantRowsArgs a) {
     pdl_wait_then_release();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = MOE_OK;

@@ -27,13 +27,13 @@ def dequantize(codes, words, recipe):
 
 
 def quantize(x, recipe):
-    """bf16 rows -> (codes uint8 [T, K], scale words int32 [K/128, scale_rows]), the layer quantizer's fp32 steps."""
+    """bf16 rows -> (codes uint8 [T, K], scale words int32 [K/128, scale_rows]), in the quantizer's fp32 steps."""
     T, K = x.shape
     g = 128 if recipe == 0 else 32
     b = x.float().reshape(T, K // g, g)
     amax = b.abs().amax(-1)
     if recipe == 0:
-        s = torch.where(amax > 0, amax / 448.0, torch.ones_like(amax))
+        s = torch.where(amax > 0, amax * torch.tensor(1.0 / 448.0), torch.ones_like(amax))
         words = s.t().contiguous().view(torch.int32)
     else:
         m, e = torch.frexp(amax)
