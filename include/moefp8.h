@@ -449,7 +449,8 @@ int moe_balance_loss(const moe_config_t *cfg, const float *router_logits, const 
  *   d_per_expert_scale  device fp32 [E] or NULL; out (needs per_expert_scale)
  *   workspace       as for moe_balance_loss with the same num_seqs; only used (and may be NULL
  *                   otherwise) when d_per_expert_scale is wanted
- * An id outside [0, E) adds nothing.  One launch, two with d_per_expert_scale. */
+ * An id outside [0, E) adds nothing; the others of a token are distinct, as moe_route's are.  One launch,
+ * two with d_per_expert_scale. */
 int moe_route_backward(const moe_config_t *cfg, const float *router_logits, const float *per_expert_scale,
                        const int32_t *topk_idx, const float *d_topk_weights, const float *d_loss, float coef,
                        const int32_t *expert_counts, const int32_t *seq_tokens, const uint8_t *token_mask,

@@ -8,9 +8,11 @@
 // f does not depend on the logits, so d loss / d p[t, e] = coef * dloss / S' * f[s, e] / n_s, the same
 // for every token of a sequence.
 //
-// Bound: one read of the logits (and one write of their gradient).  Sums are fp32 in registers, then
-// per block and chunk in a fixed order without atomics on floats, so a result is the same on every
-// run.
+// Bound: one read of the logits (and one write of their gradient).  A token is taken by G = 8 lanes
+// (16 above 128 experts) with up to 16 experts each, so that a warp works on four tokens (two) at
+// once and a sum over a row takes three shuffles (four) for all of them.  Sums are fp32 in
+// registers, then per block and chunk in a fixed order without atomics on floats, so a result is the
+// same on every run.
 #include <math.h>
 
 #include "block_kernels.h"
@@ -19,8 +21,6 @@
 namespace moe {
 
 namespace {
-
-constexpr int kWarps = 32;
 
 // Sequence s's first token (s <= S), kept inside [0, T].
 __device__ __forceinline__ int seq_at(const int32_t* off, int S, int T, int s) {
@@ -39,73 +39,147 @@ __device__ __forceinline__ int seq_after(const int32_t* off, int S, int T, int t
     return lo;
 }
 
-// A token's probabilities, NE experts a lane (expert lane + 32 i; past E: 0).
-template <int NE>
-__device__ __forceinline__ void probs(const float* row, int E, int routing, int lane, float (&p)[NE]) {
-    float z = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NE; ++i) p[i] = lane + 32 * i < E ? __ldg(row + lane + 32 * i) : -INFINITY;
-    if (routing == 0) {
-        float m = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < NE; ++i) m = fmaxf(m, p[i]);
-        m = warp_max(m);
-#pragma unroll
-        for (int i = 0; i < NE; ++i) z += (p[i] = expf(p[i] - m));
-    } else {
-#pragma unroll
-        for (int i = 0; i < NE; ++i) z += (p[i] = 1.0f / (1.0f + expf(-p[i])));
+// A row of E values over G lanes, NE a lane: four neighbours at a time (VEC: E a multiple of 4 and
+// 16-byte rows), or every G-th.
+template <int NE, int G, bool VEC>
+struct Row {
+    static __device__ __forceinline__ int expert(int i, int gl) {
+        return VEC ? (i >> 2) * (4 * G) + gl * 4 + (i & 3) : i * G + gl;
     }
-    z = 1.0f / warp_sum(z);
+    template <typename T4, typename T>
+    static __device__ __forceinline__ void load(const T* row, int E, int gl, bool ok, T (&v)[NE], T fill) {
+        if (VEC) {
 #pragma unroll
-    for (int i = 0; i < NE; ++i) p[i] *= z;
+            for (int i = 0; i < NE; i += 4) {
+                const int e = expert(i, gl);
+                if (ok && e < E) {
+                    const T4 x = __ldg(reinterpret_cast<const T4*>(row + e));
+                    v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
+                } else {
+                    v[i] = v[i + 1] = v[i + 2] = v[i + 3] = fill;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NE; ++i) v[i] = ok && expert(i, gl) < E ? __ldg(row + expert(i, gl)) : fill;
+        }
+    }
+    static __device__ __forceinline__ void store(float* row, int E, int gl, const float (&v)[NE]) {
+        if (VEC) {
+#pragma unroll
+            for (int i = 0; i < NE; i += 4)
+                if (expert(i, gl) < E)
+                    *reinterpret_cast<float4*>(row + expert(i, gl)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NE; ++i)
+                if (expert(i, gl) < E) row[expert(i, gl)] = v[i];
+        }
+    }
+};
+
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int o = 1; o < G; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
 }
+template <int G>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+    for (int o = 1; o < G; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// sigmoid(l) and sigmoid(l) (1 - sigmoid(l)) from t = e^-|l| in (0, 1]: neither overflows, and the
+// second does not lose its digits where the first is near 1.
+__device__ __forceinline__ float sigmoid(float l, float& slope) {
+    const float t = expf(-fabsf(l)), r = __frcp_rn(1.0f + t);
+    slope = t * r * r;
+    return l >= 0.0f ? r : t * r;                      // NaN: t is NaN
+}
+
+// v[i] = p for the row's experts (0 past E); returns nothing else.  Every lane of the warp calls it.
+template <int NE, int G, bool SIG>
+__device__ __forceinline__ void row_probs(float (&v)[NE]) {
+    float z = 0.0f;
+    if (SIG) {
+        float slope;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) z += (v[i] = sigmoid(v[i], slope));   // -inf past E: 0
+    } else {
+        float m = v[0];
+#pragma unroll
+        for (int i = 1; i < NE; ++i) m = fmaxf(m, v[i]);
+        m = group_max<G>(m);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) z += (v[i] = expf(v[i] - m));
+    }
+    z = 1.0f / group_sum<G>(z);
+#pragma unroll
+    for (int i = 0; i < NE; ++i) v[i] *= z;
+}
+
+constexpr int kBWarps = 32;                            // k_balance
+constexpr int kRWarps = 8;                             // k_route_backward
 
 }  // namespace
 
-// Block c takes the tokens of chunk c, sequence by sequence: a warp a token, the sums of p in
-// registers, then over the warps in order.
-template <int NE>
-__global__ void __launch_bounds__(kWarps * 32) k_balance(BalanceArgs a) {
-    __shared__ float s_p[kWarps][32 * NE];
-    __shared__ int s_n[32 * NE + 2];                   // counts, counted tokens, ids out of range
+// Block c takes the tokens of chunk c, sequence by sequence; the sums of p stay in registers and are
+// joined over the lanes and warps in order at a sequence's end.
+template <int NE, int G, bool VEC, bool SIG>
+__global__ void __launch_bounds__(kBWarps * 32) k_balance(BalanceArgs a) {
+    using R = Row<NE, G, VEC>;
+    constexpr int TPW = 32 / G, W = NE * G;
+    __shared__ float s_p[kBWarps][W];
+    __shared__ int s_n[W + 2];                         // counts, counted tokens, ids out of range
     pdl_wait_then_release();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gl = lane % G;
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         *a.status = MOE_OK;
         *a.ticket = 0;
     }
     const int c0 = blockIdx.x * a.chunk, c1 = min(a.T, c0 + a.chunk);
     for (int s = seq_after(a.off, a.S, a.T, c0); s < a.S; ++s) {
-        const int b0 = max(c0, seq_at(a.off, a.S, a.T, s)), b1 = min(c1, seq_at(a.off, a.S, a.T, s + 1));
-        if (seq_at(a.off, a.S, a.T, s) >= c1) break;
+        const int s0 = seq_at(a.off, a.S, a.T, s);
+        if (s0 >= c1) break;
+        const int b0 = max(c0, s0), b1 = min(c1, seq_at(a.off, a.S, a.T, s + 1));
         if (b0 >= b1) continue;
+        const int warps = min(kBWarps, (b1 - b0 + TPW - 1) / TPW);   // warps with a token
         for (int e = threadIdx.x; e < a.E + 2; e += blockDim.x) s_n[e] = 0;
         __syncthreads();
-        float acc[NE];
+        if (warp < warps) {
+            float acc[NE];
 #pragma unroll
-        for (int i = 0; i < NE; ++i) acc[i] = 0.0f;
-        int counted = 0;
-        for (int t = b0 + warp; t < b1; t += kWarps) {
-            if (a.mask && !__ldg(a.mask + t)) continue;
-            ++counted;
-            float p[NE];
-            probs<NE>(a.logits + static_cast<size_t>(t) * a.E, a.E, a.routing, lane, p);
+            for (int i = 0; i < NE; ++i) acc[i] = 0.0f;
+            for (int tb = b0 + warp * TPW; tb < b1; tb += kBWarps * TPW) {
+                const int t = tb + lane / G;
+                const bool ok = t < b1 && !(a.mask && !__ldg(a.mask + t));
+                float p[NE];
+                R::template load<float4>(a.logits + static_cast<size_t>(ok ? t : 0) * a.E, a.E, gl, ok, p, -INFINITY);
+                if (ok) {
+                    for (int j = gl; j < a.K; j += G) {
+                        const int e = __ldg(a.idx + static_cast<size_t>(t) * a.K + j);
+                        atomicAdd(&s_n[e >= 0 && e < a.E ? e : a.E + 1], 1);
+                    }
+                    if (gl == 0) atomicAdd(&s_n[a.E], 1);
+                }
+                row_probs<NE, G, SIG>(p);
 #pragma unroll
-            for (int i = 0; i < NE; ++i) acc[i] += p[i];
-            for (int j = lane; j < a.K; j += 32) {
-                const int e = __ldg(a.idx + static_cast<size_t>(t) * a.K + j);
-                atomicAdd(&s_n[e >= 0 && e < a.E ? e : a.E + 1], 1);
+                for (int i = 0; i < NE; ++i) acc[i] += ok ? p[i] : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < NE; ++i) {
+#pragma unroll
+                for (int o = G; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+                if (lane < G) s_p[warp][R::expert(i, gl)] = acc[i];
             }
         }
-        if (lane == 0 && counted) atomicAdd(&s_n[a.E], counted);
-#pragma unroll
-        for (int i = 0; i < NE; ++i) s_p[warp][lane + 32 * i] = acc[i];
         __syncthreads();
         const size_t slot = static_cast<size_t>(blockIdx.x) + s;
         for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
             float v = 0.0f;
-            for (int w = 0; w < kWarps; ++w) v += s_p[w][e];
+            for (int w = 0; w < warps; ++w) v += s_p[w][e];
             a.part_p[slot * a.E + e] = v;
         }
         for (int e = threadIdx.x; e < a.E + 2; e += blockDim.x) a.part_n[slot * (a.E + 2) + e] = s_n[e];
@@ -113,88 +187,76 @@ __global__ void __launch_bounds__(kWarps * 32) k_balance(BalanceArgs a) {
     }
 }
 
-// Block s joins sequence s's chunks in order; the last block to finish adds the sequences' losses.
+// Block (s, b) joins sequence s's chunks for experts 32 b .. 32 b + 31: a lane an expert, a warp every
+// 32nd chunk, then the warps in order.  The last block to finish adds the losses.
 __global__ void __launch_bounds__(1024) k_balance_join(BalanceArgs a) {
-    __shared__ float s_p[1024];
-    __shared__ int s_n[1024], s_tok, s_bad, s_last;
+    __shared__ float s_p[32][33];
+    __shared__ int s_n[32][33], s_tok[32], s_bad, s_last;
     __shared__ float s_red[32];
     pdl_wait_then_release();
     const int s = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int E2 = (a.E + 31) & ~31, groups = 1024 / E2;
-    const int g = threadIdx.x / E2, e = threadIdx.x % E2;
+    const int e = blockIdx.y * 32 + lane;
     const int b0 = seq_at(a.off, a.S, a.T, s), b1 = seq_at(a.off, a.S, a.T, s + 1);
-    if (threadIdx.x == 0) {
-        s_tok = 0, s_bad = 0;
-        if (a.off) {
-            const int o0 = a.off[s], o1 = a.off[s + 1];
-            if (o0 < 0 || o1 > a.T || o0 > o1) s_bad = 1;
-        }
-    }
+    if (threadIdx.x == 0) s_bad = a.off && (a.off[s] < 0 || a.off[s + 1] > a.T || a.off[s] > a.off[s + 1]);
     __syncthreads();
     const int lo = b0 / a.chunk, hi = b0 < b1 ? (b1 - 1) / a.chunk : lo - 1;
     float v = 0.0f;
-    int n = 0;
-    if (g < groups && e < a.E)
-        for (int c = lo + g; c <= hi; c += groups) {
-            const size_t slot = static_cast<size_t>(c) + s;
+    int n = 0, tok = 0, bad = 0;
+#pragma unroll 4
+    for (int c = lo + warp; c <= hi; c += 32) {
+        const size_t slot = static_cast<size_t>(c) + s;
+        const int32_t* cnt = a.part_n + slot * (a.E + 2);
+        if (e < a.E) {
             v += __ldcg(a.part_p + slot * a.E + e);
-            n += __ldcg(a.part_n + slot * (a.E + 2) + e);
+            n += __ldcg(cnt + e);
         }
-    s_p[threadIdx.x] = v;
-    s_n[threadIdx.x] = n;
+        tok += __ldcg(cnt + a.E);                      // one address for the warp
+        bad |= __ldcg(cnt + a.E + 1);
+    }
+    s_p[warp][lane] = v;
+    s_n[warp][lane] = n;
+    if (lane == 0) {
+        s_tok[warp] = tok;
+        if (bad) s_bad = 1;
+    }
+    __syncthreads();
     if (warp == 0) {
-        int tok = 0, bad = 0;
-        for (int c = lo + lane; c <= hi; c += 32) {
-            const int32_t* q = a.part_n + (static_cast<size_t>(c) + s) * (a.E + 2) + a.E;
-            tok += __ldcg(q);
-            bad |= __ldcg(q + 1);
+        tok = __reduce_add_sync(0xffffffffu, s_tok[lane]);
+        v = 0.0f;
+        n = 0;
+        for (int w = 0; w < 32; ++w) {
+            v += s_p[w][lane];
+            n += s_n[w][lane];
         }
-        tok = __reduce_add_sync(0xffffffffu, tok);
-        bad = __reduce_or_sync(0xffffffffu, bad);
+        float term = 0.0f;
+        if (e < a.E) {
+            const float mean = tok ? v / static_cast<float>(tok) : 0.0f;
+            a.mean[static_cast<size_t>(s) * a.E + e] = mean;
+            a.counts[static_cast<size_t>(s) * a.E + e] = n;
+            if (tok)
+                term = static_cast<float>(n) * (static_cast<float>(a.E) / (static_cast<float>(a.K) * static_cast<float>(tok))) * mean;
+        }
+        term = warp_sum(term);
         if (lane == 0) {
-            s_tok = tok;
-            s_bad |= bad;
+            a.seq_loss[static_cast<size_t>(s) * gridDim.y + blockIdx.y] = term;
+            if (blockIdx.y == 0) a.tokens[s] = tok;
+            if (s_bad) set_status(a.status, MOE_ERR_BOUNDS);
+            __threadfence();
+            s_last = atomicAdd(a.ticket, 1) == static_cast<int>(gridDim.x * gridDim.y) - 1;
         }
-    }
-    __syncthreads();
-    const int tok = s_tok;
-    float term = 0.0f;
-    if (g == 0 && e < a.E) {
-        for (int q = 1; q < groups; ++q) {
-            v += s_p[q * E2 + e];
-            n += s_n[q * E2 + e];
-        }
-        const float mean = tok ? v / static_cast<float>(tok) : 0.0f;
-        a.mean[static_cast<size_t>(s) * a.E + e] = mean;
-        a.counts[static_cast<size_t>(s) * a.E + e] = n;
-        if (tok) term = static_cast<float>(n) * (static_cast<float>(a.E) / (static_cast<float>(a.K) * tok)) * mean;
-    }
-    term = warp_sum(term);
-    if (lane == 0) s_red[warp] = term;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        float l = 0.0f;
-        for (int w = 0; w < 32; ++w) l += s_red[w];
-        a.seq_loss[s] = l;
-        a.tokens[s] = tok;
-        if (s_bad) set_status(a.status, MOE_ERR_BOUNDS);
-        __threadfence();
-        s_last = atomicAdd(a.ticket, 1) == a.S - 1;
     }
     __syncthreads();
     if (!s_last) return;
     __threadfence();
     float l = 0.0f;
     int full = 0;
-    for (int i = threadIdx.x; i < a.S; i += 1024) {
-        l += __ldcg(a.seq_loss + i);
-        full += __ldcg(a.tokens + i) > 0;
-    }
+    for (int i = threadIdx.x; i < a.S * static_cast<int>(gridDim.y); i += 1024) l += __ldcg(a.seq_loss + i);
+    for (int i = threadIdx.x; i < a.S; i += 1024) full += __ldcg(a.tokens + i) > 0;
     l = warp_sum(l);
     full = __reduce_add_sync(0xffffffffu, full);
     if (lane == 0) {
         s_red[warp] = l;
-        s_n[warp] = full;
+        s_tok[warp] = full;
     }
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -202,7 +264,7 @@ __global__ void __launch_bounds__(1024) k_balance_join(BalanceArgs a) {
         full = 0;
         for (int w = 0; w < 32; ++w) {
             l += s_red[w];
-            full += s_n[w];
+            full += s_tok[w];
         }
         a.tokens[a.S] = full;
         a.loss[0] = full ? a.coef * (l / static_cast<float>(full)) : 0.0f;
@@ -210,205 +272,251 @@ __global__ void __launch_bounds__(1024) k_balance_join(BalanceArgs a) {
 }
 
 // ------------------------------------------------------------------------------------------
-// A warp a token.  With s = the probabilities' sum Z, u_j the routing weight before its scales and
-// du_j = dw_j * rsf * per_expert_scale[e_j]:
-//   softmax:              dl = p (dp - sum p dp)   with dp[e_j] += du_j
+// With Z the sum of the scores, u_j the routing weight before its scales, x_j = rsf * dw_j and
+// du_j = x_j * per_expert_scale[e_j]:
+//   softmax:               dl = p (dp - sum p dp)   with dp[e_j] += du_j
 //   softmax, renormalized: dl = p (dp - sum p dp),  dl[e_j] += u_j (du_j - sum u du)
-//   sigmoid s:            dl = s (1 - s) ds,  ds = (dp - sum p dp) / Z,  ds[e_j] += (du_j - sum u du) / sum s[e_j]
-template <int NE>
-__global__ void __launch_bounds__(kWarps * 32) k_route_backward(RouteBackwardArgs a) {
-    extern __shared__ float s_mem[];                   // [kWarps][E] additions, then [kWarps][E] sums of dpes
+//   sigmoid s:             dl = s (1 - s) ds,  ds = (dp - sum p dp) / Z,  ds[e_j] += (du_j - sum u du) / sum_j s[e_j]
+//   dscale[e] = sum over the tokens of x_j u_j
+// The slots' terms reach the lanes that hold their experts through a row of shared memory.
+template <int NE, int G, bool VEC, bool SIG>
+__global__ void __launch_bounds__(kRWarps * 32) k_route_backward(RouteBackwardArgs a) {
+    using R = Row<NE, G, VEC>;
+    constexpr int TPW = 32 / G, W = NE * G;
+    __shared__ __align__(16) float s_add[kRWarps * TPW][W];
+    __shared__ float s_scale[kRWarps][W];
     pdl_wait_then_release();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float* add = s_mem + warp * a.E;
-    float* dpes = s_mem + (kWarps + warp) * a.E;
-    for (int e = lane; e < a.E; e += 32) {
-        add[e] = 0.0f;
-        if (a.dpes) dpes[e] = 0.0f;
-    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gl = lane % G, grp = lane / G;
+    float* add = s_add[warp * TPW + grp];
+    float* dscale = s_scale[warp];
+    for (int e = gl; e < W; e += G) add[e] = 0.0f;
+    for (int e = lane; e < W; e += 32) dscale[e] = 0.0f;
     __syncwarp();
     const int c0 = blockIdx.x * a.chunk, c1 = min(a.T, c0 + a.chunk);
-    const float gl = a.dloss ? __ldg(a.dloss) * a.coef : 0.0f;
-    int s = -1, s_lo = 0, s_hi = 0;                    // the sequence whose gradient is in g
-    float g[NE];
-#pragma unroll
-    for (int i = 0; i < NE; ++i) g[i] = 0.0f;
-    for (int t = c0 + warp; t < c1; t += kWarps) {
-        bool bal = a.dloss && !(a.mask && !__ldg(a.mask + t));
-        if (bal && !(s >= 0 && t >= s_lo && t < s_hi)) {
-            const int q = seq_after(a.off, a.S, a.T, t);
-            if (q < a.S && seq_at(a.off, a.S, a.T, q) <= t) {
-                s = q;
-                s_lo = seq_at(a.off, a.S, a.T, q);
-                s_hi = seq_at(a.off, a.S, a.T, q + 1);
+    const float gloss = a.dloss ? __ldg(a.dloss) * a.coef : 0.0f;
+    const bool norm = SIG || a.renorm;
+    const bool direct = !norm;                         // the weights' gradient goes through the softmax
+    for (int tb = c0 + warp * TPW; tb < c1; tb += kRWarps * TPW) {
+        const int t = tb + grp;
+        const bool in = t < c1;
+        const size_t tr = static_cast<size_t>(in ? t : c0);
+        const int32_t* idx = a.idx + tr * a.K;
+        const float* dw = a.dw + tr * a.K;
+        const float* row = a.logits + tr * a.E;
+        // Every load first: the row and the lane's own slot (all there is when k <= G) do not wait for
+        // what decides whether they are used.
+        float p[NE], slope[NE], d[NE];
+        R::template load<float4>(row, a.E, gl, in, p, -INFINITY);
+        int e0 = in && gl < a.K ? __ldg(idx + gl) : -1;
+        float x0 = in && a.dw && gl < a.K ? __ldg(dw + gl) : 0.0f;
+        bool bal = in && a.dloss && !(a.mask && !__ldg(a.mask + t));
+        int q = 0;
+        float f = 0.0f;
+        if (bal) {
+            q = a.S > 1 || a.off ? seq_after(a.off, a.S, a.T, t) : 0;
+            bal = q < a.S && seq_at(a.off, a.S, a.T, q) <= t;
+            if (bal) {
                 const float n = static_cast<float>(__ldg(a.tokens + q)), full = static_cast<float>(__ldg(a.tokens + a.S));
-                const float f = n > 0.0f ? gl / full * static_cast<float>(a.E) / (static_cast<float>(a.K) * n * n) : 0.0f;
-#pragma unroll
-                for (int i = 0; i < NE; ++i)
-                    g[i] = lane + 32 * i < a.E
-                               ? f * static_cast<float>(__ldg(a.counts + static_cast<size_t>(q) * a.E + lane + 32 * i))
-                               : 0.0f;
-            } else {
-                bal = false;
+                f = n > 0.0f ? gloss / full * static_cast<float>(a.E) / (static_cast<float>(a.K) * n * n) : 0.0f;
             }
         }
-        const float* row = a.logits + static_cast<size_t>(t) * a.E;
-        const int32_t* idx = a.idx + static_cast<size_t>(t) * a.K;
-        const float* dw = a.dw ? a.dw + static_cast<size_t>(t) * a.K : nullptr;
-        // ---- the routing weights (a row without any gradient stays out: its logits may be anything)
-        bool wts = false;
-        if (dw) {
-            bool nz = false;
-            for (int j = lane; j < a.K; j += 32) nz |= __ldg(dw + j) != 0.0f;
-            wts = __any_sync(0xffffffffu, nz);
-        }
-        float m = -INFINITY, z = 1.0f;                 // softmax of the whole row
-        if (a.routing == 0 && (bal || (wts && !a.renorm))) {
+        {
+            int n[NE];
+            R::template load<int4>(a.counts + static_cast<size_t>(q) * a.E, a.E, gl, bal, n, 0);
 #pragma unroll
-            for (int i = 0; i < NE; ++i)
-                if (lane + 32 * i < a.E) m = fmaxf(m, __ldg(row + lane + 32 * i));
-            m = warp_max(m);
-            z = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NE; ++i)
-                if (lane + 32 * i < a.E) z += expf(__ldg(row + lane + 32 * i) - m);
-            z = warp_sum(z);
+            for (int i = 0; i < NE; ++i) d[i] = f * static_cast<float>(n[i]);
         }
-        const bool norm = a.routing == 1 || a.renorm;
-        if (wts) {
-            float sm = -INFINITY, sz = 0.0f, sd = 0.0f;
-            if (a.routing == 0 && norm) {
-                for (int j = lane; j < a.K; j += 32) {
+        if (e0 >= a.E) e0 = -1;
+        const float l0 = e0 >= 0 ? __ldg(row + e0) : -INFINITY;
+        const float c0s = e0 >= 0 && a.pes ? __ldg(a.pes + e0) : 1.0f;
+        float nz = x0 != 0.0f ? 1.0f : 0.0f;               // NaN counts
+        if (in && a.dw)
+            for (int j = gl + G; j < a.K; j += G) nz = __ldg(dw + j) != 0.0f ? 1.0f : nz;
+        const bool wts = group_max<G>(nz) != 0.0f;
+        float z = 0.0f, m = -INFINITY;
+        if (SIG) {
+#pragma unroll
+            for (int i = 0; i < NE; ++i) z += (p[i] = sigmoid(p[i], slope[i]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < NE; ++i) m = fmaxf(m, p[i]);
+            m = group_max<G>(m);
+#pragma unroll
+            for (int i = 0; i < NE; ++i) z += (p[i] = expf(p[i] - m));
+        }
+        const float rz = 1.0f / group_sum<G>(z);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) p[i] *= rz;
+
+        // ---- the routing weights' terms (a token without them adds zeros)
+        float sm = m, sz = 0.0f, sd = 0.0f;
+        const bool more = wts && a.K > G;                  // slots behind the lanes' first
+        if (!SIG && norm) {
+            float v = l0;
+            if (more)
+                for (int j = gl + G; j < a.K; j += G) {
                     const int e = __ldg(idx + j);
-                    if (e >= 0 && e < a.E) sm = fmaxf(sm, __ldg(row + e));
+                    if (e >= 0 && e < a.E) v = fmaxf(v, __ldg(row + e));
                 }
-                sm = warp_max(sm);
-            }
-            auto raw = [&](int e) {                    // the weight before the normalization
-                const float l = __ldg(row + e);
-                return a.routing == 1 ? 1.0f / (1.0f + expf(-l)) : norm ? expf(l - sm) : expf(l - m) / z;
-            };
-            if (norm) {
-                for (int j = lane; j < a.K; j += 32) {
-                    const int e = __ldg(idx + j);
-                    if (e < 0 || e >= a.E) continue;
-                    const float v = raw(e);
-                    sz += v;
-                    sd += v * (__ldg(dw + j) * a.rsf * (a.pes ? __ldg(a.pes + e) : 1.0f));
-                }
-                sz = warp_sum(sz);
-                sd = warp_sum(sd) / sz;
-            } else {
-                sz = 1.0f;
-            }
-            for (int j = lane; j < a.K; j += 32) {
+            sm = group_max<G>(v);
+        }
+        auto raw = [&](float l) {                          // the weight before the normalization
+            float s;
+            return SIG ? sigmoid(l, s) : norm ? expf(l - sm) : expf(l - m) * rz;
+        };
+        x0 *= a.rsf;
+        const float u0 = e0 >= 0 ? raw(l0) : 0.0f, du0 = x0 * c0s;
+        sz = u0;
+        sd = u0 * du0;
+        if (more)
+            for (int j = gl + G; j < a.K; j += G) {
                 const int e = __ldg(idx + j);
                 if (e < 0 || e >= a.E) continue;
-                const float d = __ldg(dw + j) * a.rsf, du = d * (a.pes ? __ldg(a.pes + e) : 1.0f);
-                const float u = raw(e) / sz;
-                atomicAdd(&add[e], !norm ? du : a.routing == 1 ? (du - sd) / sz : u * (du - sd));
-                if (a.dpes) atomicAdd(&dpes[e], d * u);
+                const float v = raw(__ldg(row + e));
+                sz += v;
+                sd += v * (__ldg(dw + j) * a.rsf * (a.pes ? __ldg(a.pes + e) : 1.0f));
             }
-            __syncwarp();
+        if (norm) {
+            sz = 1.0f / group_sum<G>(sz);
+            sd = group_sum<G>(sd) * sz;
+        } else {
+            sz = 1.0f;
         }
-        // ---- the row's gradient
-        float* out = a.dl + static_cast<size_t>(t) * a.E;
-        if (!bal && !wts) {
+        // ids of a token are distinct: plain stores
+        if (wts && e0 >= 0) add[e0] = direct ? du0 : SIG ? (du0 - sd) * sz : u0 * sz * (du0 - sd);
+        if (more)
+            for (int j = gl + G; j < a.K; j += G) {
+                const int e = __ldg(idx + j);
+                if (e < 0 || e >= a.E) continue;
+                const float u = raw(__ldg(row + e)) * sz;
+                const float du = __ldg(dw + j) * a.rsf * (a.pes ? __ldg(a.pes + e) : 1.0f);
+                add[e] = direct ? du : SIG ? (du - sd) * sz : u * (du - sd);
+            }
+        __syncwarp();
+
+        // ---- the row
+        float x[NE], dot = 0.0f;
 #pragma unroll
-            for (int i = 0; i < NE; ++i)
-                if (lane + 32 * i < a.E) out[lane + 32 * i] = 0.0f;
-            continue;
+        for (int i = 0; i < NE; ++i) x[i] = 0.0f;
+        if (VEC) {
+#pragma unroll
+            for (int i = 0; i < NE; i += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(add + R::expert(i, gl));
+                x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NE; ++i) x[i] = add[R::expert(i, gl)];
         }
-        const bool direct = a.routing == 0 && !norm;   // the weights' gradient goes through the softmax
-        float p[NE], d[NE], zs = 0.0f, dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
-            const int e = lane + 32 * i;
-            p[i] = 0.0f, d[i] = 0.0f;
-            if (e >= a.E) continue;
-            const float l = __ldg(row + e);
-            p[i] = a.routing == 1 ? 1.0f / (1.0f + expf(-l)) : (bal || direct) ? expf(l - m) / z : 0.0f;
-            d[i] = (bal ? g[i] : 0.0f) + (direct && wts ? add[e] : 0.0f);
-            zs += p[i];
+            if (direct) d[i] += x[i], x[i] = 0.0f;
             dot = fmaf(p[i], d[i], dot);
         }
-        dot = warp_sum(dot);
-        if (a.routing == 1) {
-            zs = warp_sum(zs);
-            dot /= zs;
-        }
+        dot = group_sum<G>(dot);
+        // a token with one kind of gradient takes no part of the other (its row may hold NaN only there)
+        const bool through = bal || (direct && wts);
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
-            const int e = lane + 32 * i;
-            if (e >= a.E) continue;
-            const float x = wts && !direct ? add[e] : 0.0f;
-            float v;
-            if (a.routing == 1) {
-                const float l = __ldg(row + e);
-                v = p[i] * (1.0f / (1.0f + expf(l))) * ((bal ? (d[i] - dot) / zs : 0.0f) + x);
-            } else {
-                v = fmaf(p[i], d[i] - dot, x);
-            }
-            out[e] = v;
+            if (SIG) p[i] = slope[i] * ((through ? (d[i] - dot) * rz : 0.0f) + x[i]);
+            else p[i] = through ? fmaf(p[i], d[i] - dot, x[i]) : x[i];
+            if (!bal && !wts) p[i] = 0.0f;
         }
+        if (in) R::store(a.dl + tr * a.E, a.E, gl, p);
         __syncwarp();
-        if (wts) {                                     // back to zero for the next token
-            for (int j = lane; j < a.K; j += 32) {
+        // ---- back to zero; the scale's gradient, the warp's tokens one after the other
+        if (wts && e0 >= 0) add[e0] = 0.0f;
+        if (more)
+            for (int j = gl + G; j < a.K; j += G) {
                 const int e = __ldg(idx + j);
                 if (e >= 0 && e < a.E) add[e] = 0.0f;
             }
-            __syncwarp();
+        if (a.dpes) {
+            for (int g = 0; g < TPW; ++g) {
+                if (g == grp && wts) {
+                    if (e0 >= 0) dscale[e0] += x0 * (u0 * sz);
+                    if (more)
+                        for (int j = gl + G; j < a.K; j += G) {
+                            const int e = __ldg(idx + j);
+                            if (e >= 0 && e < a.E) dscale[e] += __ldg(dw + j) * a.rsf * (raw(__ldg(row + e)) * sz);
+                        }
+                }
+                __syncwarp();
+            }
         }
+        __syncwarp();
     }
     if (!a.dpes) return;
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
         float v = 0.0f;
-        for (int w = 0; w < kWarps; ++w) v += s_mem[(kWarps + w) * a.E + e];
+        for (int w = 0; w < kRWarps; ++w) v += s_scale[w][e];
         a.part[static_cast<size_t>(blockIdx.x) * a.E + e] = v;
     }
 }
 
-__global__ void __launch_bounds__(256) k_join_scale_grad(RouteBackwardArgs a) {
+// A block joins 32 experts: a lane an expert, a warp every 32nd chunk, then the warps in order.
+__global__ void __launch_bounds__(1024) k_join_scale_grad(RouteBackwardArgs a) {
+    __shared__ float s_p[32][33];
     pdl_wait_then_release();
-    const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (e >= a.E) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.x * 32 + lane;
     float v = 0.0f;
-    for (int c = lane; c < a.chunks; c += 32) v += __ldcg(a.part + static_cast<size_t>(c) * a.E + e);
-    v = warp_sum(v);
-    if (lane == 0) a.dpes[e] = v;
+    if (e < a.E) {
+#pragma unroll 4
+        for (int c = warp; c < a.chunks; c += 32) v += __ldcg(a.part + static_cast<size_t>(c) * a.E + e);
+    }
+    s_p[warp][lane] = v;
+    __syncthreads();
+    if (warp || e >= a.E) return;
+    v = 0.0f;
+    for (int w = 0; w < 32; ++w) v += s_p[w][lane];
+    a.dpes[e] = v;
 }
 
-template <int NE>
-static cudaError_t launch_backward_t(const RouteBackwardArgs& a, cudaStream_t s) {
-    const size_t smem = static_cast<size_t>(kWarps) * a.E * 4 * (a.dpes ? 2 : 1);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(k_route_backward<NE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-    }
-    return launch_pdl(k_route_backward<NE>, dim3(a.chunks), dim3(kWarps * 32), smem, s, a);
+namespace {
+
+template <int NE, int G>
+cudaError_t balance_t(const BalanceArgs& a, bool vec, cudaStream_t s) {
+    const dim3 grid(a.chunks), block(kBWarps * 32);
+    if (a.routing)
+        return vec ? launch_pdl(k_balance<NE, G, true, true>, grid, block, 0, s, a)
+                   : launch_pdl(k_balance<NE, G, false, true>, grid, block, 0, s, a);
+    return vec ? launch_pdl(k_balance<NE, G, true, false>, grid, block, 0, s, a)
+               : launch_pdl(k_balance<NE, G, false, false>, grid, block, 0, s, a);
 }
+
+template <int NE, int G>
+cudaError_t backward_t(const RouteBackwardArgs& a, bool vec, cudaStream_t s) {
+    const dim3 grid(a.chunks), block(kRWarps * 32);
+    if (a.routing)
+        return vec ? launch_pdl(k_route_backward<NE, G, true, true>, grid, block, 0, s, a)
+                   : launch_pdl(k_route_backward<NE, G, false, true>, grid, block, 0, s, a);
+    return vec ? launch_pdl(k_route_backward<NE, G, true, false>, grid, block, 0, s, a)
+               : launch_pdl(k_route_backward<NE, G, false, false>, grid, block, 0, s, a);
+}
+
+bool rows16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+}  // namespace
 
 cudaError_t launch_balance(const BalanceArgs& a, cudaStream_t s) {
-    const int ne = (a.E + 31) / 32;
-    const dim3 grid(a.chunks), block(kWarps * 32);
-    const cudaError_t e = ne <= 1   ? launch_pdl(k_balance<1>, grid, block, 0, s, a)
-                          : ne <= 2 ? launch_pdl(k_balance<2>, grid, block, 0, s, a)
-                          : ne <= 4 ? launch_pdl(k_balance<4>, grid, block, 0, s, a)
-                                    : launch_pdl(k_balance<8>, grid, block, 0, s, a);
+    const bool vec = a.E % 4 == 0 && rows16(a.logits);
+    const cudaError_t e = a.E <= 32    ? balance_t<4, 8>(a, vec, s)
+                          : a.E <= 64  ? balance_t<8, 8>(a, vec, s)
+                          : a.E <= 128 ? balance_t<16, 8>(a, vec, s)
+                                       : balance_t<16, 16>(a, vec, s);
     if (e != cudaSuccess) return e;
-    return launch_pdl(k_balance_join, dim3(a.S), dim3(1024), 0, s, a);
+    return launch_pdl(k_balance_join, dim3(a.S, (a.E + 31) / 32), dim3(1024), 0, s, a);
 }
 
 cudaError_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t s) {
-    const int ne = (a.E + 31) / 32;
-    const cudaError_t e = ne <= 1   ? launch_backward_t<1>(a, s)
-                          : ne <= 2 ? launch_backward_t<2>(a, s)
-                          : ne <= 4 ? launch_backward_t<4>(a, s)
-                                    : launch_backward_t<8>(a, s);
+    const bool vec = a.E % 4 == 0 && rows16(a.logits) && rows16(a.dl) && rows16(a.counts);
+    const cudaError_t e = a.E <= 32    ? backward_t<4, 8>(a, vec, s)
+                          : a.E <= 64  ? backward_t<8, 8>(a, vec, s)
+                          : a.E <= 128 ? backward_t<16, 8>(a, vec, s)
+                                       : backward_t<16, 16>(a, vec, s);
     if (e != cudaSuccess || !a.dpes) return e;
-    return launch_pdl(k_join_scale_grad, dim3((a.E + 7) / 8), dim3(256), 0, s, a);
+    return launch_pdl(k_join_scale_grad, dim3((a.E + 31) / 32), dim3(1024), 0, s, a);
 }
 
 }  // namespace moe

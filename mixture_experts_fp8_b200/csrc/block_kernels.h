@@ -77,6 +77,13 @@ inline int balance_chunk(int T) {
     return c < 32 ? 32 : c;
 }
 inline int balance_chunks(int T) { return (T + balance_chunk(T) - 1) / balance_chunk(T); }
+// The gradients' chunks: a block of 8 warps each, several blocks on an SM.
+constexpr int kBackwardChunks = 592;
+inline int backward_chunk(int T) {
+    const int c = (T + kBackwardChunks - 1) / kBackwardChunks;
+    return c < 16 ? 16 : c;
+}
+inline int backward_chunks(int T) { return (T + backward_chunk(T) - 1) / backward_chunk(T); }
 
 struct BalanceArgs {
     const float* logits;        // [T, E]
@@ -85,7 +92,7 @@ struct BalanceArgs {
     const int32_t* off;         // [S + 1] or null (one sequence of all tokens)
     float* part_p;              // [chunks + S][E]
     int32_t* part_n;            // [chunks + S][E + 2] counts, counted tokens, ids out of range
-    float* seq_loss;            // [S]
+    float* seq_loss;            // [S][ceil(E / 32)]
     int32_t* ticket;
     int32_t* counts;            // [S, E]
     int32_t* tokens;            // [S + 1]
