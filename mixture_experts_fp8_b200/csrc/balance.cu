@@ -91,15 +91,23 @@ __device__ __forceinline__ float group_max(float v) {
     return v;
 }
 
+// e^x for x <= 0 as 2^(x log2 e): the product's rounding makes its relative error up to |x| 2^-24, under
+// 2e-6 wherever e^x is above 1e-12, in two instructions against expf's eight.
+__device__ __forceinline__ float exp_neg(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));
+    return y;
+}
+
 // sigmoid(l) and sigmoid(l) (1 - sigmoid(l)) from t = e^-|l| in (0, 1]: neither overflows, and the
 // second does not lose its digits where the first is near 1.
 __device__ __forceinline__ float sigmoid(float l, float& slope) {
-    const float t = expf(-fabsf(l)), r = __frcp_rn(1.0f + t);
+    const float t = exp_neg(-fabsf(l)), r = __frcp_rn(1.0f + t);
     slope = t * r * r;
     return l >= 0.0f ? r : t * r;                      // NaN: t is NaN
 }
 
-// v[i] = p for the row's experts (0 past E); returns nothing else.  Every lane of the warp calls it.
+// v[i]: the logits (-inf past E) in, the probabilities out.  Every lane of the warp calls it.
 template <int NE, int G, bool SIG>
 __device__ __forceinline__ void row_probs(float (&v)[NE]) {
     float z = 0.0f;
@@ -113,7 +121,7 @@ __device__ __forceinline__ void row_probs(float (&v)[NE]) {
         for (int i = 1; i < NE; ++i) m = fmaxf(m, v[i]);
         m = group_max<G>(m);
 #pragma unroll
-        for (int i = 0; i < NE; ++i) z += (v[i] = expf(v[i] - m));
+        for (int i = 0; i < NE; ++i) z += (v[i] = exp_neg(v[i] - m));
     }
     z = 1.0f / group_sum<G>(z);
 #pragma unroll
@@ -279,7 +287,9 @@ __global__ void __launch_bounds__(1024) k_balance_join(BalanceArgs a) {
 //   sigmoid s:             dl = s (1 - s) ds,  ds = (dp - sum p dp) / Z,  ds[e_j] += (du_j - sum u du) / sum_j s[e_j]
 //   dscale[e] = sum over the tokens of x_j u_j
 // The slots' terms reach the lanes that hold their experts through a row of shared memory.
-template <int NE, int G, bool VEC, bool SIG>
+enum { kDirect = 0, kRenorm = 1, kSigmoid = 2 };      // softmax, softmax renormalized, sigmoid
+
+template <int NE, int G, bool VEC, int MODE>
 __global__ void __launch_bounds__(kRWarps * 32) k_route_backward(RouteBackwardArgs a) {
     using R = Row<NE, G, VEC>;
     constexpr int TPW = 32 / G, W = NE * G;
@@ -294,8 +304,10 @@ __global__ void __launch_bounds__(kRWarps * 32) k_route_backward(RouteBackwardAr
     __syncwarp();
     const int c0 = blockIdx.x * a.chunk, c1 = min(a.T, c0 + a.chunk);
     const float gloss = a.dloss ? __ldg(a.dloss) * a.coef : 0.0f;
-    const bool norm = SIG || a.renorm;
-    const bool direct = !norm;                         // the weights' gradient goes through the softmax
+    int q = -1, q0 = 0, q1 = 0;                        // the sequence whose gradient is in g, its tokens
+    float g[NE];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) g[i] = 0.0f;
     for (int tb = c0 + warp * TPW; tb < c1; tb += kRWarps * TPW) {
         const int t = tb + grp;
         const bool in = t < c1;
@@ -305,36 +317,36 @@ __global__ void __launch_bounds__(kRWarps * 32) k_route_backward(RouteBackwardAr
         const float* row = a.logits + tr * a.E;
         // Every load first: the row and the lane's own slot (all there is when k <= G) do not wait for
         // what decides whether they are used.
-        float p[NE], slope[NE], d[NE];
+        float p[NE], slope[NE];
         R::template load<float4>(row, a.E, gl, in, p, -INFINITY);
         int e0 = in && gl < a.K ? __ldg(idx + gl) : -1;
         float x0 = in && a.dw && gl < a.K ? __ldg(dw + gl) : 0.0f;
         bool bal = in && a.dloss && !(a.mask && !__ldg(a.mask + t));
-        int q = 0;
-        float f = 0.0f;
-        if (bal) {
-            q = a.S > 1 || a.off ? seq_after(a.off, a.S, a.T, t) : 0;
-            bal = q < a.S && seq_at(a.off, a.S, a.T, q) <= t;
-            if (bal) {
+        if (bal && !(t >= q0 && t < q1)) {             // another sequence than the last token's
+            q = seq_after(a.off, a.S, a.T, t);
+            q0 = seq_at(a.off, a.S, a.T, q);           // q = S: no sequence ends behind t
+            q1 = q < a.S ? seq_at(a.off, a.S, a.T, q + 1) : 0;
+            if (t >= q0 && t < q1) {
                 const float n = static_cast<float>(__ldg(a.tokens + q)), full = static_cast<float>(__ldg(a.tokens + a.S));
-                f = n > 0.0f ? gloss / full * static_cast<float>(a.E) / (static_cast<float>(a.K) * n * n) : 0.0f;
+                const float f = n > 0.0f ? gloss / full * static_cast<float>(a.E) / (static_cast<float>(a.K) * n * n) : 0.0f;
+                int n_e[NE];
+                R::template load<int4>(a.counts + static_cast<size_t>(q) * a.E, a.E, gl, true, n_e, 0);
+#pragma unroll
+                for (int i = 0; i < NE; ++i) g[i] = f * static_cast<float>(n_e[i]);
+            } else {
+                q1 = 0;                                // in no sequence: g is not this range's
             }
         }
-        {
-            int n[NE];
-            R::template load<int4>(a.counts + static_cast<size_t>(q) * a.E, a.E, gl, bal, n, 0);
-#pragma unroll
-            for (int i = 0; i < NE; ++i) d[i] = f * static_cast<float>(n[i]);
-        }
+        bal = bal && t >= q0 && t < q1;
         if (e0 >= a.E) e0 = -1;
         const float l0 = e0 >= 0 ? __ldg(row + e0) : -INFINITY;
-        const float c0s = e0 >= 0 && a.pes ? __ldg(a.pes + e0) : 1.0f;
-        float nz = x0 != 0.0f ? 1.0f : 0.0f;               // NaN counts
+        const float scale0 = e0 >= 0 && a.pes ? __ldg(a.pes + e0) : 1.0f;
+        float nz = x0 != 0.0f ? 1.0f : 0.0f;           // NaN counts
         if (in && a.dw)
             for (int j = gl + G; j < a.K; j += G) nz = __ldg(dw + j) != 0.0f ? 1.0f : nz;
         const bool wts = group_max<G>(nz) != 0.0f;
         float z = 0.0f, m = -INFINITY;
-        if (SIG) {
+        if (MODE == kSigmoid) {
 #pragma unroll
             for (int i = 0; i < NE; ++i) z += (p[i] = sigmoid(p[i], slope[i]));
         } else {
@@ -342,16 +354,14 @@ __global__ void __launch_bounds__(kRWarps * 32) k_route_backward(RouteBackwardAr
             for (int i = 0; i < NE; ++i) m = fmaxf(m, p[i]);
             m = group_max<G>(m);
 #pragma unroll
-            for (int i = 0; i < NE; ++i) z += (p[i] = expf(p[i] - m));
+            for (int i = 0; i < NE; ++i) z += (p[i] = exp_neg(p[i] - m));
         }
-        const float rz = 1.0f / group_sum<G>(z);
-#pragma unroll
-        for (int i = 0; i < NE; ++i) p[i] *= rz;
+        const float rz = 1.0f / group_sum<G>(z);       // p[i] stays unscaled: the probability is p[i] * rz
 
         // ---- the routing weights' terms (a token without them adds zeros)
-        float sm = m, sz = 0.0f, sd = 0.0f;
-        const bool more = wts && a.K > G;                  // slots behind the lanes' first
-        if (!SIG && norm) {
+        float sm = m;
+        const bool more = wts && a.K > G;              // slots behind the lanes' first
+        if (MODE == kRenorm) {
             float v = l0;
             if (more)
                 for (int j = gl + G; j < a.K; j += G) {
@@ -360,14 +370,13 @@ __global__ void __launch_bounds__(kRWarps * 32) k_route_backward(RouteBackwardAr
                 }
             sm = group_max<G>(v);
         }
-        auto raw = [&](float l) {                          // the weight before the normalization
+        auto raw = [&](float l) {                      // the weight before the normalization
             float s;
-            return SIG ? sigmoid(l, s) : norm ? expf(l - sm) : expf(l - m) * rz;
+            return MODE == kSigmoid ? sigmoid(l, s) : MODE == kRenorm ? exp_neg(l - sm) : exp_neg(l - m) * rz;
         };
         x0 *= a.rsf;
-        const float u0 = e0 >= 0 ? raw(l0) : 0.0f, du0 = x0 * c0s;
-        sz = u0;
-        sd = u0 * du0;
+        const float u0 = e0 >= 0 ? raw(l0) : 0.0f, du0 = x0 * scale0;
+        float sz = u0, sd = u0 * du0;
         if (more)
             for (int j = gl + G; j < a.K; j += G) {
                 const int e = __ldg(idx + j);
@@ -376,28 +385,26 @@ __global__ void __launch_bounds__(kRWarps * 32) k_route_backward(RouteBackwardAr
                 sz += v;
                 sd += v * (__ldg(dw + j) * a.rsf * (a.pes ? __ldg(a.pes + e) : 1.0f));
             }
-        if (norm) {
+        if (MODE == kDirect) {
+            sz = 1.0f;
+        } else {
             sz = 1.0f / group_sum<G>(sz);
             sd = group_sum<G>(sd) * sz;
-        } else {
-            sz = 1.0f;
         }
-        // ids of a token are distinct: plain stores
-        if (wts && e0 >= 0) add[e0] = direct ? du0 : SIG ? (du0 - sd) * sz : u0 * sz * (du0 - sd);
+        auto term = [&](float v, float du) {           // what a slot adds to its expert
+            return MODE == kDirect ? du : MODE == kSigmoid ? (du - sd) * sz : v * sz * (du - sd);
+        };
+        if (wts && e0 >= 0) add[e0] = term(u0, du0);   // ids of a token are distinct: plain stores
         if (more)
             for (int j = gl + G; j < a.K; j += G) {
                 const int e = __ldg(idx + j);
-                if (e < 0 || e >= a.E) continue;
-                const float u = raw(__ldg(row + e)) * sz;
-                const float du = __ldg(dw + j) * a.rsf * (a.pes ? __ldg(a.pes + e) : 1.0f);
-                add[e] = direct ? du : SIG ? (du - sd) * sz : u * (du - sd);
+                if (e >= 0 && e < a.E)
+                    add[e] = term(raw(__ldg(row + e)), __ldg(dw + j) * a.rsf * (a.pes ? __ldg(a.pes + e) : 1.0f));
             }
         __syncwarp();
 
         // ---- the row
         float x[NE], dot = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NE; ++i) x[i] = 0.0f;
         if (VEC) {
 #pragma unroll
             for (int i = 0; i < NE; i += 4) {
@@ -408,19 +415,22 @@ __global__ void __launch_bounds__(kRWarps * 32) k_route_backward(RouteBackwardAr
 #pragma unroll
             for (int i = 0; i < NE; ++i) x[i] = add[R::expert(i, gl)];
         }
+        // dp: the balance loss's, and for kDirect the slots' too
+        const bool through = bal || (MODE == kDirect && wts);
+        const float on = bal ? 1.0f : 0.0f;
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
-            if (direct) d[i] += x[i], x[i] = 0.0f;
-            dot = fmaf(p[i], d[i], dot);
+            const float d = MODE == kDirect ? fmaf(on, g[i], x[i]) : on * g[i];
+            dot = fmaf(p[i], d, dot);
         }
-        dot = group_sum<G>(dot);
-        // a token with one kind of gradient takes no part of the other (its row may hold NaN only there)
-        const bool through = bal || (direct && wts);
+        dot = group_sum<G>(dot) * rz;
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
-            if (SIG) p[i] = slope[i] * ((through ? (d[i] - dot) * rz : 0.0f) + x[i]);
-            else p[i] = through ? fmaf(p[i], d[i] - dot, x[i]) : x[i];
-            if (!bal && !wts) p[i] = 0.0f;
+            const float d = MODE == kDirect ? fmaf(on, g[i], x[i]) : on * g[i];
+            // a token takes no part of a gradient that it does not have (its row may hold NaN)
+            if (MODE == kSigmoid) p[i] = slope[i] * ((through ? (d - dot) * rz : 0.0f) + x[i]);
+            else p[i] = (MODE == kDirect ? 0.0f : x[i]) + (through ? p[i] * rz * (d - dot) : 0.0f);
+            if (MODE == kSigmoid && !bal && !wts) p[i] = 0.0f;
         }
         if (in) R::store(a.dl + tr * a.E, a.E, gl, p);
         __syncwarp();
@@ -432,8 +442,8 @@ __global__ void __launch_bounds__(kRWarps * 32) k_route_backward(RouteBackwardAr
                 if (e >= 0 && e < a.E) add[e] = 0.0f;
             }
         if (a.dpes) {
-            for (int g = 0; g < TPW; ++g) {
-                if (g == grp && wts) {
+            for (int w = 0; w < TPW; ++w) {
+                if (w == grp && wts) {
                     if (e0 >= 0) dscale[e0] += x0 * (u0 * sz);
                     if (more)
                         for (int j = gl + G; j < a.K; j += G) {
@@ -485,14 +495,18 @@ cudaError_t balance_t(const BalanceArgs& a, bool vec, cudaStream_t s) {
                : launch_pdl(k_balance<NE, G, false, false>, grid, block, 0, s, a);
 }
 
+template <int NE, int G, int MODE>
+cudaError_t backward_m(const RouteBackwardArgs& a, bool vec, cudaStream_t s) {
+    const dim3 grid(a.chunks), block(kRWarps * 32);
+    return vec ? launch_pdl(k_route_backward<NE, G, true, MODE>, grid, block, 0, s, a)
+               : launch_pdl(k_route_backward<NE, G, false, MODE>, grid, block, 0, s, a);
+}
+
 template <int NE, int G>
 cudaError_t backward_t(const RouteBackwardArgs& a, bool vec, cudaStream_t s) {
-    const dim3 grid(a.chunks), block(kRWarps * 32);
-    if (a.routing)
-        return vec ? launch_pdl(k_route_backward<NE, G, true, true>, grid, block, 0, s, a)
-                   : launch_pdl(k_route_backward<NE, G, false, true>, grid, block, 0, s, a);
-    return vec ? launch_pdl(k_route_backward<NE, G, true, false>, grid, block, 0, s, a)
-               : launch_pdl(k_route_backward<NE, G, false, false>, grid, block, 0, s, a);
+    return a.routing  ? backward_m<NE, G, kSigmoid>(a, vec, s)
+           : a.renorm ? backward_m<NE, G, kRenorm>(a, vec, s)
+                      : backward_m<NE, G, kDirect>(a, vec, s);
 }
 
 bool rows16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -513,8 +527,8 @@ cudaError_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t s) {
     const bool vec = a.E % 4 == 0 && rows16(a.logits) && rows16(a.dl) && rows16(a.counts);
     const cudaError_t e = a.E <= 32    ? backward_t<4, 8>(a, vec, s)
                           : a.E <= 64  ? backward_t<8, 8>(a, vec, s)
-                          : a.E <= 128 ? backward_t<16, 8>(a, vec, s)
-                                       : backward_t<16, 16>(a, vec, s);
+                          : a.E <= 128 ? backward_t<8, 16>(a, vec, s)
+                                       : backward_t<8, 32>(a, vec, s);
     if (e != cudaSuccess || !a.dpes) return e;
     return launch_pdl(k_join_scale_grad, dim3((a.E + 31) / 32), dim3(1024), 0, s, a);
 }

@@ -77,7 +77,7 @@ inline int balance_chunk(int T) {
     return c < 32 ? 32 : c;
 }
 inline int balance_chunks(int T) { return (T + balance_chunk(T) - 1) / balance_chunk(T); }
-// The gradients' chunks: a block of 8 warps each, several blocks on an SM.
+// The gradients' chunks: a block of 8 warps each, four blocks on an SM at 64 registers a thread.
 constexpr int kBackwardChunks = 592;
 inline int backward_chunk(int T) {
     const int c = (T + kBackwardChunks - 1) / kBackwardChunks;
