@@ -269,11 +269,30 @@ cudaError_t launch_linear_fp32(const LinearArgs& a, const CUtensorMap& tmX, cons
     return launch_pdl(k_linear_fp32, dim3(num_sms), dim3(kThreads), kSmemBytes, s, tmX, tmW, a);
 }
 
-uint32_t linear_token_box(const LinearArgs&) { return kTileM; }
-uint32_t linear_weight_box(const LinearArgs& a) { return a.recipe == 0 ? kTileN : 128; }
+// The narrow kernel takes a product when its estimated time is below the wide kernel's: both are
+// (rounds of CTAs over the SMs) x (K groups of a CTA) x (time of a group).
+bool linear_is_narrow(int T, int N, int K, int recipe, int num_sms) {
+    const long long KB = K / kTileK;
+    const int nt = linear_narrow_tokens(T), split = linear_narrow_split(T, N, K, num_sms);
+    const long long tiles = static_cast<long long>((N + kTileM - 1) / kTileM) * ((T + nt - 1) / nt);
+    if ((T + nt - 1) / nt > 65535) return false;       // grid.z
+    const int wn = recipe == 0 ? kTileN : 128;
+    const long long units = static_cast<long long>((N + wn - 1) / wn) * ((T + kTileM - 1) / kTileM);
+    const long long narrow = (tiles * split + num_sms - 1) / num_sms * ((KB + split - 1) / split) * 700;
+    const long long wide = (units + num_sms - 1) / num_sms * KB * (recipe == 0 ? 1550 : 700);
+    return narrow < wide;
+}
+
+uint32_t linear_token_box(const LinearArgs& a, int num_sms) {
+    return linear_is_narrow(a.T, a.N, a.K, a.recipe, num_sms) ? linear_narrow_tokens(a.T) : kTileM;
+}
+uint32_t linear_weight_box(const LinearArgs& a, int num_sms) {
+    return a.recipe != 0 || linear_is_narrow(a.T, a.N, a.K, a.recipe, num_sms) ? 128 : kTileN;
+}
 
 cudaError_t launch_linear(const LinearArgs& a, const CUtensorMap& tmX, const CUtensorMap& tmW, int num_sms,
                           cudaStream_t s) {
+    if (linear_is_narrow(a.T, a.N, a.K, a.recipe, num_sms)) return launch_linear_narrow(a, tmX, tmW, num_sms, s);
     return a.recipe == 0 ? launch_linear_fp32(a, tmX, tmW, num_sms, s) : launch_linear_mx(a, tmX, tmW, num_sms, s);
 }
 

@@ -1,0 +1,392 @@
+// linear_narrow.cu -- the dense FP8 product for few tokens (moe_linear), every recipe: swap-AB, so
+// that a tile is 128 weight rows (output columns) by 32 or 64 tokens and computes little padding,
+// with K split over a cluster so that a product of few tiles still uses every SM.
+//
+// A CTA of the cluster takes a contiguous share of the K groups: TMA loads of 128 weight rows and the
+// token rows per 128-deep stage, then
+//   recipe 0:    tcgen05.mma.kind::f8f6f4 per group into one of four TMEM buffers, promoted by the
+//                epilogue warps, acc[token] += P * (a_s[token] * w_s[row]);
+//   recipes 1, 2: the block-scaled MMA over the whole share in one TMEM accumulator, the weights'
+//                scale atoms as SFA, the tokens' built per stage by one warp as SFB.
+// The shares meet in shared memory: each CTA stores its partial sums of a token into the CTA that
+// owns the token (distributed shared memory), which adds them in rank order and runs the epilogue.
+// What bounds it: the weight bytes, and at one token the latency of one load, one MMA chain and the
+// exchange.  Two CTAs fit an SM.  Every wait is bounded.
+#include "linear_common.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kSThreads = 256;
+constexpr int kSEpiWarps = 4;
+constexpr int kSBuf = 4;                               // TMEM buffers of recipe 0
+constexpr uint32_t kSA = kTileM * kTileK;              // 16 KB of weights
+constexpr uint32_t kSSf = 512;
+
+template <int NT>
+struct SL {
+    static constexpr int stages = NT == 32 ? 4 : 3;    // two CTAs an SM
+    static constexpr uint32_t bytes_b = NT * kTileK;
+    static constexpr uint32_t b = kSA;
+    static constexpr uint32_t ws = kSA + bytes_b;      // fp32 weight scales, or the weights' atom
+    static constexpr uint32_t ts = ws + kSSf;          // fp32 token scales, or the tokens' atom
+    static constexpr uint32_t stage = ts + kSSf;
+    static constexpr uint32_t part = stages * stage;   // [source rank][token of mine][128]
+    static constexpr uint32_t bars = part + NT * 128 * 4;
+    static constexpr uint32_t nbars = 3 * stages + 2 * kSBuf + 1;   // full, sfready, empty, tfull, tempty, drain
+    static constexpr uint32_t misc = bars + nbars * 8;
+    static constexpr uint32_t end = misc + 16;
+    static constexpr uint32_t smem = end + 1024;
+    static constexpr uint32_t tmem_cols = NT == 32 ? 128 : 256;
+    static constexpr uint32_t sf_col0 = NT;            // scale factors behind the one accumulator
+    static_assert(stage % 1024 == 0, "stage alignment");
+    static_assert(kSBuf * NT <= tmem_cols && sf_col0 + stages * 8 <= tmem_cols, "TMEM");
+    static_assert(smem <= 113 * 1024, "two CTAs an SM");
+};
+
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t smem_addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// The cluster barrier in its two halves (every thread of every CTA, once each).
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void finish_one(const LinearArgs& p, float v, int t, int n) {
+    if (p.bias) v += __bfloat162float(p.bias[n]);
+    v = linear_act(v, p.act);
+    const size_t at = static_cast<size_t>(t) * p.N + n;
+    if (p.res) v += __bfloat162float(p.res[at]);
+    p.y[at] = __float2bfloat16_rn(v);
+}
+
+}  // namespace
+
+// Grid (split, weight blocks, token blocks), clusters of `split` CTAs.
+template <int NT, bool MX>
+__global__ void __launch_bounds__(kSThreads, 2)
+    k_linear_narrow(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmT, const LinearArgs p) {
+    using S = SL<NT>;
+    constexpr int ST = S::stages;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::bars);
+    uint64_t* sfready = full + ST;
+    uint64_t* empty = sfready + ST;
+    uint64_t* tfull = empty + ST;
+    uint64_t* tempty = tfull + kSBuf;
+    uint64_t* drain = tempty + kSBuf;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + S::misc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::misc + 4);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split = gridDim.x, rank = blockIdx.x;
+    const int n0 = blockIdx.y * kTileM, t0 = blockIdx.z * NT;
+    const int KB = p.K / kTileK;
+    const int g0 = static_cast<int>(static_cast<long long>(rank) * KB / split);
+    const int n = static_cast<int>(static_cast<long long>(rank + 1) * KB / split) - g0;   // this CTA's groups (may be 0)
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&sfready[s], 1);
+            mbar_init(&empty[s], MX ? 1 : 1 + kSEpiWarps);
+        }
+        for (int b = 0; b < kSBuf; ++b) {
+            mbar_init(&tfull[b], 1);
+            mbar_init(&tempty[b], kSEpiWarps);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&tmW);
+        prefetch_tmap(&tmT);
+        for (int i = 0; i < n && i < ST; ++i) tma_prefetch_2d(&tmW, (g0 + i) * kTileK, n0);   // toward L2, ahead of the wait
+    }
+    if (warp == 1) tmem_alloc(tmem_holder, S::tmem_cols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (split > 1) cluster_arrive();                   // this CTA has started (waited for before the exchange)
+    pdl_wait_then_release();
+    if (p.clear && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *p.status = MOE_OK;
+    const uint32_t tmem_base = *tmem_holder;
+    float acc[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[j] = 0.0f;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------------------------ TMA producer
+            const uint32_t a_bytes = p.recipe == 2 ? kSA / 2 : kSA;   // E2M1 weights arrive packed
+            const int n_pad = (p.N + kLinearPad - 1) / kLinearPad * kLinearPad;
+            int it = 0;
+            bool ok = true;
+            for (; it < n; ++it) {
+                const int s = it % ST, kb = g0 + it;
+                if (it >= ST && !mbar_wait(&empty[s], ((it / ST) & 1) ^ 1, abort_flag, p.status)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t* st = smem + s * S::stage;
+                mbar_arrive_expect_tx(&full[s], a_bytes + S::bytes_b + kSSf + (MX ? 0 : NT * 4));
+                tma_load_2d(st, &tmW, kb * kTileK, n0, &full[s]);
+                tma_load_2d(st + S::b, &tmT, kb * kTileK, t0, &full[s]);
+                if (MX) {
+                    bulk_load(st + S::ws, static_cast<const uint8_t*>(p.w_scale) +
+                                              (static_cast<size_t>(blockIdx.y) * KB + kb) * kSSf, kSSf, &full[s]);
+                } else {
+                    bulk_load(st + S::ws, static_cast<const float*>(p.w_scale) + static_cast<size_t>(kb) * n_pad + n0,
+                              kSSf, &full[s]);
+                    bulk_load(st + S::ts, static_cast<const float*>(p.a_scale) + static_cast<size_t>(kb) * p.a_pad + t0,
+                              NT * 4, &full[s]);
+                }
+            }
+            if (!ok) {   // let the copies already issued land before the CTA leaves
+                for (int i = it > ST ? it - ST : 0; i < it; ++i) drain_wait(&full[i % ST], (i / ST) & 1);
+            }
+        }
+    } else if (warp == 2) {
+        if (MX) {
+            // -------------------------------------------------------------------- token-scale atoms
+            // lane i: the words of tokens i (and 32 + i); the scale rows reach 132 past T
+            const uint32_t* src = static_cast<const uint32_t*>(p.a_scale) + static_cast<size_t>(g0) * p.a_pad + t0 + lane;
+            for (int it = 0; it < n; ++it, src += p.a_pad) {
+                const uint32_t w0 = __ldg(src), w1 = NT == 64 ? __ldg(src + 32) : 0u;
+                const int s = it % ST;
+                if (it >= ST && !mbar_wait(&empty[s], ((it / ST) & 1) ^ 1, abort_flag, p.status)) break;
+                *reinterpret_cast<uint2*>(smem + s * S::stage + S::ts + 16 * lane) = make_uint2(w0, w1);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // visible to tcgen05.cp
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sfready[s]);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ------------------------------------------------------------------ MMA issuer
+            const uint32_t idesc = f8_idesc(kTileM, NT);
+            const uint32_t afmt = p.recipe == 2 ? 5u : 0u;
+            bool ok = true;
+            for (int it = 0; it < n; ++it) {
+                const int s = it % ST, b = it % kSBuf;
+                if (!mbar_wait(&full[s], (it / ST) & 1, abort_flag, p.status) ||
+                    (MX && !mbar_wait(&sfready[s], (it / ST) & 1, abort_flag, p.status)) ||
+                    (!MX && it >= kSBuf && !mbar_wait(&tempty[b], ((it / kSBuf) & 1) ^ 1, abort_flag, p.status))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t st = smem_u32(smem + s * S::stage);
+                if (MX) {
+                    const uint32_t sfa_t = tmem_base + S::sf_col0 + static_cast<uint32_t>(s * 8), sfb_t = sfa_t + 4;
+                    sf_copy(sfa_t, sf_atom_desc(st + S::ws));
+                    sf_copy(sfb_t, sf_atom_desc(st + S::ts));
+#pragma unroll
+                    for (uint32_t k = 0; k < 4; ++k)
+                        mma_mx(tmem_base, sw128_kmajor_desc(st + k * 32), sw128_kmajor_desc(st + S::b + k * 32),
+                               mx_block_idesc(k, afmt, 0u, kTileM, NT), sfa_t, sfb_t, (it > 0 || k > 0) ? 1u : 0u);
+                } else {
+                    const uint32_t d = tmem_base + static_cast<uint32_t>(b * NT);
+#pragma unroll
+                    for (uint32_t k = 0; k < 4; ++k)
+                        mma_f8(d, sw128_kmajor_desc(st + k * 32), sw128_kmajor_desc(st + S::b + k * 32), idesc,
+                               k > 0 ? 1u : 0u);
+                    mma_commit(&tfull[b]);
+                }
+                mma_commit(&empty[s]);
+            }
+            if (MX && ok && n > 0) mma_commit(&tfull[0]);
+            mma_commit(drain);          // all MMAs issued by this thread have finished
+            drain_wait(drain, 0);
+        }
+    } else if (warp >= 4) {
+        // ---------------------------------------------------------------------- epilogue: the share's sums
+        const int quad = warp & 3;      // TMEM lanes 32*quad .. = weight rows of the tile
+        const uint32_t trow = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+        bool ok = true;
+        if (MX) {
+            if (n > 0) {
+                ok = mbar_wait(&tfull[0], 0, abort_flag, p.status);
+                if (__all_sync(0xffffffffu, ok)) {
+                    tc_fence_after();
+#pragma unroll
+                    for (int h = 0; h < NT; h += 32) {
+                        uint32_t v[32];
+                        MOE_TMEM_LD32(trow + h, v);
+                        MOE_TMEM_WAIT_LD(v);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) acc[h + j] = __uint_as_float(v[j]);
+                    }
+                }
+            }
+        } else {
+            for (int it = 0; it < n; ++it) {
+                const int s = it % ST, b = it % kSBuf;
+                // the stage's scales (bulk copies), then the group's partial sums
+                ok = mbar_wait(&full[s], (it / ST) & 1, abort_flag, p.status) &&
+                     mbar_wait(&tfull[b], (it / kSBuf) & 1, abort_flag, p.status);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t st = smem_u32(smem + s * S::stage);
+                const float ws = ld_shared_f32(st + S::ws + static_cast<uint32_t>((quad * 32 + lane) * 4));
+#pragma unroll
+                for (int h = 0; h < NT; h += 32) {
+                    uint32_t v[32];
+                    MOE_TMEM_LD32(trow + static_cast<uint32_t>(b * NT + h), v);
+                    MOE_TMEM_WAIT_LD(v);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 a4 = ld_shared_f32x4(st + S::ts + static_cast<uint32_t>((h + j) * 4));
+                        acc[h + j] = fmaf(__uint_as_float(v[j]), a4.x * ws, acc[h + j]);
+                        acc[h + j + 1] = fmaf(__uint_as_float(v[j + 1]), a4.y * ws, acc[h + j + 1]);
+                        acc[h + j + 2] = fmaf(__uint_as_float(v[j + 2]), a4.z * ws, acc[h + j + 2]);
+                        acc[h + j + 3] = fmaf(__uint_as_float(v[j + 3]), a4.w * ws, acc[h + j + 3]);
+                    }
+                }
+                tc_fence_before();
+                // the scales were read through the generic proxy; the next bulk copy into this stage
+                // is an async-proxy write: order the reads before it
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&tempty[b]);
+                    mbar_arrive(&empty[s]);
+                }
+            }
+        }
+        if (!__all_sync(0xffffffffu, ok)) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[j] = __int_as_float(0x7fc00000);   // a wait ran out: NaN
+        }
+    }
+    __syncwarp();
+
+    // -------------------------------------------------------------------------- the shares meet
+    const int row = (warp & 3) * 32 + lane, col = n0 + row;
+    if (split == 1) {
+        if (warp >= 4 && col < p.N) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                if (t0 + j < p.T) finish_one(p, acc[j], t0 + j, col);
+        }
+    } else {
+        const int per = NT / split;                    // tokens a CTA finishes
+        const uint32_t part = smem_u32(smem + S::part);
+        // Two neighbouring columns a thread, tokens threadIdx / 64, + 4, ...; the first residuals are
+        // fetched while the shares are on their way.
+        const int c2 = (threadIdx.x & 63) * 2, tq = threadIdx.x >> 6, n2 = n0 + c2;
+        const bool pair = p.N % 2 == 0;
+        __nv_bfloat162 r0 = __floats2bfloat162_rn(0.0f, 0.0f), r1 = r0;
+        const int ta = t0 + rank * per + tq, tb = ta + 4;
+        if (p.res && pair && n2 < p.N) {
+            if (tq < per && ta < p.T) r0 = *reinterpret_cast<const __nv_bfloat162*>(p.res + static_cast<size_t>(ta) * p.N + n2);
+            if (tq + 4 < per && tb < p.T) r1 = *reinterpret_cast<const __nv_bfloat162*>(p.res + static_cast<size_t>(tb) * p.N + n2);
+        }
+        const float b0 = p.bias && n2 < p.N ? __bfloat162float(p.bias[n2]) : 0.0f;
+        const float b1 = p.bias && n2 + 1 < p.N ? __bfloat162float(p.bias[n2 + 1]) : 0.0f;
+        cluster_wait();                                // every CTA of the cluster has started
+        if (warp >= 4) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int owner = j / per, jl = j - owner * per;
+                if (t0 + j < p.T)
+                    st_cluster_f32(cluster_addr(part + static_cast<uint32_t>(((rank * per + jl) * 128 + row) * 4),
+                                                static_cast<uint32_t>(owner)), acc[j]);
+            }
+        }
+        cluster_sync_all();
+        const float* mine = reinterpret_cast<const float*>(smem + S::part) + c2;
+        for (int jl = tq; jl < per; jl += 4) {
+            const int t = t0 + rank * per + jl;
+            if (t >= p.T || n2 >= p.N) break;
+            float2 v = *reinterpret_cast<const float2*>(mine + jl * 128);
+#pragma unroll 8
+            for (int r = 1; r < split; ++r) {
+                const float2 x = *reinterpret_cast<const float2*>(mine + (r * per + jl) * 128);
+                v.x += x.x, v.y += x.y;
+            }
+            v.x = linear_act(v.x + b0, p.act), v.y = linear_act(v.y + b1, p.act);
+            const size_t at = static_cast<size_t>(t) * p.N + n2;
+            if (pair) {
+                if (p.res) {
+                    const float2 r = __bfloat1622float2(
+                        jl == tq ? r0 : jl == tq + 4 ? r1 : *reinterpret_cast<const __nv_bfloat162*>(p.res + at));
+                    v.x += r.x, v.y += r.y;
+                }
+                *reinterpret_cast<__nv_bfloat162*>(p.y + at) = __floats2bfloat162_rn(v.x, v.y);
+            } else {
+                if (p.res) v.x += __bfloat162float(p.res[at]);
+                p.y[at] = __float2bfloat16_rn(v.x);
+                if (n2 + 1 < p.N) {
+                    if (p.res) v.y += __bfloat162float(p.res[at + 1]);
+                    p.y[at + 1] = __float2bfloat16_rn(v.y);
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem_base, S::tmem_cols);
+    }
+}
+
+int linear_narrow_tokens(int T) { return T <= 32 ? 32 : 64; }
+
+// The widest split that still lets every CTA run at once (two an SM) and gives each a K group.
+int linear_narrow_split(int T, int N, int K, int num_sms) {
+    const int nt = linear_narrow_tokens(T);
+    const long long tiles = static_cast<long long>((N + kTileM - 1) / kTileM) * ((T + nt - 1) / nt);
+    int split = 8;
+    while (split > 1 && (tiles * split > 2LL * num_sms || split > K / kTileK)) split >>= 1;
+    return split;
+}
+
+template <int NT, bool MX>
+static cudaError_t launch_narrow_t(const LinearArgs& a, const CUtensorMap& tmX, const CUtensorMap& tmW, int split,
+                                   cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(k_linear_narrow<NT, MX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(SL<NT>::smem));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(split, (a.N + kTileM - 1) / kTileM, (a.T + NT - 1) / NT);
+    cfg.blockDim = dim3(kSThreads);
+    cfg.dynamicSmemBytes = SL<NT>::smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k_linear_narrow<NT, MX>, tmW, tmX, a);
+}
+
+cudaError_t launch_linear_narrow(const LinearArgs& a, const CUtensorMap& tmX, const CUtensorMap& tmW, int num_sms,
+                                 cudaStream_t s) {
+    const int split = linear_narrow_split(a.T, a.N, a.K, num_sms);
+    if (linear_narrow_tokens(a.T) == 32)
+        return a.recipe == 0 ? launch_narrow_t<32, false>(a, tmX, tmW, split, s)
+                             : launch_narrow_t<32, true>(a, tmX, tmW, split, s);
+    return a.recipe == 0 ? launch_narrow_t<64, false>(a, tmX, tmW, split, s)
+                         : launch_narrow_t<64, true>(a, tmX, tmW, split, s);
+}
+
+}  // namespace moe

@@ -833,8 +833,8 @@ int moe_linear(const moe_linear_config_t* cfg, const void* x, const void* codes,
     a.status = static_cast<int32_t*>(workspace);
     a.clear = x == nullptr;
     CUtensorMap tm_x, tm_w;
-    if ((rc = make_kmajor_map(&tm_x, x ? ws + q_at : codes, T, K, moe::linear_token_box(a)))) return rc;
-    if ((rc = make_kmajor_map(&tm_w, w_t, N, K, moe::linear_weight_box(a), cfg->recipe == 2))) return rc;
+    if ((rc = make_kmajor_map(&tm_x, x ? ws + q_at : codes, T, K, moe::linear_token_box(a, di.sms)))) return rc;
+    if ((rc = make_kmajor_map(&tm_w, w_t, N, K, moe::linear_weight_box(a, di.sms), cfg->recipe == 2))) return rc;
     if (x) {
         moe::QuantRowsArgs q{static_cast<const __nv_bfloat16*>(x), ws + q_at, reinterpret_cast<uint32_t*>(ws + s_at),
                              a.status, T, K, cfg->recipe, a.a_pad};
