@@ -216,7 +216,7 @@ def _stream(stream):
 
 def _raw_stream(stream, dev):
     """The stream's handle; the current stream of dev by default."""
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
 
 
 # --------------------------------------------------------------------------------------------
@@ -437,10 +437,10 @@ def _refuse(msg: str):
 
 
 def _device_of(t, name: str):
-    """The device of a call's first tensor, which has to be the current one (its stream and kernels)."""
-    dev = t.device
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        _refuse(f"{name} is on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    """The device index of a call's first tensor, which has to be the current one (its stream and kernels)."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        _refuse(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
     return dev
 
 
@@ -448,16 +448,16 @@ def _arg(t, name: str, shape, dtype, dev):
     """Pointer of tensor t (None: NULL); anything but a contiguous tensor of this shape, type and device is refused."""
     if t is None:
         return None
-    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
         return t.data_ptr()
-    _refuse(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got "
+    _refuse(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}, got "
             f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
 def _workspace_arg(t, dev):
-    if t.device != dev or not t.is_contiguous():
-        _refuse(f"workspace must be a contiguous tensor on {dev}")
-    return t.data_ptr(), t.numel() * t.element_size()
+    if t.get_device() != dev or not t.is_contiguous():
+        _refuse(f"workspace must be a contiguous tensor on cuda:{dev}")
+    return t.data_ptr(), t.nbytes
 
 
 def quantized_size(rows: int, cols: int):
@@ -523,7 +523,7 @@ def transform_linear_weights(cfg: LinearConfig, w, w_scale, stream=None):
     [K/32, N]) -> (w_t, ws_t) uint8 device tensors, for any num_tokens."""
     dev = _device_of(w, "w")
     K, N, g = cfg.in_features, cfg.out_features, 128 if cfg.recipe == 0 else 32
-    outs = [torch.empty(n, dtype=torch.uint8, device=dev) for n in transformed_linear_size(cfg)]
+    outs = [w.new_empty(n, dtype=torch.uint8) for n in transformed_linear_size(cfg)]
     c = cfg.c()
     _check(_load().moe_transform_linear_weights(
         ctypes.byref(c), _arg(w, "w", (K, N // 2 if cfg.recipe == 2 else N), torch.uint8, dev),
@@ -556,7 +556,7 @@ def linear(cfg: LinearConfig, weights, x=None, quantized=None, bias=None, residu
         y = weights[0].new_empty((T, N), dtype=torch.bfloat16)
     if workspace is None:
         n = linear_workspace_size(cfg) if quantized is None else MOE_LINEAR_STATUS_BYTES
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        workspace = y.new_empty(n, dtype=torch.uint8)
     c = cfg.c()
     w_t, ws_t = weights
     w_bytes = K * N // (2 if cfg.recipe == 2 else 1)
@@ -605,7 +605,7 @@ def balance_loss(cfg: Config, router_logits, topk_idx, coef: float, seq_offsets=
     counts, tokens = topk_idx.new_empty((S, E)), topk_idx.new_empty(S + 1)
     mean, loss = router_logits.new_empty((S, E)), router_logits.new_empty(1)
     if workspace is None:
-        workspace = new_balance_workspace(cfg, S, dev)
+        workspace = new_balance_workspace(cfg, S, router_logits.device)
     c = cfg.c()
     _check(_load().moe_balance_loss(
         ctypes.byref(c), _arg(router_logits, "router_logits", (T, E), torch.float32, dev),
@@ -630,7 +630,7 @@ def route_backward(cfg: Config, router_logits, topk_idx, d_topk_weights=None, pe
     if per_expert_scale is not None:
         d_scale = torch.empty_like(per_expert_scale)
         if workspace is None:
-            workspace = new_balance_workspace(cfg, S, dev)
+            workspace = new_balance_workspace(cfg, S, router_logits.device)
         ws = _workspace_arg(workspace, dev)
     c = cfg.c()
     _check(_load().moe_route_backward(

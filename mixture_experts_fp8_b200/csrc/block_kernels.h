@@ -59,21 +59,26 @@ inline int linear_n_pad(int N) { return (N + kLinearPad - 1) / kLinearPad * kLin
 cudaError_t launch_add_rms_norm(NormArgs a, cudaStream_t s);
 cudaError_t launch_quant_rows(const QuantRowsArgs& a, cudaStream_t s);
 cudaError_t launch_linear_transform(const LinearTransformArgs& a, cudaStream_t s);
-// Which kernel takes a product: the narrow one (few tokens, K split over a cluster) or the wide ones.
+// The tensor maps of a product: x codes [T, K], w codes [N, K], the weights' scale atoms as 32-bit words
+// [n_pad/128, K/128, 128] (the block-scaled pair kernel), y [T, N] (the pair kernels, N a multiple of 8).
+struct LinearMaps {
+    CUtensorMap x, w, sf, y;
+};
+
+// Which kernel takes a product: the narrow one (few tokens, K split over a cluster) or a pair kernel.
 bool linear_is_narrow(int T, int N, int K, int recipe, int num_sms);
 int linear_narrow_tokens(int T);
 int linear_narrow_split(int T, int N, int K, int num_sms);
-// tmX: codes [T, K], tmW: codes [N, K] (box rows as the two functions say).
-uint32_t linear_token_box(const LinearArgs& a, int num_sms);
-uint32_t linear_weight_box(const LinearArgs& a, int num_sms);
-cudaError_t launch_linear(const LinearArgs& a, const CUtensorMap& tmX, const CUtensorMap& tmW, int num_sms,
-                          cudaStream_t s);
-cudaError_t launch_linear_narrow(const LinearArgs& a, const CUtensorMap& tmX, const CUtensorMap& tmW, int num_sms,
-                                 cudaStream_t s);
-cudaError_t launch_linear_fp32(const LinearArgs& a, const CUtensorMap& tmX, const CUtensorMap& tmW, int num_sms,
-                               cudaStream_t s);
-cudaError_t launch_linear_mx(const LinearArgs& a, const CUtensorMap& tmX, const CUtensorMap& tmW, int num_sms,
-                             cudaStream_t s);
+// Rows of the tensor maps' boxes.
+struct LinearBoxes {
+    uint32_t x, w;
+    bool pair;                  // the pair kernels' maps are needed too
+};
+LinearBoxes linear_boxes(const LinearArgs& a, int num_sms);
+cudaError_t launch_linear(const LinearArgs& a, const LinearMaps& m, int num_sms, cudaStream_t s);
+cudaError_t launch_linear_narrow(const LinearArgs& a, const LinearMaps& m, int num_sms, cudaStream_t s);
+cudaError_t launch_linear_fp32(const LinearArgs& a, const LinearMaps& m, int num_sms, cudaStream_t s);
+cudaError_t launch_linear_mx(const LinearArgs& a, const LinearMaps& m, int num_sms, cudaStream_t s);
 
 // Tokens are taken in chunks; chunk c and sequence s that meet have the partial sums of slot c + s:
 // walking the tokens in order raises c or s at every step, so no two pairs share a slot.

@@ -5,53 +5,65 @@
 //
 // The fp32 scales vary with the row, the column and the 128-deep group, so each group's partial
 // leaves the tensor core and is promoted, acc += P * (a_s * w_s): the FP32 pipe does as much work as
-// the tensor core.  Persistent, one CTA per SM, tiles of 128 tokens x 256 columns, as the layer's
-// wide GEMM lays them out: warp 0 loads by TMA, warp 1 issues tcgen05.mma.kind::f8f6f4 (M 128, N 256,
-// K 32) into one of two 256-column TMEM buffers per group, warps 4-19 promote into registers and run
-// the epilogue.  Units go column block by column block, token blocks fastest, so that CTAs working
-// at the same time share a weight tile in L2.  Every wait is bounded.
+// the tensor core, 2 x 128 x 192 operations at 128 a cycle (384 cycles) beside the MMAs' 384.
+//
+// CTA pairs (cta_group::2), persistent: a tile is 256 tokens x 192 columns; each CTA of the pair holds
+// 128 token rows and half of the weight rows (28 KB a stage) and promotes its own 128 x 192 sums.
+// Against the 128 x 256 tiles of one CTA (48 KB a stage, 4 stages, 64 accumulators a thread) six stages
+// fit, a thread keeps 48 accumulators, and a group's whole partial goes to registers at once, so that
+// its TMEM buffer is handed back before the arithmetic.  The scales have a ring of their own, so that
+// an operand stage is free when its MMAs are done.
+//
+// Threads (640): warp 0 TMA producer, warp 1 MMA issuer (the even CTA's, for both), warp 2 scales,
+// warp 3 idle, warps 4-19 epilogue (TMEM lanes 32 (w % 4).., 48 columns each).  Units go column block
+// by column block, token blocks fastest, so that pairs working at the same time share weight tiles in
+// L2.  Every wait is bounded.
 #include "linear_common.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int kStages = 4;
+constexpr int kStages = 6;
+constexpr int kScSlots = 7;                            // scale slots, and barriers of finished groups
+constexpr int kScAhead = 4;                            // groups that the scales are fetched ahead
 constexpr int kThreads = 640;
 constexpr int kFirstEpiWarp = 4;
 constexpr int kEpiWarps = 16;
-constexpr int kCols = kTileN / 4;                  // columns per epilogue thread (32 per half)
-constexpr int kHalf = kTileN / 2;
 // 640 threads launch with 96 registers each; warpgroup 0 keeps 32, the epilogue takes 112.
 constexpr int kRegsLaunch = 96, kRegsLow = 32, kRegsHigh = 112;
 static_assert(128 * kRegsLow + 512 * kRegsHigh == kThreads * kRegsLaunch, "register split");
 constexpr uint32_t kABytes = kTileM * kTileK;
-constexpr uint32_t kBBytes = kTileN * kTileK;
-constexpr uint32_t kWsBytes = kTileN * 4;
-constexpr uint32_t kSaBytes = kTileM * 4;
-constexpr uint32_t kScaleSlot = 2048;
-constexpr uint32_t kTmemCols = 2 * kTileN;
-constexpr int kStageCols = 8;                      // columns a warp stages at once when N is not a multiple of 8
+constexpr uint32_t kBBytes = kPairN / 2 * kTileK;
+constexpr uint32_t kStageBytes = kABytes + kBBytes;
+constexpr uint32_t kWsBytes = kPairN * 4;
+constexpr uint32_t kScSlot = kWsBytes + kTileM * 4;   // weight scales of the tile, then the rows' own
+constexpr uint32_t kTmemCols = 512;                   // two buffers of 192 columns
+constexpr uint32_t kBufCols = 256;
 
 struct L {
-    static constexpr uint32_t a = 0;
-    static constexpr uint32_t b = a + kStages * kABytes;
-    static constexpr uint32_t sc = b + kStages * kBBytes;
-    static constexpr uint32_t stage = sc + kStages * kScaleSlot;
-    static constexpr uint32_t full = stage + kEpiWarps * 32 * (kStageCols + 1) * 4;
-    static constexpr uint32_t empty = full + 8 * kStages;
-    static constexpr uint32_t tfull = empty + 8 * kStages;
-    static constexpr uint32_t tempty = tfull + 16;
-    static constexpr uint32_t drain = tempty + 16;
-    static constexpr uint32_t misc = drain + 8;    // tmem holder, abort flag
+    static constexpr uint32_t out = kStages * kStageBytes;
+    static constexpr uint32_t sc = out + kEpiWarps * kSubBytes;
+    static constexpr uint32_t bars = sc + kScSlots * kScSlot;
+    // full[kStages], empty[kStages], tfull[kScSlots], tempty[2], drain
+    static constexpr uint32_t nbars = 2 * kStages + kScSlots + 3;
+    static constexpr uint32_t misc = bars + nbars * 8;    // tmem holder, abort flag
     static constexpr uint32_t end = misc + 16;
 };
-static_assert(kWsBytes + kSaBytes <= kScaleSlot, "scale slot");
-constexpr uint32_t kSmemBytes = L::end + 1024;     // + slack to align the base to 1024 bytes
+static_assert(kStageBytes % 1024 == 0 && L::out % 128 == 0 && kScSlot % 16 == 0, "alignment");
+constexpr uint32_t kSmemBytes = L::end + 1024;         // + slack to align the base to 1024 bytes
 static_assert(kSmemBytes <= 232448, "shared memory");
 
+__device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
 // acc[a0 + j] += P[j] * (sa * ws[j]) for j < 16 (packed fp32x2; each lane rounds as scalars would).
-__device__ __forceinline__ void promote16(float2 (&acc)[kCols / 2], const uint32_t (&v)[16], uint32_t ws, int a0,
+__device__ __forceinline__ void promote16(float2 (&acc)[kSubCols / 2], const uint32_t (&v)[16], uint32_t ws, int a0,
                                           float2 sa2) {
 #pragma unroll
     for (int j = 0; j < 16; j += 4) {
@@ -65,23 +77,34 @@ __device__ __forceinline__ void promote16(float2 (&acc)[kCols / 2], const uint32
     }
 }
 
+// One arrival from lane 0 of the warp on a barrier of the cluster, predicated inside the asm.
+__device__ __forceinline__ void arrive_pair_lane0(uint32_t bar, int lane) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(
+            bar),
+        "r"(lane)
+        : "memory");
+}
+
 }  // namespace
 
 __global__ void __launch_bounds__(kThreads, 1)
-    k_linear_fp32(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const LinearArgs p) {
+    k_linear_fp32(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                  const __grid_constant__ CUtensorMap, const __grid_constant__ CUtensorMap tmY, const LinearArgs p) {
     extern __shared__ uint8_t smem_raw[];
-    const int mt = (p.T + kTileM - 1) / kTileM, nt = (p.N + kTileN - 1) / kTileN;
+    const int mt = (p.T + kPairM - 1) / kPairM, nt = (p.N + kPairN - 1) / kPairN;
     const int total_units = mt * nt;
     const int KB = p.K / kTileK;
-    const int n_pad = (p.N + kLinearPad - 1) / kLinearPad * kLinearPad;
+    const uint32_t rank = cluster_ctarank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     const uint32_t raw_addr = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::full);
-    uint64_t* empty = reinterpret_cast<uint64_t*>(smem + L::empty);
-    uint64_t* tfull = reinterpret_cast<uint64_t*>(smem + L::tfull);
-    uint64_t* tempty = reinterpret_cast<uint64_t*>(smem + L::tempty);
-    uint64_t* drain = reinterpret_cast<uint64_t*>(smem + L::drain);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bars);      // the even CTA's count for both
+    uint64_t* empty = full + kStages;                                  // one in each CTA
+    uint64_t* tfull = empty + kStages;                                 // in each CTA: a group's MMAs and scales
+    uint64_t* tempty = tfull + kScSlots;                               // the even CTA's
+    uint64_t* drain = tempty + 2;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::misc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::misc + 4);
 
@@ -89,21 +112,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1 + kEpiWarps);   // the MMA commit + one arrival per epilogue warp
+            mbar_init(&empty[s], 1);
         }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], kEpiWarps);
-        }
+        for (int s = 0; s < kScSlots; ++s) mbar_init(&tfull[s], 2);    // the MMA commit, and the scales' producer
+        for (int b = 0; b < 2; ++b) mbar_init(&tempty[b], 2 * kEpiWarps);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&tmA);
         prefetch_tmap(&tmB);
+        if (p.N % 8 == 0) prefetch_tmap(&tmY);
     }
-    if (warp == 1) tmem_alloc(tmem_holder, kTmemCols);
+    if (warp == 1) tmem_alloc2(tmem_holder, kTmemCols);
     tc_fence_before();
     __syncthreads();
+    cluster_sync_all();                                // both CTAs' barriers and TMEM are there
     tc_fence_after();
     pdl_wait_then_release();
     if (p.clear && blockIdx.x == 0 && threadIdx.x == 0) *p.status = MOE_OK;
@@ -116,37 +139,73 @@ __global__ void __launch_bounds__(kThreads, 1)
             // -------------------------------------------------------------- TMA producer
             uint32_t it = 0;
             bool ok = true;
-            for (int u = blockIdx.x; u < total_units && ok; u += gridDim.x) {
+            for (int u = pair; u < total_units && ok; u += pairs) {
                 const int nb = u / mt, mb = u - nb * mt;
-                const int row0 = mb * kTileM, brow0 = nb * kTileN;
-                const float* ws_src = static_cast<const float*>(p.w_scale) + brow0;
-                const float* sa_src = static_cast<const float*>(p.a_scale) + row0;
+                const int row0 = mb * kPairM + static_cast<int>(rank) * kTileM;
+                const int brow0 = nb * kPairN + static_cast<int>(rank) * (kPairN / 2);
                 for (int kb = 0; kb < KB; ++kb, ++it) {
                     const int s = it % kStages;
                     if (!mbar_wait<kProducerSleepNs>(&empty[s], ((it / kStages) & 1) ^ 1, abort_flag, p.status)) {
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&full[s], kABytes + kBBytes + kWsBytes + kSaBytes);
-                    tma_load_2d(smem + L::a + s * kABytes, &tmA, kb * kTileK, row0, &full[s]);
-                    tma_load_2d(smem + L::b + s * kBBytes, &tmB, kb * kTileK, brow0, &full[s]);
-                    bulk_load(smem + L::sc + s * kScaleSlot, ws_src + static_cast<size_t>(kb) * n_pad, kWsBytes, &full[s]);
-                    bulk_load(smem + L::sc + s * kScaleSlot + kWsBytes, sa_src + static_cast<size_t>(kb) * p.a_pad,
-                              kSaBytes, &full[s]);
+                    const uint32_t bar = pair_addr(smem_u32(&full[s]), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
+                    tma_load_2d_pair(smem + s * kStageBytes, &tmA, kb * kTileK, row0, bar);
+                    tma_load_2d_pair(smem + s * kStageBytes + kABytes, &tmB, kb * kTileK, brow0, bar);
                 }
             }
-            if (!ok) {   // let the copies already issued land before the CTA leaves
+            // after an abort: the copies already issued land (the even CTA's barriers count both CTAs')
+            // before either CTA passes the cluster barrier below
+            if (!ok && rank == 0) {
                 const uint32_t n = it < static_cast<uint32_t>(kStages) ? it : kStages;
                 for (uint32_t i = it - n; i < it; ++i) drain_wait(&full[i % kStages], (i / kStages) & 1);
             }
-        } else if (warp == 1 && lane == 0) {
-            // -------------------------------------------------------------- MMA issuer
-            const uint32_t idesc = f8_idesc(kTileM, kTileN);
-            const uint64_t a_desc0 = sw128_kmajor_desc(smem_u32(smem + L::a));
-            const uint64_t b_desc0 = sw128_kmajor_desc(smem_u32(smem + L::b));
-            uint32_t s = 0, ph = 0, buf = 0, bph = 0;
+        } else if (warp == 2 && lane == 0) {
+            // -------------------------------------------------------------- scales
+            // Group g's scales go to slot g % kScSlots and count on that slot's barrier.  The slot was last
+            // read for group g - kScSlots; the MMAs of group g - kScAhead are issued only when every
+            // epilogue warp has taken the partial of group g - kScAhead - 2 (two TMEM buffers), and so has
+            // finished group g - kScAhead - 3 = g - kScSlots.
+            static_assert(kScAhead + 3 == kScSlots, "a slot is read out before it is filled again");
+            const int n_pad = (p.N + kLinearPad - 1) / kLinearPad * kLinearPad;
+            uint32_t it = 0;
             bool ok = true;
-            for (int u = blockIdx.x; u < total_units && ok; u += gridDim.x) {
+            for (int u = pair; u < total_units && ok; u += pairs) {
+                const int nb = u / mt, mb = u - nb * mt;
+                const int row0 = mb * kPairM + static_cast<int>(rank) * kTileM;
+                // the scale rows reach 132 past T, the columns' scales to n_pad
+                const uint32_t w_bytes = static_cast<uint32_t>(min(kPairN, n_pad - nb * kPairN)) * 4u;
+                const uint32_t a_bytes = row0 < p.T ? kTileM * 4u : 0u;
+                const float* ws_src = static_cast<const float*>(p.w_scale) + nb * kPairN;
+                const float* sa_src = static_cast<const float*>(p.a_scale) + row0;
+                for (int kb = 0; kb < KB; ++kb, ++it) {
+                    if (it >= kScAhead) {
+                        const uint32_t g = it - kScAhead;
+                        if (!mbar_wait<kProducerSleepNs>(&tfull[g % kScSlots], (g / kScSlots) & 1, abort_flag, p.status)) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                    const int s = it % kScSlots;
+                    uint8_t* slot = smem + L::sc + s * kScSlot;
+                    mbar_arrive_expect_tx(&tfull[s], w_bytes + a_bytes);
+                    bulk_load(slot, ws_src + static_cast<size_t>(kb) * n_pad, w_bytes, &tfull[s]);
+                    if (a_bytes) bulk_load(slot + kWsBytes, sa_src + static_cast<size_t>(kb) * p.a_pad, a_bytes, &tfull[s]);
+                }
+            }
+            if (!ok) {   // let the copies already issued land: their groups' barriers may never complete
+                const unsigned long long t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+            }
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            // -------------------------------------------------------------- MMA issuer, for the pair
+            const uint32_t idesc = f8_idesc(kPairM, kPairN);
+            const uint64_t a_desc0 = sw128_kmajor_desc(smem_u32(smem));
+            const uint64_t b_desc0 = sw128_kmajor_desc(smem_u32(smem + kABytes));
+            uint32_t s = 0, ph = 0, buf = 0, bph = 0, slot = 0;
+            bool ok = true;
+            for (int u = pair; u < total_units && ok; u += pairs) {
                 for (int kb = 0; kb < KB; ++kb) {
                     if (!mbar_wait<kIssuerSleepNs>(&full[s], ph, abort_flag, p.status) ||
                         !mbar_wait<kIssuerSleepNs>(&tempty[buf], bph ^ 1, abort_flag, p.status)) {
@@ -154,146 +213,137 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t ad = a_desc0 + s * (kABytes >> 4), bd = b_desc0 + s * (kBBytes >> 4);
-                    const uint32_t d = tmem_base + buf * static_cast<uint32_t>(kTileN);
+                    const uint64_t ad = a_desc0 + s * (kStageBytes >> 4), bd = b_desc0 + s * (kStageBytes >> 4);
+                    const uint32_t d = tmem_base + buf * kBufCols;
 #pragma unroll
-                    for (int m = 0; m < MPG; ++m) mma_f8(d, ad + 2 * m, bd + 2 * m, idesc, m > 0 ? 1u : 0u);
-                    mma_commit(&tfull[buf]);
-                    mma_commit(&empty[s]);
+                    for (int m = 0; m < MPG; ++m) mma_f8_pair(d, ad + 2 * m, bd + 2 * m, idesc, m > 0 ? 1u : 0u);
+                    mma_commit2(&tfull[slot]);
+                    mma_commit2(&empty[s]);
                     if (++s == kStages) {
                         s = 0;
                         ph ^= 1;
                     }
+                    if (++slot == kScSlots) slot = 0;
                     buf ^= 1;
-                    bph ^= buf ^ 1;
+                    bph ^= buf ^ 1;                    // flips after both buffers were used
                 }
             }
-            mma_commit(drain);
+            mma_commit2_own(drain);
             drain_wait(drain, 0);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
         // ------------------------------------------------------------------ epilogue
-        const int quad = warp & 3;                 // TMEM lanes 32*quad .. 32*quad+31
+        const int quad = warp & 3;                     // TMEM lanes 32*quad .. 32*quad+31
         const int qtr = (warp - kFirstEpiWarp) >> 2;
         const int row_in_tile = quad * 32 + lane;
-        const uint32_t t_warp = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(32 * qtr);
-        const uint32_t ws0 = smem_u32(smem + L::sc) + static_cast<uint32_t>(32 * qtr * 4);
+        const uint32_t t_warp = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(kSubCols * qtr);
+        const uint32_t ws0 = smem_u32(smem + L::sc) + static_cast<uint32_t>(kSubCols * qtr * 4);
         const uint32_t sa0 = smem_u32(smem + L::sc + kWsBytes) + static_cast<uint32_t>(row_in_tile * 4);
-        const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
-        const uint32_t tfull0 = smem_u32(tfull), tempty0 = smem_u32(tempty);
+        const uint32_t sub = smem_u32(smem + L::out) + static_cast<uint32_t>(warp - kFirstEpiWarp) * kSubBytes;
+        const uint32_t tfull0 = smem_u32(tfull), tempty0 = pair_addr(smem_u32(tempty), 0);
         const uint32_t abort_at = smem_u32(smem + L::misc + 4);
-        uint32_t s = 0, ph = 0, buf = 0, bph = 0;
+        uint32_t s = 0, ph = 0, buf = 0;
         bool ok = true;
-        for (int u = blockIdx.x; u < total_units && ok; u += gridDim.x) {
-            float2 acc2[kCols / 2];
+        for (int u = pair; u < total_units && ok; u += pairs) {
+            {
+                const int nb = u / mt, mb = u - nb * mt;
+                epilogue_store_wait();                 // the last tile's store has read the subtile
+                epilogue_residual<1>(p, sub, mb * kPairM + static_cast<int>(rank) * kTileM + quad * 32,
+                                     nb * kPairN + kSubCols * qtr);
+            }
+            float2 acc2[kSubCols / 2];
 #pragma unroll
-            for (int i = 0; i < kCols / 2; ++i) acc2[i] = make_float2(0.0f, 0.0f);
-            float* acc = reinterpret_cast<float*>(acc2);
+            for (int i = 0; i < kSubCols / 2; ++i) acc2[i] = make_float2(0.0f, 0.0f);
             for (int kb = 0; kb < KB; ++kb) {
-                if (!mbar_wait_at(full0 + 8 * s, ph, abort_at, p.status) ||
-                    !mbar_wait_at(tfull0 + 8 * buf, bph, abort_at, p.status)) {
+                if (!mbar_wait_at(tfull0 + 8 * s, ph, abort_at, p.status)) {   // the partial and its scales
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t so = s * kScaleSlot;
-                const float sa = ld_shared_f32(sa0 + so);
-                const float2 sa2 = make_float2(sa, sa);
-                const uint32_t ws = ws0 + so;
-                const uint32_t taddr = t_warp + buf * static_cast<uint32_t>(kTileN);
-                uint32_t va[16], vb[16];
+                const uint32_t taddr = t_warp + buf * kBufCols;
+                uint32_t va[16], vb[16], vc[16];
                 MOE_TMEM_LD16(taddr, va);
-                MOE_TMEM_WAIT_LD16(va);
                 MOE_TMEM_LD16(taddr + 16, vb);
-                promote16(acc2, va, ws, 0, sa2);
-                MOE_TMEM_WAIT_LD16(vb);
-                MOE_TMEM_LD16(taddr + kHalf, va);
-                promote16(acc2, vb, ws + 64, 16, sa2);
+                MOE_TMEM_LD16(taddr + 32, vc);
+                const float sa = ld_shared_f32(sa0 + s * kScSlot);
+                const float2 sa2 = make_float2(sa, sa);
+                const uint32_t ws = ws0 + s * kScSlot;
                 MOE_TMEM_WAIT_LD16(va);
-                MOE_TMEM_LD16(taddr + kHalf + 16, vb);
-                promote16(acc2, va, ws + 4 * kHalf, 32, sa2);
                 MOE_TMEM_WAIT_LD16(vb);
+                MOE_TMEM_WAIT_LD16(vc);
+                // the warp holds its whole partial: hand the buffer back
                 tc_fence_before();
-                mbar_arrive_lane0(tempty0 + 8 * buf, lane);
-                promote16(acc2, vb, ws + 4 * kHalf + 64, 48, sa2);
-                // the scales were read through the generic proxy; the next bulk copy into this
-                // stage is an async-proxy write: order the reads before it
+                arrive_pair_lane0(tempty0 + 8 * buf, lane);
+                promote16(acc2, va, ws, 0, sa2);
+                promote16(acc2, vb, ws + 64, 16, sa2);
+                promote16(acc2, vc, ws + 128, 32, sa2);
+                // the scales were read through the generic proxy; the next bulk copy into this slot is an
+                // async-proxy write: order the reads before it (the next group's arrival carries that on)
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                mbar_arrive_lane0(empty0 + 8 * s, lane);
-                if (++s == kStages) {
+                if (++s == kScSlots) {
                     s = 0;
                     ph ^= 1;
                 }
                 buf ^= 1;
-                bph ^= buf ^ 1;
             }
-            if (!ok) break;
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
             const int nb = u / mt, mb = u - nb * mt;
-            const int t = mb * kTileM + row_in_tile;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int c0 = nb * kTileN + h * kHalf + qtr * 32;
-                if (c0 >= p.N) continue;
-                if (p.N % 8 == 0) {
-                    if (t < p.T) linear_store32(p, acc + 32 * h, t, c0);
-                } else {
-                    float* stage = reinterpret_cast<float*>(smem + L::stage) + (warp - kFirstEpiWarp) * 32 * (kStageCols + 1);
-#pragma unroll
-                    for (int c = 0; c < 32; c += kStageCols)
-                        linear_store_any<kStageCols>(p, stage, acc + 32 * h + c, mb * kTileM + quad * 32, c0 + c);
-                }
-            }
+            const int t0 = mb * kPairM + static_cast<int>(rank) * kTileM + quad * 32, c0 = nb * kPairN + kSubCols * qtr;
+            epilogue_residual_wait(p);
+            epilogue_chunks<6>(p, sub, reinterpret_cast<float*>(acc2), c0, 0);
+            epilogue_store<1>(p, &tmY, sub, t0, c0);
         }
+        epilogue_drain();
     }
 
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
+    cluster_sync_all();                                // neither CTA leaves while the other's MMAs or arrivals need it
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc(tmem_base, kTmemCols);
+        tmem_dealloc2(tmem_base, kTmemCols);
     }
 }
 
-cudaError_t launch_linear_fp32(const LinearArgs& a, const CUtensorMap& tmX, const CUtensorMap& tmW, int num_sms,
-                               cudaStream_t s) {
+cudaError_t launch_linear_fp32(const LinearArgs& a, const LinearMaps& m, int num_sms, cudaStream_t s) {
     // The register split above must fit what the block is launched with, or setmaxnreg.inc would
     // wait forever: refuse to launch otherwise.
     cudaFuncAttributes fa;
-    cudaError_t e = cudaFuncGetAttributes(&fa, k_linear_fp32);
+    const cudaError_t e = cudaFuncGetAttributes(&fa, k_linear_fp32);
     if (e != cudaSuccess) return e;
     if (fa.numRegs * kThreads < kRegsLow * 128 + kRegsHigh * 512) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(k_linear_fp32, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
-    if (e != cudaSuccess) return e;
-    return launch_pdl(k_linear_fp32, dim3(num_sms), dim3(kThreads), kSmemBytes, s, tmX, tmW, a);
+    return launch_pair(k_linear_fp32, kThreads, kSmemBytes, a, m, num_sms, s);
 }
 
-// The narrow kernel takes a product when its estimated time is below the wide kernel's: both are
-// (rounds of CTAs over the SMs) x (K groups of a CTA) x (time of a group).
+// The narrow kernel takes a product when its estimated time is below the pair kernel's: both are
+// (rounds of CTAs over the SMs) x (K groups of a CTA) x (cycles of a group).
 bool linear_is_narrow(int T, int N, int K, int recipe, int num_sms) {
     const long long KB = K / kTileK;
     const int nt = linear_narrow_tokens(T), split = linear_narrow_split(T, N, K, num_sms);
     const long long tiles = static_cast<long long>((N + kTileM - 1) / kTileM) * ((T + nt - 1) / nt);
     if ((T + nt - 1) / nt > 65535) return false;       // grid.z
-    const int wn = recipe == 0 ? kTileN : 128;
-    const long long units = static_cast<long long>((N + wn - 1) / wn) * ((T + kTileM - 1) / kTileM);
+    const long long units = static_cast<long long>((N + kPairN - 1) / kPairN) * ((T + kPairM - 1) / kPairM);
+    const long long pairs = num_sms / 2;
     const long long narrow = (tiles * split + num_sms - 1) / num_sms * ((KB + split - 1) / split) * 700;
-    const long long wide = (units + num_sms - 1) / num_sms * KB * (recipe == 0 ? 1550 : 700);
+    const long long wide = (units + pairs - 1) / pairs * KB * (recipe == 0 ? 900 : 700);
     return narrow < wide;
 }
 
-uint32_t linear_token_box(const LinearArgs& a, int num_sms) {
-    return linear_is_narrow(a.T, a.N, a.K, a.recipe, num_sms) ? linear_narrow_tokens(a.T) : kTileM;
-}
-uint32_t linear_weight_box(const LinearArgs& a, int num_sms) {
-    return a.recipe != 0 || linear_is_narrow(a.T, a.N, a.K, a.recipe, num_sms) ? 128 : kTileN;
+LinearBoxes linear_boxes(const LinearArgs& a, int num_sms) {
+    if (linear_is_narrow(a.T, a.N, a.K, a.recipe, num_sms))
+        return {static_cast<uint32_t>(linear_narrow_tokens(a.T)), kTileM, false};
+    return {kTileM, kPairN / 2, true};
 }
 
-cudaError_t launch_linear(const LinearArgs& a, const CUtensorMap& tmX, const CUtensorMap& tmW, int num_sms,
-                          cudaStream_t s) {
-    if (linear_is_narrow(a.T, a.N, a.K, a.recipe, num_sms)) return launch_linear_narrow(a, tmX, tmW, num_sms, s);
-    return a.recipe == 0 ? launch_linear_fp32(a, tmX, tmW, num_sms, s) : launch_linear_mx(a, tmX, tmW, num_sms, s);
+cudaError_t launch_linear(const LinearArgs& a, const LinearMaps& m, int num_sms, cudaStream_t s) {
+    if (linear_is_narrow(a.T, a.N, a.K, a.recipe, num_sms)) return launch_linear_narrow(a, m, num_sms, s);
+    return a.recipe == 0 ? launch_linear_fp32(a, m, num_sms, s) : launch_linear_mx(a, m, num_sms, s);
 }
 
 // ------------------------------------------------------------------------------------------

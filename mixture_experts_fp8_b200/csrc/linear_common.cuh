@@ -10,20 +10,27 @@ namespace moe {
 // cfg.activation: 0 none, 1 relu, 2 silu, 3 gelu (erf), 4 gelu (tanh form).  The two with a logistic
 // take the hardware exponential and reciprocal (a few fp32 ulps, far below the bf16 rounding that
 // follows); NaN stays NaN in every one.
+template <int ACT>
+__device__ __forceinline__ float linear_act_t(float v) {
+    if (ACT == 1) return v < 0.0f ? 0.0f : v;
+    if (ACT == 2) return silu(v);
+    if (ACT == 3) return 0.5f * v * (1.0f + erff(v * 0.70710678f));
+    if (ACT == 4) {   // 0.5 (1 + tanh u) = 1 / (1 + e^-2u),  u = sqrt(2/pi) (v + 0.044715 v^3)
+        const float u2 = 1.5957691f * fmaf(0.044715f * v * v, v, v);
+        return __fdividef(v, 1.0f + __expf(-u2));
+    }
+    return v;
+}
+
 __device__ __forceinline__ float linear_act(float v, int act) {
     switch (act) {
-        case 1: return v < 0.0f ? 0.0f : v;
-        case 2: return silu(v);
-        case 3: return 0.5f * v * (1.0f + erff(v * 0.70710678f));
-        case 4: {   // 0.5 (1 + tanh u) = 1 / (1 + e^-2u),  u = sqrt(2/pi) (v + 0.044715 v^3)
-            const float u2 = 1.5957691f * fmaf(0.044715f * v * v, v, v);
-            return __fdividef(v, 1.0f + __expf(-u2));
-        }
+        case 1: return linear_act_t<1>(v);
+        case 2: return linear_act_t<2>(v);
+        case 3: return linear_act_t<3>(v);
+        case 4: return linear_act_t<4>(v);
         default: return v;
     }
 }
-
-__device__ __forceinline__ void add_bf16x8(float* v, uint4 w) { add_bias8(v, w); }
 
 __device__ __forceinline__ uint4 pack_bf16x8(const float* v) {
     uint32_t w[4];
@@ -35,45 +42,230 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float* v) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The lane's row t, columns c0 .. c0+31 from acc, when N is a multiple of 8 (16-byte rows).
-__device__ __forceinline__ void linear_store32(const LinearArgs& p, float* acc, int t, int c0) {
-    const size_t at = static_cast<size_t>(t) * p.N + c0;
+// ---- A warp's output goes through shared memory of its own, in subtiles of 32 rows x 48 columns
+// bf16 (rows of 96 bytes, as a TMA box without swizzle lays them out; a quarter warp's 16-byte accesses
+// meet two at a time): the residual is fetched into it while the sums are still being made, each lane
+// replaces its row's residual by the result, and the subtile leaves by a TMA store (N a multiple of 8)
+// or by coalesced stores (any N).
+constexpr int kSubCols = 48;
+constexpr uint32_t kSubRow = kSubCols * 2;
+constexpr uint32_t kSubBytes = 32 * kSubRow;
+
+__device__ __forceinline__ uint4 lds_u4(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts_u4(uint32_t a, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_u32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts_u32(uint32_t a, uint32_t v) {
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
+// Fetch the residual of rows t0 .. +31, columns c0 .. c0 + 48 SUBS - 1 into the warp's subtiles at sub.
+// N a multiple of 8: asynchronous, 16 bytes a lane (epilogue_residual_wait before use).
+template <int SUBS>
+__device__ __forceinline__ void epilogue_residual(const LinearArgs& p, uint32_t sub, int t0, int c0) {
+    if (!p.res) return;
+    const int lane = threadIdx.x & 31;
+    if (p.N % 8 == 0) {
+        const int t = t0 + lane;
+        if (t < p.T) {
+            const __nv_bfloat16* row = p.res + static_cast<size_t>(t) * p.N;
 #pragma unroll
-    for (int c = 0; c < 32; c += 8) {
-        if (c0 + c < p.N) {
-            float* v = acc + c;
-            if (p.bias) add_bias8(v, ld_nc_u4(reinterpret_cast<const uint4*>(p.bias + c0 + c)));
-            if (p.act) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = linear_act(v[i], p.act);
+            for (int j = 0; j < 6 * SUBS; ++j) {
+                const int c = c0 + 8 * j;
+                if (c < p.N)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(
+                                     sub + (j / 6) * kSubBytes + lane * kSubRow + (j % 6) * 16),
+                                 "l"(row + c)
+                                 : "memory");
             }
-            // y may be the residual buffer itself: a plain load, by the thread that then stores
-            if (p.res) add_bias8(v, *reinterpret_cast<const uint4*>(p.res + at + c));
-            *reinterpret_cast<uint4*>(p.y + at + c) = pack_bf16x8(v);
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        return;
+    }
+    constexpr int kWords = 24 * SUBS;                   // of a row
+    const bool even = p.N % 2 == 0;
+#pragma unroll 8
+    for (int i = lane; i < 32 * kWords; i += 32) {
+        const int r = i / kWords, w = i % kWords, t = t0 + r, c = c0 + 2 * w;
+        if (t >= p.T || c >= p.N) continue;
+        const __nv_bfloat16* q = p.res + static_cast<size_t>(t) * p.N + c;
+        uint32_t v;
+        if (even) {
+            v = *reinterpret_cast<const uint32_t*>(q);
+        } else {
+            const uint16_t lo = *reinterpret_cast<const uint16_t*>(q);
+            const uint16_t hi = c + 1 < p.N ? *reinterpret_cast<const uint16_t*>(q + 1) : uint16_t(0);
+            v = lo | (static_cast<uint32_t>(hi) << 16);
+        }
+        sts_u32(sub + (w / 24) * kSubBytes + r * kSubRow + (w % 24) * 4, v);
+    }
+}
+__device__ __forceinline__ void epilogue_residual_wait(const LinearArgs& p) {
+    if (p.res && p.N % 8 == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();
+}
+
+// Columns c0 .. c0 + 8 CH - 1 of the lane's row, chunk j0 of the subtile on, from acc.
+template <int ACT, int CH>
+__device__ __forceinline__ void epilogue_chunks_t(const LinearArgs& p, uint32_t sub, float* acc, int c0, int j0) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+        float* v = acc + 8 * j;
+        const int c = c0 + 8 * j;
+        if (p.bias) {
+            if (c + 8 <= p.N) {
+                add_bias8(v, ld_nc_u4(reinterpret_cast<const uint4*>(p.bias + c)));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (c + i < p.N) v[i] += __bfloat162float(p.bias[c + i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = linear_act_t<ACT>(v[i]);
+        const uint32_t at = sub + lane * kSubRow + (j0 + j) * 16;
+        if (p.res) add_bias8(v, lds_u4(at));
+        sts_u4(at, pack_bf16x8(v));
+    }
+}
+template <int CH>
+__device__ __forceinline__ void epilogue_chunks(const LinearArgs& p, uint32_t sub, float* acc, int c0, int j0) {
+    switch (p.act) {
+        case 1: return epilogue_chunks_t<1, CH>(p, sub, acc, c0, j0);
+        case 2: return epilogue_chunks_t<2, CH>(p, sub, acc, c0, j0);
+        case 3: return epilogue_chunks_t<3, CH>(p, sub, acc, c0, j0);
+        case 4: return epilogue_chunks_t<4, CH>(p, sub, acc, c0, j0);
+        default: return epilogue_chunks_t<0, CH>(p, sub, acc, c0, j0);
     }
 }
 
-// Any N: a warp's 32 rows x CW columns through shared memory (stage: 32 x (CW + 1) floats of the
-// warp's own), stored by columns so that a warp writes runs of a row.  Every lane takes part.
-template <int CW>
-__device__ __forceinline__ void linear_store_any(const LinearArgs& p, float* stage, const float* acc, int t0, int c0) {
+// Store the warp's SUBS subtiles (rows t0 .., columns c0 ..) to y.  tmY: y [T, N] bf16, box 48 x 32; used
+// when N is a multiple of 8, and then asynchronous (epilogue_store_wait).
+template <int SUBS>
+__device__ __forceinline__ void epilogue_store(const LinearArgs& p, const CUtensorMap* tmY, uint32_t sub, int t0, int c0) {
     const int lane = threadIdx.x & 31;
-    __syncwarp();
+    if (p.N % 8 == 0) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0 && t0 < p.T) {
 #pragma unroll
-    for (int j = 0; j < CW; ++j) stage[lane * (CW + 1) + j] = acc[j];
+            for (int k = 0; k < SUBS; ++k)
+                if (c0 + kSubCols * k < p.N)
+                    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                                     reinterpret_cast<uint64_t>(tmY)),
+                                 "r"(sub + k * kSubBytes), "r"(c0 + kSubCols * k), "r"(t0)
+                                 : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+        return;
+    }
     __syncwarp();
-    for (int i = lane; i < 32 * CW; i += 32) {
-        const int t = t0 + i / CW, c = c0 + i % CW;
-        if (t < p.T && c < p.N) {
-            float v = stage[(i / CW) * (CW + 1) + i % CW];
-            if (p.bias) v += __bfloat162float(p.bias[c]);
-            v = linear_act(v, p.act);
-            const size_t at = static_cast<size_t>(t) * p.N + c;
-            if (p.res) v += __bfloat162float(p.res[at]);
-            p.y[at] = __float2bfloat16_rn(v);
+    constexpr int kWords = 24 * SUBS;
+    const bool even = p.N % 2 == 0;
+#pragma unroll 8
+    for (int i = lane; i < 32 * kWords; i += 32) {
+        const int r = i / kWords, w = i % kWords, t = t0 + r, c = c0 + 2 * w;
+        const uint32_t v = lds_u32(sub + (w / 24) * kSubBytes + r * kSubRow + (w % 24) * 4);
+        if (t >= p.T || c >= p.N) continue;
+        __nv_bfloat16* q = p.y + static_cast<size_t>(t) * p.N + c;
+        if (even) {
+            *reinterpret_cast<uint32_t*>(q) = v;
+        } else {
+            *reinterpret_cast<uint16_t*>(q) = static_cast<uint16_t>(v);
+            if (c + 1 < p.N) *reinterpret_cast<uint16_t*>(q + 1) = static_cast<uint16_t>(v >> 16);
         }
     }
+    __syncwarp();
+}
+// Before the subtiles are written again: the stores have read them.
+__device__ __forceinline__ void epilogue_store_wait() {
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+}
+// Before the warp leaves.
+__device__ __forceinline__ void epilogue_drain() {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+// ---- CTA pairs (cta_group::2): the even CTA issues the MMAs of both
+__device__ __forceinline__ void tmem_alloc2(uint32_t* holder_smem, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(holder_smem)),
+                 "r"(ncols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// Arrive on the barrier at this offset in both CTAs once the MMAs issued so far have finished.
+__device__ __forceinline__ void mma_commit2(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     smem_u32(bar)),
+                 "h"(static_cast<uint16_t>(3)) : "memory");
+}
+// The same on this CTA's barrier alone.
+__device__ __forceinline__ void mma_commit2_own(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t pair_addr(uint32_t smem_addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr), "r"(rank));
+    return r;
+}
+// A load into this CTA that counts on a barrier of the even CTA (bar: its cluster address).
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+// Arrive on a barrier of either CTA of the pair, for what fences of their own order: an accumulator read
+// out (tcgen05.fence), shared memory written for the other CTA's tcgen05 operations (fence.proxy.async).
+// (A release at cluster scope here waits out the thread's loads in flight: about 1200 cycles.)
+__device__ __forceinline__ void arrive_pair(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Tiles of the pair kernels: 256 tokens x 192 columns.
+constexpr int kPairM = 2 * kTileM;
+constexpr int kPairN = 192;
+
+// Launch a pair kernel: one CTA an SM, clusters of two.
+template <typename K>
+inline cudaError_t launch_pair(K kernel, int threads, uint32_t smem, const LinearArgs& a, const LinearMaps& m,
+                               int num_sms, cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(num_sms / 2 * 2);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, m.x, m.w, m.sf, m.y, a);
 }
 
 }  // namespace moe

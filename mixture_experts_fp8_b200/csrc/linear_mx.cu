@@ -3,59 +3,86 @@
 // scale per 32 K-elements.  tcgen05.mma.kind::mxf8f6f4.block_scale applies 2^(ex + ew) to every
 // 32-deep block itself and accumulates the whole K in TMEM, so nothing is promoted.
 //
-// Tiles of 128 tokens x 128 columns, persistent, two TMEM accumulators so that a tile's epilogue
-// overlaps the next tile's MMAs.  Warp 0 loads by TMA, warp 1 issues, warp 2 builds the tokens'
-// scale-factor atoms (word 4i + c of an atom = the four scale bytes of tile row 32c + i), warps 4-11
-// are the epilogue.  Every wait is bounded.
+// CTA pairs (cta_group::2), persistent: a tile is 256 tokens x 192 columns, each CTA of the pair
+// holding 128 token rows and half of the weight rows, so that an SM loads 28 KB for 128 x 192 x 128
+// products.  With 128 x 128 tiles of one CTA the same loop was bound by the loads in flight: 33 KB a
+// stage, 5 stages, 735 cycles a stage where the MMAs take 256.  N = 192 leaves TMEM for two
+// accumulators (384 columns) beside the scale factors (12 columns a stage), so that a tile's epilogue
+// overlaps the next tile's MMAs.
+//
+// Scale factors: a CTA's SFA are its own rows', SFB the whole tile's in both CTAs; word 4i + c of a
+// 512-byte atom = the four scale bytes of row 32c + i.  A tile's columns start in the middle of a
+// weight atom when its index is odd: SFB then starts two TMEM columns in.
+//
+// Threads (384): warp 0 TMA producer, warp 1 MMA issuer (the even CTA's, for both), warp 2 the tokens'
+// scale atoms, warp 3 idle, warps 4-11 epilogue (TMEM lanes 32 (w % 4).., 96 of the columns each).
+// Units go column block by column block, token blocks fastest.  Every wait is bounded.
 #include "linear_common.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int kXStages = 5;
+constexpr int kXStages = 6;
 constexpr int kXThreads = 384;
 constexpr int kXEpiWarps = 8;
-constexpr int kXN = 128;
+constexpr int kXN = kPairN, kXM = kPairM;
+constexpr int kXSubs = kXN / 2 / kSubCols;        // subtiles of an epilogue warp
 constexpr uint32_t kXA = kTileM * kTileK;         // 16 KB
-constexpr uint32_t kXB = kXN * kTileK;            // 16 KB
+constexpr uint32_t kXB = kXN / 2 * kTileK;        // 12 KB
 constexpr uint32_t kXSf = 512;
-constexpr uint32_t kXStage = kXA + kXB + 2 * kXSf + 1024;   // [A | B | SFA | SFB | pad]
+constexpr uint32_t kXStage = kXA + kXB;
+constexpr uint32_t kXSfStage = 3 * kXSf;          // [SFA | SFB two atoms]
 constexpr uint32_t kXSfCol0 = 2 * kXN;            // scale factors after the two accumulators
 constexpr uint32_t kXTmemCols = 512;
-constexpr int kXStageCols = 16;
-static_assert(kXSfCol0 + kXStages * 8 <= kXTmemCols, "TMEM");
+static_assert(kXSfCol0 + kXStages * 12 <= kXTmemCols, "TMEM");
+static_assert(kXStage % 1024 == 0 && kXA % 1024 == 0, "stage alignment");
 
 struct XL {
     static constexpr uint32_t b = kXA;
-    static constexpr uint32_t sfa = kXA + kXB;
-    static constexpr uint32_t sfb = sfa + kXSf;
-    static constexpr uint32_t stage = kXStages * kXStage;
-    static constexpr uint32_t bars = stage + kXEpiWarps * 32 * (kXStageCols + 1) * 4;
+    static constexpr uint32_t out = kXStages * kXStage;                       // the epilogue's subtiles
+    static constexpr uint32_t sf = out + kXEpiWarps * kXSubs * kSubBytes;
+    static constexpr uint32_t bars = sf + kXStages * kXSfStage;
     static constexpr uint32_t nbars = 3 * kXStages + 5;   // full, sfready, empty, tfull[2], tempty[2], drain
     static constexpr uint32_t misc = bars + nbars * 8;
     static constexpr uint32_t end = misc + 16;
 };
-static_assert(kXStage % 1024 == 0, "stage alignment");
+static_assert(XL::out % 1024 == 0, "subtile alignment");
 constexpr uint32_t kXSmemBytes = XL::end + 1024;
 static_assert(kXSmemBytes <= 232448, "shared memory");
+
+__device__ __forceinline__ void mma_mx2(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void sf_copy2(uint32_t tmem_col_addr, uint64_t sdesc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem_col_addr), "l"(sdesc) : "memory");
+}
 
 }  // namespace
 
 __global__ void __launch_bounds__(kXThreads, 1)
-    k_linear_mx(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const LinearArgs p) {
+    k_linear_mx(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                const __grid_constant__ CUtensorMap tmSf, const __grid_constant__ CUtensorMap tmY, const LinearArgs p) {
     extern __shared__ uint8_t smem_raw[];
-    const int mt = (p.T + kTileM - 1) / kTileM, nt = (p.N + kXN - 1) / kXN;
+    const int mt = (p.T + kXM - 1) / kXM, nt = (p.N + kXN - 1) / kXN;
     const int total_units = mt * nt;
     const int KB = p.K / kTileK;
+    const uint32_t rank = cluster_ctarank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
+    // the same offsets in both CTAs: the dynamic shared memory starts at one address in every CTA
     const uint32_t raw_addr = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + XL::bars);
-    uint64_t* sfready = full + kXStages;
-    uint64_t* empty = sfready + kXStages;
-    uint64_t* tfull = empty + kXStages;
-    uint64_t* tempty = tfull + 2;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + XL::bars);     // the even CTA's count for both
+    uint64_t* sfready = full + kXStages;                               // likewise
+    uint64_t* empty = sfready + kXStages;                              // one in each CTA
+    uint64_t* tfull = empty + kXStages;                                // one in each CTA
+    uint64_t* tempty = tfull + 2;                                      // the even CTA's
     uint64_t* drain = tempty + 2;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + XL::misc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + XL::misc + 4);
@@ -64,22 +91,25 @@ __global__ void __launch_bounds__(kXThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kXStages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&sfready[s], 1);
+            mbar_init(&sfready[s], 2);
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], kXEpiWarps);
+            mbar_init(&tempty[b], 2 * kXEpiWarps);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&tmA);
         prefetch_tmap(&tmB);
+        prefetch_tmap(&tmSf);
+        if (p.N % 8 == 0) prefetch_tmap(&tmY);
     }
-    if (warp == 1) tmem_alloc(tmem_holder, kXTmemCols);
+    if (warp == 1) tmem_alloc2(tmem_holder, kXTmemCols);
     tc_fence_before();
     __syncthreads();
+    cluster_sync_all();                                // both CTAs' barriers and TMEM are there
     tc_fence_after();
     pdl_wait_then_release();
     if (p.clear && blockIdx.x == 0 && threadIdx.x == 0) *p.status = MOE_OK;
@@ -91,9 +121,10 @@ __global__ void __launch_bounds__(kXThreads, 1)
             const uint32_t b_bytes = p.recipe == 2 ? kXB / 2 : kXB;   // E2M1 weights arrive packed
             uint32_t it = 0;
             bool ok = true;
-            for (int u = blockIdx.x; u < total_units && ok; u += gridDim.x) {
+            for (int u = pair; u < total_units && ok; u += pairs) {
                 const int nb = u / mt, mb = u - nb * mt;
-                const uint8_t* sfb_src = static_cast<const uint8_t*>(p.w_scale) + static_cast<size_t>(nb) * KB * kXSf;
+                const int row0 = mb * kXM + static_cast<int>(rank) * kTileM;
+                const int brow0 = nb * kXN + static_cast<int>(rank) * (kXN / 2);
                 for (int kb = 0; kb < KB; ++kb, ++it) {
                     const int s = it % kXStages;
                     if (!mbar_wait<kProducerSleepNs>(&empty[s], ((it / kXStages) & 1) ^ 1, abort_flag, p.status)) {
@@ -101,54 +132,82 @@ __global__ void __launch_bounds__(kXThreads, 1)
                         break;
                     }
                     uint8_t* st = smem + s * kXStage;
-                    mbar_arrive_expect_tx(&full[s], kXA + b_bytes + kXSf);
-                    tma_load_2d(st, &tmA, kb * kTileK, mb * kTileM, &full[s]);
-                    tma_load_2d(st + XL::b, &tmB, kb * kTileK, nb * kXN, &full[s]);
-                    bulk_load(st + XL::sfb, sfb_src + static_cast<size_t>(kb) * kXSf, kXSf, &full[s]);
+                    const uint32_t bar = pair_addr(smem_u32(&full[s]), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (kXA + b_bytes + 2 * kXSf));
+                    tma_load_2d_pair(st, &tmA, kb * kTileK, row0, bar);
+                    tma_load_2d_pair(st + XL::b, &tmB, kb * kTileK, brow0, bar);
+                    tma_load_3d_pair(smem + XL::sf + s * kXSfStage + kXSf, &tmSf, 0, kb, nb * kXN / 128, bar);
                 }
             }
-            if (!ok) {
+            // after an abort: the copies already issued land (the even CTA's barriers count both CTAs')
+            // before either CTA passes the cluster barrier below
+            if (!ok && rank == 0) {
                 const uint32_t n = it < static_cast<uint32_t>(kXStages) ? it : kXStages;
                 for (uint32_t i = it - n; i < it; ++i) drain_wait(&full[i % kXStages], (i / kXStages) & 1);
             }
         }
     } else if (warp == 2) {
         // ---------------------------------------------------------------------- token-scale atoms
-        // lane i writes the atom's row i: the scale words of tile rows i, 32+i, 64+i, 96+i (the
-        // scale rows reach 132 past T, so a ragged tile reads words that no stored row uses)
-        uint32_t it = 0;
-        bool ok = true;
-        for (int u = blockIdx.x; u < total_units && ok; u += gridDim.x) {
-            const uint32_t* src = static_cast<const uint32_t*>(p.a_scale) + static_cast<size_t>(u % mt) * kTileM + lane;
-            uint4 next = make_uint4(__ldg(src), __ldg(src + 32), __ldg(src + 64), __ldg(src + 96));
-            for (int kb = 0; kb < KB; ++kb, ++it) {
-                const uint4 w = next;
-                if (kb + 1 < KB) {
-                    src += p.a_pad;
-                    next = make_uint4(__ldg(src), __ldg(src + 32), __ldg(src + 64), __ldg(src + 96));
+        // lane i writes the atom's row i: the scale words of tile rows i, 32+i, 64+i, 96+i (rows past T:
+        // zero).  The words are fetched kSfAhead stages ahead of the stage being written (a register
+        // ring), so that a load's latency is not paid per stage.
+        constexpr int kSfAhead = 4;
+        const int my_units = total_units > pair ? (total_units - 1 - pair) / pairs + 1 : 0;
+        const long long n_stages = static_cast<long long>(my_units) * KB;
+        int gu = pair, gkb = 0;                        // the fetch's own position
+        auto fetch = [&]() {
+            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+            if (gu < total_units) {
+                const int r = (gu % mt) * kXM + static_cast<int>(rank) * kTileM + lane;
+                const uint32_t* src = static_cast<const uint32_t*>(p.a_scale) + static_cast<size_t>(gkb) * p.a_pad + r;
+                if (r < p.T) w.x = __ldg(src);
+                if (r + 32 < p.T) w.y = __ldg(src + 32);
+                if (r + 64 < p.T) w.z = __ldg(src + 64);
+                if (r + 96 < p.T) w.w = __ldg(src + 96);
+                if (++gkb == KB) {
+                    gkb = 0;
+                    gu += pairs;
                 }
-                const int s = it % kXStages;
-                if (!mbar_wait<kProducerSleepNs>(&empty[s], ((it / kXStages) & 1) ^ 1, abort_flag, p.status)) {
+            }
+            return w;
+        };
+        uint4 ring[kSfAhead];
+#pragma unroll
+        for (int d = 0; d < kSfAhead; ++d) ring[d] = fetch();
+        uint32_t s = 0, ph = 1;
+        bool ok = true;
+        for (long long base = 0; base < n_stages && ok; base += kSfAhead) {
+#pragma unroll
+            for (int d = 0; d < kSfAhead; ++d) {
+                if (base + d >= n_stages) break;
+                const uint4 w = ring[d];
+                ring[d] = fetch();
+                if (!mbar_wait<kProducerSleepNs>(&empty[s], ph, abort_flag, p.status)) {
                     ok = false;
                     break;
                 }
-                *reinterpret_cast<uint4*>(smem + s * kXStage + XL::sfa + 16 * lane) = w;
+                *reinterpret_cast<uint4*>(smem + XL::sf + s * kXSfStage + 16 * lane) = w;
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // visible to tcgen05.cp
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sfready[s]);
+                if (lane == 0) arrive_pair(pair_addr(smem_u32(&sfready[s]), 0));
+                if (++s == kXStages) {
+                    s = 0;
+                    ph ^= 1;
+                }
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            // ------------------------------------------------------------------ MMA issuer
+        if (lane == 0 && rank == 0) {
+            // ------------------------------------------------------------------ MMA issuer, for the pair
             const uint32_t bfmt = p.recipe == 2 ? 5u : 0u;
             uint32_t it = 0, tile = 0;
             bool ok = true;
-            for (int u = blockIdx.x; u < total_units && ok; u += gridDim.x, ++tile) {
+            for (int u = pair; u < total_units && ok; u += pairs, ++tile) {
                 const int b = tile & 1;
                 if (!mbar_wait<kIssuerSleepNs>(&tempty[b], ((tile >> 1) & 1) ^ 1, abort_flag, p.status)) break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + static_cast<uint32_t>(b * kXN);
+                const uint32_t sfb_off = 4 + (u / mt & 1) * 2;
                 for (int kb = 0; kb < KB; ++kb, ++it) {
                     const int s = it % kXStages;
                     if (!mbar_wait<kIssuerSleepNs>(&full[s], (it / kXStages) & 1, abort_flag, p.status) ||
@@ -157,79 +216,78 @@ __global__ void __launch_bounds__(kXThreads, 1)
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t st = smem_u32(smem + s * kXStage);
-                    const uint32_t sfa_t = tmem_base + kXSfCol0 + static_cast<uint32_t>(s * 8);
-                    const uint32_t sfb_t = sfa_t + 4;
-                    sf_copy(sfa_t, sf_atom_desc(st + XL::sfa));
-                    sf_copy(sfb_t, sf_atom_desc(st + XL::sfb));
+                    const uint32_t st = smem_u32(smem + s * kXStage), sf = smem_u32(smem + XL::sf + s * kXSfStage);
+                    const uint32_t sf_t = tmem_base + kXSfCol0 + static_cast<uint32_t>(s * 12);
+                    sf_copy2(sf_t, sf_atom_desc(sf));
+                    sf_copy2(sf_t + 4, sf_atom_desc(sf + kXSf));
+                    sf_copy2(sf_t + 8, sf_atom_desc(sf + 2 * kXSf));
 #pragma unroll
                     for (uint32_t k = 0; k < 4; ++k)
-                        mma_mx(d, sw128_kmajor_desc(st + k * 32), sw128_kmajor_desc(st + XL::b + k * 32),
-                               mx_block_idesc(k, 0u, bfmt, kTileM, kXN), sfa_t, sfb_t, (kb > 0 || k > 0) ? 1u : 0u);
-                    mma_commit(&empty[s]);
+                        mma_mx2(d, sw128_kmajor_desc(st + k * 32), sw128_kmajor_desc(st + XL::b + k * 32),
+                                mx_block_idesc(k, 0u, bfmt, kXM, kXN), sf_t, sf_t + sfb_off, (kb > 0 || k > 0) ? 1u : 0u);
+                    mma_commit2(&empty[s]);
                 }
                 if (!ok) break;
-                mma_commit(&tfull[b]);
+                mma_commit2(&tfull[b]);
             }
-            mma_commit(drain);
+            mma_commit2_own(drain);
             drain_wait(drain, 0);
         }
     } else if (warp >= 4) {
         // ---------------------------------------------------------------------- epilogue
         const int quad = warp & 3;
-        const int h = (warp - 4) >> 2;             // columns h*64 .. h*64+63 of the tile
-        float* stage = reinterpret_cast<float*>(smem + XL::stage) + (warp - 4) * 32 * (kXStageCols + 1);
+        const int h = (warp - 4) >> 2;             // columns h*96 .. h*96+95 of the tile
+        const uint32_t sub = smem_u32(smem + XL::out) + static_cast<uint32_t>(warp - 4) * kXSubs * kSubBytes;
         uint32_t tile = 0;
-        for (int u = blockIdx.x; u < total_units; u += gridDim.x, ++tile) {
+        for (int u = pair; u < total_units; u += pairs, ++tile) {
             const int nb = u / mt, mb = u - nb * mt;
-            const int t0 = mb * kTileM + quad * 32, t = t0 + lane, c0 = nb * kXN + h * 64;
+            const int t0 = mb * kXM + static_cast<int>(rank) * kTileM + quad * 32, c0 = nb * kXN + h * (kXN / 2);
             const int b = tile & 1;
-            if (!mbar_wait(&tfull[b], (tile >> 1) & 1, abort_flag, p.status)) break;
+            epilogue_store_wait();                 // the last tile's stores have read the subtiles
+            epilogue_residual<kXSubs>(p, sub, t0, c0);
+            const bool ok = mbar_wait(&tfull[b], (tile >> 1) & 1, abort_flag, p.status);
+            if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
-            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
-                                   static_cast<uint32_t>(b * kXN + h * 64);
-            uint32_t v[32], w[32];
-            MOE_TMEM_LD32(taddr, v);
-            MOE_TMEM_LD32(taddr + 32, w);
-            MOE_TMEM_WAIT_LD(v);
-            MOE_TMEM_WAIT_LD(w);
-            float acc[64];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                acc[i] = __uint_as_float(v[i]);
-                acc[32 + i] = __uint_as_float(w[i]);
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&tempty[b]);     // the accumulator may be refilled now
-            if (p.N % 8 == 0) {
-                if (t < p.T) {
-                    linear_store32(p, acc, t, c0);
-                    linear_store32(p, acc + 32, t, c0 + 32);
+            epilogue_residual_wait(p);
+#pragma unroll 1
+            for (int k = 0; k < kXSubs; ++k) {
+                const uint32_t at = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
+                                    static_cast<uint32_t>(b * kXN + h * (kXN / 2) + kSubCols * k);
+                uint32_t v[32], w[16];
+                MOE_TMEM_LD32(at, v);
+                MOE_TMEM_LD16(at + 32, w);
+                MOE_TMEM_WAIT_LD(v);
+                MOE_TMEM_WAIT_LD16(w);
+                if (k == kXSubs - 1) {             // the accumulator may be refilled now
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_pair(pair_addr(smem_u32(&tempty[b]), 0));
                 }
-            } else {
+                float acc[kSubCols];
 #pragma unroll
-                for (int c = 0; c < 64; c += kXStageCols)
-                    linear_store_any<kXStageCols>(p, stage, acc + c, t0, c0 + c);
+                for (int i = 0; i < 32; ++i) acc[i] = __uint_as_float(v[i]);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[32 + i] = __uint_as_float(w[i]);
+                epilogue_chunks<6>(p, sub + k * kSubBytes, acc, c0 + kSubCols * k, 0);
             }
+            epilogue_store<kXSubs>(p, &tmY, sub, t0, c0);
         }
+        epilogue_drain();
     }
 
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
+    cluster_sync_all();                                // neither CTA leaves while the other's MMAs or arrivals need it
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc(tmem_base, kXTmemCols);
+        tmem_dealloc2(tmem_base, kXTmemCols);
     }
 }
 
-cudaError_t launch_linear_mx(const LinearArgs& a, const CUtensorMap& tmX, const CUtensorMap& tmW, int num_sms,
-                             cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(k_linear_mx, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(kXSmemBytes));
-    if (e != cudaSuccess) return e;
-    return launch_pdl(k_linear_mx, dim3(num_sms), dim3(kXThreads), kXSmemBytes, s, tmX, tmW, a);
+cudaError_t launch_linear_mx(const LinearArgs& a, const LinearMaps& m, int num_sms, cudaStream_t s) {
+    return launch_pair(k_linear_mx, kXThreads, kXSmemBytes, a, m, num_sms, s);
 }
 
 }  // namespace moe

@@ -8,10 +8,11 @@
 //                epilogue warps, acc[token] += P * (a_s[token] * w_s[row]);
 //   recipes 1, 2: the block-scaled MMA over the whole share in one TMEM accumulator, the weights'
 //                scale atoms as SFA, the tokens' built per stage by one warp as SFB.
-// The shares meet in shared memory: each CTA stores its partial sums of a token into the CTA that
-// owns the token (distributed shared memory), which adds them in rank order and runs the epilogue.
+// The shares meet in shared memory: each CTA sends its partial sums of a token to the CTA that owns
+// the token, one bulk copy per owner, which adds them in rank order and runs the epilogue.  (Plain
+// distributed-shared-memory stores of the same sums took 14000 cycles at 64 tokens.)
 // What bounds it: the weight bytes, and at one token the latency of one load, one MMA chain and the
-// exchange.  Two CTAs fit an SM.  Every wait is bounded.
+// exchange.  Every wait is bounded.
 #include "linear_common.cuh"
 
 namespace moe {
@@ -24,9 +25,11 @@ constexpr int kSBuf = 4;                               // TMEM buffers of recipe
 constexpr uint32_t kSA = kTileM * kTileK;              // 16 KB of weights
 constexpr uint32_t kSSf = 512;
 
+// Two CTAs an SM.  (One CTA with a ring as deep as its share was slower at one token, 18 against 14
+// us: its shared memory keeps it off an SM until the kernel before it has left.)
 template <int NT>
 struct SL {
-    static constexpr int stages = NT == 32 ? 4 : 3;    // two CTAs an SM
+    static constexpr int stages = NT == 32 ? 4 : 3;
     static constexpr uint32_t bytes_b = NT * kTileK;
     static constexpr uint32_t b = kSA;
     static constexpr uint32_t ws = kSA + bytes_b;      // fp32 weight scales, or the weights' atom
@@ -34,7 +37,7 @@ struct SL {
     static constexpr uint32_t stage = ts + kSSf;
     static constexpr uint32_t part = stages * stage;   // [source rank][token of mine][128]
     static constexpr uint32_t bars = part + NT * 128 * 4;
-    static constexpr uint32_t nbars = 3 * stages + 2 * kSBuf + 1;   // full, sfready, empty, tfull, tempty, drain
+    static constexpr uint32_t nbars = 3 * stages + 2 * kSBuf + 2;   // full, sfready, empty, tfull, tempty, drain, xbar
     static constexpr uint32_t misc = bars + nbars * 8;
     static constexpr uint32_t end = misc + 16;
     static constexpr uint32_t smem = end + 1024;
@@ -42,6 +45,7 @@ struct SL {
     static constexpr uint32_t sf_col0 = NT;            // scale factors behind the one accumulator
     static_assert(stage % 1024 == 0, "stage alignment");
     static_assert(kSBuf * NT <= tmem_cols && sf_col0 + stages * 8 <= tmem_cols, "TMEM");
+    static_assert(NT * 128 * 4 <= part, "the share's own sums fit in the stages");
     static_assert(smem <= 113 * 1024, "two CTAs an SM");
 };
 
@@ -51,8 +55,12 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t smem_addr, uint32_t ra
     return r;
 }
 
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+// One bulk copy from this CTA's shared memory into another's of the cluster, counted on the barrier there.
+__device__ __forceinline__ void bulk_send(uint32_t dst_cluster, uint32_t src, uint32_t bytes, uint32_t bar_cluster) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     dst_cluster),
+                 "r"(src), "r"(bytes), "r"(bar_cluster)
+                 : "memory");
 }
 
 // The cluster barrier in its two halves (every thread of every CTA, once each).
@@ -84,6 +92,7 @@ __global__ void __launch_bounds__(kSThreads, 2)
     uint64_t* tfull = empty + ST;
     uint64_t* tempty = tfull + kSBuf;
     uint64_t* drain = tempty + kSBuf;
+    uint64_t* xbar = drain + 1;                        // the shares of this CTA's tokens have arrived
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + S::misc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::misc + 4);
 
@@ -92,7 +101,8 @@ __global__ void __launch_bounds__(kSThreads, 2)
     const int n0 = blockIdx.y * kTileM, t0 = blockIdx.z * NT;
     const int KB = p.K / kTileK;
     const int g0 = static_cast<int>(static_cast<long long>(rank) * KB / split);
-    const int n = static_cast<int>(static_cast<long long>(rank + 1) * KB / split) - g0;   // this CTA's groups (may be 0)
+    const int n = static_cast<int>(static_cast<long long>(rank + 1) * KB / split) - g0;   // this CTA's groups
+    const int per = NT / split;                        // tokens that a CTA of the cluster owns
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
@@ -105,8 +115,10 @@ __global__ void __launch_bounds__(kSThreads, 2)
             mbar_init(&tempty[b], kSEpiWarps);
         }
         mbar_init(drain, 1);
+        mbar_init(xbar, 1);
         *abort_flag = 0;
         fence_mbar_init();
+        if (split > 1 && t0 + rank * per < p.T) mbar_arrive_expect_tx(xbar, static_cast<uint32_t>(NT * 512));
         prefetch_tmap(&tmW);
         prefetch_tmap(&tmT);
         for (int i = 0; i < n && i < ST; ++i) tma_prefetch_2d(&tmW, (g0 + i) * kTileK, n0);   // toward L2, ahead of the wait
@@ -158,15 +170,32 @@ __global__ void __launch_bounds__(kSThreads, 2)
         if (MX) {
             // -------------------------------------------------------------------- token-scale atoms
             // lane i: the words of tokens i (and 32 + i); the scale rows reach 132 past T
+            // (eight stages' words at a time, so that a load's latency is not paid per stage)
             const uint32_t* src = static_cast<const uint32_t*>(p.a_scale) + static_cast<size_t>(g0) * p.a_pad + t0 + lane;
-            for (int it = 0; it < n; ++it, src += p.a_pad) {
-                const uint32_t w0 = __ldg(src), w1 = NT == 64 ? __ldg(src + 32) : 0u;
-                const int s = it % ST;
-                if (it >= ST && !mbar_wait(&empty[s], ((it / ST) & 1) ^ 1, abort_flag, p.status)) break;
-                *reinterpret_cast<uint2*>(smem + s * S::stage + S::ts + 16 * lane) = make_uint2(w0, w1);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // visible to tcgen05.cp
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sfready[s]);
+            constexpr int kAhead = 8;
+            for (int base = 0; base < n; base += kAhead) {
+                uint32_t w0[kAhead], w1[kAhead];
+#pragma unroll
+                for (int d = 0; d < kAhead; ++d) {
+                    const uint32_t* q = src + static_cast<size_t>(min(base + d, n - 1)) * p.a_pad;
+                    w0[d] = __ldg(q);
+                    w1[d] = NT == 64 ? __ldg(q + 32) : 0u;
+                }
+                bool ok = true;
+#pragma unroll
+                for (int d = 0; d < kAhead; ++d) {
+                    const int it = base + d, s = it % ST;
+                    if (it >= n || !ok) break;
+                    if (it >= ST && !mbar_wait(&empty[s], ((it / ST) & 1) ^ 1, abort_flag, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    *reinterpret_cast<uint2*>(smem + s * S::stage + S::ts + 16 * lane) = make_uint2(w0[d], w1[d]);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // visible to tcgen05.cp
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sfready[s]);
+                }
+                if (!ok) break;
             }
         }
     } else if (warp == 1) {
@@ -281,8 +310,6 @@ __global__ void __launch_bounds__(kSThreads, 2)
                 if (t0 + j < p.T) finish_one(p, acc[j], t0 + j, col);
         }
     } else {
-        const int per = NT / split;                    // tokens a CTA finishes
-        const uint32_t part = smem_u32(smem + S::part);
         // Two neighbouring columns a thread, tokens threadIdx / 64, + 4, ...; the first residuals are
         // fetched while the shares are on their way.
         const int c2 = (threadIdx.x & 63) * 2, tq = threadIdx.x >> 6, n2 = n0 + c2;
@@ -295,17 +322,26 @@ __global__ void __launch_bounds__(kSThreads, 2)
         }
         const float b0 = p.bias && n2 < p.N ? __bfloat162float(p.bias[n2]) : 0.0f;
         const float b1 = p.bias && n2 + 1 < p.N ? __bfloat162float(p.bias[n2 + 1]) : 0.0f;
-        cluster_wait();                                // every CTA of the cluster has started
-        if (warp >= 4) {
+        if (warp >= 4) {                               // this share's sums, [token][row], over the stages' space
+            if (!MX) named_bar_sync(1, 32 * kSEpiWarps);   // no warp still reads a stage's scales
+            float* own = reinterpret_cast<float*>(smem) + row;
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int owner = j / per, jl = j - owner * per;
-                if (t0 + j < p.T)
-                    st_cluster_f32(cluster_addr(part + static_cast<uint32_t>(((rank * per + jl) * 128 + row) * 4),
-                                                static_cast<uint32_t>(owner)), acc[j]);
-            }
+            for (int j = 0; j < NT; ++j) own[j * 128] = acc[j];
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        cluster_sync_all();
+        __syncthreads();
+        cluster_wait();                                // every CTA of the cluster has set its barrier up
+        if (warp == 4 && lane < split && t0 + lane * per < p.T) {   // lane r sends rank r its tokens
+            const uint32_t bytes = static_cast<uint32_t>(per * 512);
+            const uint32_t to = static_cast<uint32_t>(lane);
+            bulk_send(cluster_addr(smem_u32(smem + S::part) + static_cast<uint32_t>(rank) * bytes, to),
+                      smem_u32(smem) + to * bytes, bytes, cluster_addr(smem_u32(xbar), to));
+        }
+        __syncwarp();
+        bool have = true;
+        if (t0 + rank * per < p.T) have = mbar_wait(xbar, 0, abort_flag, p.status);
+        __syncwarp();
+        cluster_arrive();                              // this CTA holds its shares: its senders may leave
         const float* mine = reinterpret_cast<const float*>(smem + S::part) + c2;
         for (int jl = tq; jl < per; jl += 4) {
             const int t = t0 + rank * per + jl;
@@ -316,6 +352,7 @@ __global__ void __launch_bounds__(kSThreads, 2)
                 const float2 x = *reinterpret_cast<const float2*>(mine + (r * per + jl) * 128);
                 v.x += x.x, v.y += x.y;
             }
+            if (!have) v.x = v.y = __int_as_float(0x7fc00000);
             v.x = linear_act(v.x + b0, p.act), v.y = linear_act(v.y + b1, p.act);
             const size_t at = static_cast<size_t>(t) * p.N + n2;
             if (pair) {
@@ -334,6 +371,8 @@ __global__ void __launch_bounds__(kSThreads, 2)
                 }
             }
         }
+        __syncwarp();
+        cluster_wait();                                // every copy out of this CTA has landed
     }
 
     tc_fence_before();
@@ -357,15 +396,15 @@ int linear_narrow_split(int T, int N, int K, int num_sms) {
 }
 
 template <int NT, bool MX>
-static cudaError_t launch_narrow_t(const LinearArgs& a, const CUtensorMap& tmX, const CUtensorMap& tmW, int split,
-                                   cudaStream_t s) {
+static cudaError_t launch_narrow_t(const LinearArgs& a, const LinearMaps& m, int split, cudaStream_t s) {
+    constexpr uint32_t smem = SL<NT>::smem;
     cudaError_t e = cudaFuncSetAttribute(k_linear_narrow<NT, MX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(SL<NT>::smem));
+                                         static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(split, (a.N + kTileM - 1) / kTileM, (a.T + NT - 1) / NT);
     cfg.blockDim = dim3(kSThreads);
-    cfg.dynamicSmemBytes = SL<NT>::smem;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -376,17 +415,18 @@ static cudaError_t launch_narrow_t(const LinearArgs& a, const CUtensorMap& tmX, 
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k_linear_narrow<NT, MX>, tmW, tmX, a);
+    return cudaLaunchKernelEx(&cfg, k_linear_narrow<NT, MX>, m.w, m.x, a);
 }
 
-cudaError_t launch_linear_narrow(const LinearArgs& a, const CUtensorMap& tmX, const CUtensorMap& tmW, int num_sms,
-                                 cudaStream_t s) {
+template <int NT>
+static cudaError_t launch_narrow_n(const LinearArgs& a, const LinearMaps& m, int num_sms, cudaStream_t s) {
     const int split = linear_narrow_split(a.T, a.N, a.K, num_sms);
-    if (linear_narrow_tokens(a.T) == 32)
-        return a.recipe == 0 ? launch_narrow_t<32, false>(a, tmX, tmW, split, s)
-                             : launch_narrow_t<32, true>(a, tmX, tmW, split, s);
-    return a.recipe == 0 ? launch_narrow_t<64, false>(a, tmX, tmW, split, s)
-                         : launch_narrow_t<64, true>(a, tmX, tmW, split, s);
+    return a.recipe == 0 ? launch_narrow_t<NT, false>(a, m, split, s)
+                         : launch_narrow_t<NT, true>(a, m, split, s);
+}
+
+cudaError_t launch_linear_narrow(const LinearArgs& a, const LinearMaps& m, int num_sms, cudaStream_t s) {
+    return linear_narrow_tokens(a.T) == 32 ? launch_narrow_n<32>(a, m, num_sms, s) : launch_narrow_n<64>(a, m, num_sms, s);
 }
 
 }  // namespace moe

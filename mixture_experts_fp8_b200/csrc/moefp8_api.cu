@@ -194,6 +194,36 @@ int make_kmajor_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t co
     return MOE_OK;
 }
 
+// 3D map over a dense product's weight-scale atoms [col_blocks][k_blocks][128 words]: a box is the atoms of
+// two neighbouring column blocks for one K block; atoms past the end read as zero.
+int make_atom_map(CUtensorMap* m, const void* base, uint64_t k_blocks, uint64_t col_blocks) {
+    auto fn = encode_fn();
+    if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
+    cuuint64_t dims[3] = {128, k_blocks, col_blocks};
+    cuuint64_t strides[2] = {512, 512 * k_blocks};
+    cuuint32_t box[3] = {128, 1, 2};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+    return MOE_OK;
+}
+
+// 2D map over a dense product's bf16 output [rows, cols] (cols a multiple of 8), box 32 rows x 48 columns.
+int make_output_map(CUtensorMap* m, void* base, uint64_t rows, uint64_t cols) {
+    auto fn = encode_fn();
+    if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {2 * cols};
+    cuuint32_t box[2] = {48, 32};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+    return MOE_OK;
+}
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 }  // namespace
@@ -832,15 +862,18 @@ int moe_linear(const moe_linear_config_t* cfg, const void* x, const void* codes,
     a.y = static_cast<__nv_bfloat16*>(y);
     a.status = static_cast<int32_t*>(workspace);
     a.clear = x == nullptr;
-    CUtensorMap tm_x, tm_w;
-    if ((rc = make_kmajor_map(&tm_x, x ? ws + q_at : codes, T, K, moe::linear_token_box(a, di.sms)))) return rc;
-    if ((rc = make_kmajor_map(&tm_w, w_t, N, K, moe::linear_weight_box(a, di.sms), cfg->recipe == 2))) return rc;
+    moe::LinearMaps m{};
+    const moe::LinearBoxes box = moe::linear_boxes(a, di.sms);
+    if ((rc = make_kmajor_map(&m.x, x ? ws + q_at : codes, T, K, box.x))) return rc;
+    if ((rc = make_kmajor_map(&m.w, w_t, N, K, box.w, cfg->recipe == 2))) return rc;
+    if (box.pair && cfg->recipe != 0 && (rc = make_atom_map(&m.sf, ws_t, K / 128, moe::linear_n_pad(N) / 128))) return rc;
+    if (box.pair && N % 8 == 0 && (rc = make_output_map(&m.y, y, T, N))) return rc;
     if (x) {
         moe::QuantRowsArgs q{static_cast<const __nv_bfloat16*>(x), ws + q_at, reinterpret_cast<uint32_t*>(ws + s_at),
                              a.status, T, K, cfg->recipe, a.a_pad};
         MOE_CUDA_TRY(moe::launch_quant_rows(q, s));
     }
-    MOE_CUDA_TRY(moe::launch_linear(a, tm_x, tm_w, di.sms, s));
+    MOE_CUDA_TRY(moe::launch_linear(a, m, di.sms, s));
     return ok();
 }
 
