@@ -69,9 +69,9 @@ struct LinearMaps {
 bool linear_is_narrow(int T, int N, int K, int recipe, int num_sms);
 int linear_narrow_tokens(int T);
 int linear_narrow_split(int T, int N, int K, int num_sms);
-// Rows of the tensor maps' boxes.
+// Rows of the tensor maps' boxes, and columns of y's.
 struct LinearBoxes {
-    uint32_t x, w;
+    uint32_t x, w, y;
     bool pair;                  // the pair kernels' maps are needed too
 };
 LinearBoxes linear_boxes(const LinearArgs& a, int num_sms);

@@ -4,18 +4,18 @@
 //   y[t, n] = act( sum_g a_s[t,g] * w_s[g,n] * sum_{k in g} xq[t,k] * w[n,k] + b[n] ) + residual[t, n]
 //
 // The fp32 scales vary with the row, the column and the 128-deep group, so each group's partial
-// leaves the tensor core and is promoted, acc += P * (a_s * w_s): the FP32 pipe does as much work as
-// the tensor core, 2 x 128 x 192 operations at 128 a cycle (384 cycles) beside the MMAs' 384.
+// leaves the tensor core and is promoted, acc += P * (a_s * w_s): two fp32 operations an element and
+// group, 256 cycles for 128 x 128 at 128 a cycle, as long as the MMAs themselves.
 //
-// CTA pairs (cta_group::2), persistent: a tile is 256 tokens x 192 columns; each CTA of the pair holds
-// 128 token rows and half of the weight rows (28 KB a stage) and promotes its own 128 x 192 sums.
-// Against the 128 x 256 tiles of one CTA (48 KB a stage, 4 stages, 64 accumulators a thread) six stages
-// fit, a thread keeps 48 accumulators, and a group's whole partial goes to registers at once, so that
-// its TMEM buffer is handed back before the arithmetic.  The scales have a ring of their own, so that
-// an operand stage is free when its MMAs are done.
+// CTA pairs (cta_group::2), persistent: a tile is 256 tokens x 128 columns; each CTA of the pair holds
+// 128 token rows and half of the weight rows (24 KB a stage) and promotes its own 128 x 128 sums.  Two
+// groups are handed over at a time (a step): four 128-column TMEM buffers make two steps, the epilogue
+// waits once, takes both partials into registers (64, beside 32 sums), hands the buffers back, and only
+// then computes, so that the MMAs of the step after next run meanwhile.  The scales have a ring of their
+// own, and an operand stage is free when its MMAs are done.
 //
 // Threads (640): warp 0 TMA producer, warp 1 MMA issuer (the even CTA's, for both), warp 2 scales,
-// warp 3 idle, warps 4-19 epilogue (TMEM lanes 32 (w % 4).., 48 columns each).  Units go column block
+// warp 3 idle, warps 4-19 epilogue (TMEM lanes 32 (w % 4).., 32 columns each).  Units go column block
 // by column block, token blocks fastest, so that pairs working at the same time share weight tiles in
 // L2.  Every wait is bounded.
 #include "linear_common.cuh"
@@ -24,9 +24,10 @@ namespace moe {
 
 namespace {
 
-constexpr int kStages = 6;
-constexpr int kScSlots = 7;                            // scale slots, and barriers of finished groups
-constexpr int kScAhead = 4;                            // groups that the scales are fetched ahead
+constexpr int kN = kPairN0;
+constexpr int kStages = 7;
+constexpr int kSteps = 6;                              // scale slots, and barriers of finished steps
+constexpr int kAhead = 3;                              // steps that the scales are fetched ahead
 constexpr int kThreads = 640;
 constexpr int kFirstEpiWarp = 4;
 constexpr int kEpiWarps = 16;
@@ -34,23 +35,25 @@ constexpr int kEpiWarps = 16;
 constexpr int kRegsLaunch = 96, kRegsLow = 32, kRegsHigh = 112;
 static_assert(128 * kRegsLow + 512 * kRegsHigh == kThreads * kRegsLaunch, "register split");
 constexpr uint32_t kABytes = kTileM * kTileK;
-constexpr uint32_t kBBytes = kPairN / 2 * kTileK;
+constexpr uint32_t kBBytes = kN / 2 * kTileK;
 constexpr uint32_t kStageBytes = kABytes + kBBytes;
-constexpr uint32_t kWsBytes = kPairN * 4;
-constexpr uint32_t kScSlot = kWsBytes + kTileM * 4;   // weight scales of the tile, then the rows' own
-constexpr uint32_t kTmemCols = 512;                   // two buffers of 192 columns
-constexpr uint32_t kBufCols = 256;
+constexpr uint32_t kWsBytes = kN * 4;
+constexpr uint32_t kGroupScales = kWsBytes + kTileM * 4;   // a group's weight scales, then the rows' own
+constexpr uint32_t kScSlot = 2 * kGroupScales;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kStepCols = 2 * kN;
 
 struct L {
     static constexpr uint32_t out = kStages * kStageBytes;
-    static constexpr uint32_t sc = out + kEpiWarps * kSubBytes;
-    static constexpr uint32_t bars = sc + kScSlots * kScSlot;
-    // full[kStages], empty[kStages], tfull[kScSlots], tempty[2], drain
-    static constexpr uint32_t nbars = 2 * kStages + kScSlots + 3;
+    static constexpr uint32_t sc = out + kEpiWarps * Sub<kSubCols0>::bytes;
+    static constexpr uint32_t bars = sc + kSteps * kScSlot;
+    // full[kStages], empty[kStages], tempty[2], tfull[kSteps], drain
+    static constexpr uint32_t nbars = 2 * kStages + kSteps + 3;
     static constexpr uint32_t misc = bars + nbars * 8;    // tmem holder, abort flag
     static constexpr uint32_t end = misc + 16;
+    static_assert((bars + 16 * kStages) % 16 == 0, "the two tempty barriers are one bit apart");
 };
-static_assert(kStageBytes % 1024 == 0 && L::out % 128 == 0 && kScSlot % 16 == 0, "alignment");
+static_assert(kStageBytes % 1024 == 0 && L::out % 512 == 0 && kScSlot % 16 == 0, "alignment");
 constexpr uint32_t kSmemBytes = L::end + 1024;         // + slack to align the base to 1024 bytes
 static_assert(kSmemBytes <= 232448, "shared memory");
 
@@ -62,26 +65,34 @@ __device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t adesc, uin
         ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
 }
 
-// acc[a0 + j] += P[j] * (sa * ws[j]) for j < 16 (packed fp32x2; each lane rounds as scalars would).
-__device__ __forceinline__ void promote16(float2 (&acc)[kSubCols / 2], const uint32_t (&v)[16], uint32_t ws, int a0,
-                                          float2 sa2) {
-#pragma unroll
-    for (int j = 0; j < 16; j += 4) {
-        const float4 w4 = ld_shared_f32x4(ws + 4 * j);
+// A load at a constant offset from a shared-memory address (the offset stays in the instruction).
+template <int OFF>
+__device__ __forceinline__ float4 lds_f32x4_at(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4+%5];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a), "n"(OFF)
+                 : "memory");
+    return v;
+}
+
+// acc[j] += P[j] * (sa * ws[j]) from column 4 J on (packed fp32x2; each lane rounds as scalars would);
+// OFF: the group's place in the scale slot.
+template <int OFF, int J>
+__device__ __forceinline__ void promote(float2 (&acc)[16], const uint32_t (&v)[32], uint32_t sc, float2 sa2) {
+    if constexpr (J < 8) {
+        const float4 w4 = lds_f32x4_at<OFF + 16 * J>(sc);
         const float2 s0 = __fmul2_rn(make_float2(w4.x, w4.y), sa2);
         const float2 s1 = __fmul2_rn(make_float2(w4.z, w4.w), sa2);
-        acc[(a0 + j) / 2] = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), s0,
-                                       acc[(a0 + j) / 2]);
-        acc[(a0 + j) / 2 + 1] = __ffma2_rn(make_float2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])), s1,
-                                           acc[(a0 + j) / 2 + 1]);
+        acc[2 * J] = __ffma2_rn(make_float2(__uint_as_float(v[4 * J]), __uint_as_float(v[4 * J + 1])), s0, acc[2 * J]);
+        acc[2 * J + 1] = __ffma2_rn(make_float2(__uint_as_float(v[4 * J + 2]), __uint_as_float(v[4 * J + 3])), s1,
+                                    acc[2 * J + 1]);
+        promote<OFF, J + 1>(acc, v, sc, sa2);
     }
 }
 
-// One arrival from lane 0 of the warp on a barrier of the cluster, predicated inside the asm.
+// One arrival from lane 0 of the warp on a barrier of the cluster (arrive_pair), predicated inside the asm.
 __device__ __forceinline__ void arrive_pair_lane0(uint32_t bar, int lane) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(
-            bar),
+        "{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
         "r"(lane)
         : "memory");
 }
@@ -92,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_linear_fp32(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap, const __grid_constant__ CUtensorMap tmY, const LinearArgs p) {
     extern __shared__ uint8_t smem_raw[];
-    const int mt = (p.T + kPairM - 1) / kPairM, nt = (p.N + kPairN - 1) / kPairN;
+    const int mt = (p.T + kPairM - 1) / kPairM, nt = (p.N + kN - 1) / kN;
     const int total_units = mt * nt;
     const int KB = p.K / kTileK;
     const uint32_t rank = cluster_ctarank();
@@ -102,19 +113,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bars);      // the even CTA's count for both
     uint64_t* empty = full + kStages;                                  // one in each CTA
-    uint64_t* tfull = empty + kStages;                                 // in each CTA: a group's MMAs and scales
-    uint64_t* tempty = tfull + kScSlots;                               // the even CTA's
-    uint64_t* drain = tempty + 2;
+    uint64_t* tempty = empty + kStages;                                // the even CTA's
+    uint64_t* tfull = tempty + 2;                                      // in each CTA: a step's MMAs and scales
+    uint64_t* drain = tfull + kSteps;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::misc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::misc + 4);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        for (int s = 0; s < kScSlots; ++s) mbar_init(&tfull[s], 2);    // the MMA commit, and the scales' producer
+        for (int s = 0; s < kSteps; ++s) mbar_init(&tfull[s], 2);      // the MMA commit, and the scales' producer
         for (int b = 0; b < 2; ++b) mbar_init(&tempty[b], 2 * kEpiWarps);
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -142,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int u = pair; u < total_units && ok; u += pairs) {
                 const int nb = u / mt, mb = u - nb * mt;
                 const int row0 = mb * kPairM + static_cast<int>(rank) * kTileM;
-                const int brow0 = nb * kPairN + static_cast<int>(rank) * (kPairN / 2);
+                const int brow0 = nb * kN + static_cast<int>(rank) * (kN / 2);
                 for (int kb = 0; kb < KB; ++kb, ++it) {
                     const int s = it % kStages;
                     if (!mbar_wait<kProducerSleepNs>(&empty[s], ((it / kStages) & 1) ^ 1, abort_flag, p.status)) {
@@ -163,72 +174,80 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == 2 && lane == 0) {
             // -------------------------------------------------------------- scales
-            // Group g's scales go to slot g % kScSlots and count on that slot's barrier.  The slot was last
-            // read for group g - kScSlots; the MMAs of group g - kScAhead are issued only when every
-            // epilogue warp has taken the partial of group g - kScAhead - 2 (two TMEM buffers), and so has
-            // finished group g - kScAhead - 3 = g - kScSlots.
-            static_assert(kScAhead + 3 == kScSlots, "a slot is read out before it is filled again");
+            // Step g's scales go to slot g % kSteps and count on that slot's barrier.  The slot was last
+            // read for step g - kSteps; the MMAs of step g - kAhead are issued only when every epilogue
+            // warp has taken the partials of step g - kAhead - 2 (two steps of TMEM), and so has finished
+            // step g - kAhead - 3 = g - kSteps.
+            static_assert(kAhead + 3 == kSteps, "a slot is read out before it is filled again");
             const int n_pad = (p.N + kLinearPad - 1) / kLinearPad * kLinearPad;
             uint32_t it = 0;
             bool ok = true;
             for (int u = pair; u < total_units && ok; u += pairs) {
                 const int nb = u / mt, mb = u - nb * mt;
                 const int row0 = mb * kPairM + static_cast<int>(rank) * kTileM;
-                // the scale rows reach 132 past T, the columns' scales to n_pad
-                const uint32_t w_bytes = static_cast<uint32_t>(min(kPairN, n_pad - nb * kPairN)) * 4u;
-                const uint32_t a_bytes = row0 < p.T ? kTileM * 4u : 0u;
-                const float* ws_src = static_cast<const float*>(p.w_scale) + nb * kPairN;
+                const uint32_t a_bytes = row0 < p.T ? kTileM * 4u : 0u;   // the scale rows reach 132 past T
+                const float* ws_src = static_cast<const float*>(p.w_scale) + nb * kN;
                 const float* sa_src = static_cast<const float*>(p.a_scale) + row0;
-                for (int kb = 0; kb < KB; ++kb, ++it) {
-                    if (it >= kScAhead) {
-                        const uint32_t g = it - kScAhead;
-                        if (!mbar_wait<kProducerSleepNs>(&tfull[g % kScSlots], (g / kScSlots) & 1, abort_flag, p.status)) {
+                for (int kb = 0; kb < KB; kb += 2, ++it) {
+                    if (it >= kAhead) {
+                        const uint32_t g = it - kAhead;
+                        if (!mbar_wait<kProducerSleepNs>(&tfull[g % kSteps], (g / kSteps) & 1, abort_flag, p.status)) {
                             ok = false;
                             break;
                         }
                     }
-                    const int s = it % kScSlots;
-                    uint8_t* slot = smem + L::sc + s * kScSlot;
-                    mbar_arrive_expect_tx(&tfull[s], w_bytes + a_bytes);
-                    bulk_load(slot, ws_src + static_cast<size_t>(kb) * n_pad, w_bytes, &tfull[s]);
-                    if (a_bytes) bulk_load(slot + kWsBytes, sa_src + static_cast<size_t>(kb) * p.a_pad, a_bytes, &tfull[s]);
+                    const int s = it % kSteps, n = min(2, KB - kb);
+                    mbar_arrive_expect_tx(&tfull[s], static_cast<uint32_t>(n) * (kWsBytes + a_bytes));
+                    for (int i = 0; i < n; ++i) {
+                        uint8_t* slot = smem + L::sc + s * kScSlot + i * kGroupScales;
+                        bulk_load(slot, ws_src + static_cast<size_t>(kb + i) * n_pad, kWsBytes, &tfull[s]);
+                        if (a_bytes)
+                            bulk_load(slot + kWsBytes, sa_src + static_cast<size_t>(kb + i) * p.a_pad, a_bytes, &tfull[s]);
+                    }
                 }
             }
-            if (!ok) {   // let the copies already issued land: their groups' barriers may never complete
+            if (!ok) {   // let the copies already issued land: their steps' barriers may never complete
                 const unsigned long long t0 = globaltimer_ns();
                 while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
             }
-        } else if (warp == 1 && lane == 0 && rank == 0) {
+        } else if (warp == 1 && rank == 0) {
             // -------------------------------------------------------------- MMA issuer, for the pair
-            const uint32_t idesc = f8_idesc(kPairM, kPairN);
+            const uint32_t idesc = f8_idesc(kPairM, kN);
             const uint64_t a_desc0 = sw128_kmajor_desc(smem_u32(smem));
             const uint64_t b_desc0 = sw128_kmajor_desc(smem_u32(smem + kABytes));
-            uint32_t s = 0, ph = 0, buf = 0, bph = 0, slot = 0;
+            uint32_t s = 0, ph = 0, buf = 0, bph = 0, step = 0;
             bool ok = true;
             for (int u = pair; u < total_units && ok; u += pairs) {
                 for (int kb = 0; kb < KB; ++kb) {
-                    if (!mbar_wait<kIssuerSleepNs>(&full[s], ph, abort_flag, p.status) ||
-                        !mbar_wait<kIssuerSleepNs>(&tempty[buf], bph ^ 1, abort_flag, p.status)) {
+                    if (((kb & 1) == 0 && !mbar_wait<kIssuerSleepNs>(&tempty[buf], bph ^ 1, abort_flag, p.status)) ||
+                        !mbar_wait<kIssuerSleepNs>(&full[s], ph, abort_flag, p.status)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint64_t ad = a_desc0 + s * (kStageBytes >> 4), bd = b_desc0 + s * (kStageBytes >> 4);
-                    const uint32_t d = tmem_base + buf * kBufCols;
+                    const uint32_t d = tmem_base + buf * kStepCols + (kb & 1) * kN;
+                    const bool last = (kb & 1) || kb == KB - 1;    // the step is complete
+                    if (elect_one()) {
 #pragma unroll
-                    for (int m = 0; m < MPG; ++m) mma_f8_pair(d, ad + 2 * m, bd + 2 * m, idesc, m > 0 ? 1u : 0u);
-                    mma_commit2(&tfull[slot]);
-                    mma_commit2(&empty[s]);
+                        for (int m = 0; m < MPG; ++m) mma_f8_pair(d, ad + 2 * m, bd + 2 * m, idesc, m > 0 ? 1u : 0u);
+                        mma_commit2(&empty[s]);
+                        if (last) mma_commit2(&tfull[step]);
+                    }
+                    __syncwarp();
                     if (++s == kStages) {
                         s = 0;
                         ph ^= 1;
                     }
-                    if (++slot == kScSlots) slot = 0;
-                    buf ^= 1;
-                    bph ^= buf ^ 1;                    // flips after both buffers were used
+                    if (last) {
+                        if (++step == kSteps) step = 0;
+                        buf ^= 1;
+                        bph ^= buf ^ 1;                // flips after both steps of TMEM were used
+                    }
                 }
             }
-            mma_commit2_own(drain);
+            if (elect_one()) mma_commit2_own(drain);
+            __syncwarp();
             drain_wait(drain, 0);
         }
     } else {
@@ -236,66 +255,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------------ epilogue
         const int quad = warp & 3;                     // TMEM lanes 32*quad .. 32*quad+31
         const int qtr = (warp - kFirstEpiWarp) >> 2;
-        const int row_in_tile = quad * 32 + lane;
-        const uint32_t t_warp = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(kSubCols * qtr);
-        const uint32_t ws0 = smem_u32(smem + L::sc) + static_cast<uint32_t>(kSubCols * qtr * 4);
-        const uint32_t sa0 = smem_u32(smem + L::sc + kWsBytes) + static_cast<uint32_t>(row_in_tile * 4);
-        const uint32_t sub = smem_u32(smem + L::out) + static_cast<uint32_t>(warp - kFirstEpiWarp) * kSubBytes;
-        const uint32_t tfull0 = smem_u32(tfull), tempty0 = pair_addr(smem_u32(tempty), 0);
+        const uint32_t sub = smem_u32(smem + L::out) + static_cast<uint32_t>(warp - kFirstEpiWarp) * Sub<kSubCols0>::bytes;
         const uint32_t abort_at = smem_u32(smem + L::misc + 4);
-        uint32_t s = 0, ph = 0, buf = 0;
+        // the step's barrier, weight scales, TMEM and TMEM barrier (256 columns and 8 bytes apart)
+        const uint32_t tf0 = smem_u32(tfull), tf_end = tf0 + 8 * kSteps;
+        const uint32_t sc0 = smem_u32(smem + L::sc) + static_cast<uint32_t>(32 * qtr * 4);
+        const uint32_t sa_off = kWsBytes + static_cast<uint32_t>((quad * 32 + lane - 32 * qtr) * 4);   // from there, the row's scale
+        uint32_t tf_at = tf0, sc_at = sc0, ph = 0;
+        uint32_t t_at = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(32 * qtr);
+        uint32_t te_at = pair_addr(smem_u32(tempty), 0);
         bool ok = true;
         for (int u = pair; u < total_units && ok; u += pairs) {
-            {
-                const int nb = u / mt, mb = u - nb * mt;
-                epilogue_store_wait();                 // the last tile's store has read the subtile
-                epilogue_residual<1>(p, sub, mb * kPairM + static_cast<int>(rank) * kTileM + quad * 32,
-                                     nb * kPairN + kSubCols * qtr);
-            }
-            float2 acc2[kSubCols / 2];
+            const int nb = u / mt, mb = u - nb * mt;
+            const int t0 = mb * kPairM + static_cast<int>(rank) * kTileM + quad * 32, c0 = nb * kN + 32 * qtr;
+            epilogue_store_wait();                     // the last tile's store has read the subtile
+            epilogue_residual<kSubCols0, 1>(p, sub, t0, c0);
+            float2 acc2[16];
 #pragma unroll
-            for (int i = 0; i < kSubCols / 2; ++i) acc2[i] = make_float2(0.0f, 0.0f);
-            for (int kb = 0; kb < KB; ++kb) {
-                if (!mbar_wait_at(tfull0 + 8 * s, ph, abort_at, p.status)) {   // the partial and its scales
+            for (int i = 0; i < 16; ++i) acc2[i] = make_float2(0.0f, 0.0f);
+            for (int kb = 0; kb < KB; kb += 2) {
+                if (!mbar_wait_at(tf_at, ph, abort_at, p.status)) {   // the partials and their scales
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t taddr = t_warp + buf * kBufCols;
-                uint32_t va[16], vb[16], vc[16];
-                MOE_TMEM_LD16(taddr, va);
-                MOE_TMEM_LD16(taddr + 16, vb);
-                MOE_TMEM_LD16(taddr + 32, vc);
-                const float sa = ld_shared_f32(sa0 + s * kScSlot);
-                const float2 sa2 = make_float2(sa, sa);
-                const uint32_t ws = ws0 + s * kScSlot;
-                MOE_TMEM_WAIT_LD16(va);
-                MOE_TMEM_WAIT_LD16(vb);
-                MOE_TMEM_WAIT_LD16(vc);
-                // the warp holds its whole partial: hand the buffer back
+                const bool two = kb + 1 < KB;
+                uint32_t va[32], vb[32];
+                MOE_TMEM_LD32(t_at, va);
+                if (two) MOE_TMEM_LD32(t_at + kN, vb);
+                const float s0 = ld_shared_f32(sc_at + sa_off), s1 = two ? ld_shared_f32(sc_at + sa_off + kGroupScales) : 0.0f;
+                MOE_TMEM_WAIT_LD(va);
+                if (two) MOE_TMEM_WAIT_LD(vb);
+                // the warp holds its partials: hand the buffers back
                 tc_fence_before();
-                arrive_pair_lane0(tempty0 + 8 * buf, lane);
-                promote16(acc2, va, ws, 0, sa2);
-                promote16(acc2, vb, ws + 64, 16, sa2);
-                promote16(acc2, vc, ws + 128, 32, sa2);
+                arrive_pair_lane0(te_at, lane);
+                promote<0, 0>(acc2, va, sc_at, make_float2(s0, s0));
+                if (two) promote<kGroupScales, 0>(acc2, vb, sc_at, make_float2(s1, s1));
                 // the scales were read through the generic proxy; the next bulk copy into this slot is an
-                // async-proxy write: order the reads before it (the next group's arrival carries that on)
+                // async-proxy write: order the reads before it (the next step's arrival carries that on)
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                if (++s == kScSlots) {
-                    s = 0;
+                tf_at += 8;
+                sc_at += kScSlot;
+                if (tf_at == tf_end) {
+                    tf_at = tf0;
+                    sc_at = sc0;
                     ph ^= 1;
                 }
-                buf ^= 1;
+                t_at ^= kStepCols;
+                te_at ^= 8;
             }
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
-            const int nb = u / mt, mb = u - nb * mt;
-            const int t0 = mb * kPairM + static_cast<int>(rank) * kTileM + quad * 32, c0 = nb * kPairN + kSubCols * qtr;
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
             epilogue_residual_wait(p);
-            epilogue_chunks<6>(p, sub, reinterpret_cast<float*>(acc2), c0, 0);
-            epilogue_store<1>(p, &tmY, sub, t0, c0);
+            epilogue_sub<kSubCols0>(p, sub, reinterpret_cast<float*>(acc2), c0);
+            epilogue_store<kSubCols0, 1>(p, &tmY, sub, t0, c0);
         }
         epilogue_drain();
     }
@@ -328,7 +341,8 @@ bool linear_is_narrow(int T, int N, int K, int recipe, int num_sms) {
     const int nt = linear_narrow_tokens(T), split = linear_narrow_split(T, N, K, num_sms);
     const long long tiles = static_cast<long long>((N + kTileM - 1) / kTileM) * ((T + nt - 1) / nt);
     if ((T + nt - 1) / nt > 65535) return false;       // grid.z
-    const long long units = static_cast<long long>((N + kPairN - 1) / kPairN) * ((T + kPairM - 1) / kPairM);
+    const int wn = recipe == 0 ? kPairN0 : kPairNX;
+    const long long units = static_cast<long long>((N + wn - 1) / wn) * ((T + kPairM - 1) / kPairM);
     const long long pairs = num_sms / 2;
     const long long narrow = (tiles * split + num_sms - 1) / num_sms * ((KB + split - 1) / split) * 700;
     const long long wide = (units + pairs - 1) / pairs * KB * (recipe == 0 ? 900 : 700);
@@ -337,8 +351,8 @@ bool linear_is_narrow(int T, int N, int K, int recipe, int num_sms) {
 
 LinearBoxes linear_boxes(const LinearArgs& a, int num_sms) {
     if (linear_is_narrow(a.T, a.N, a.K, a.recipe, num_sms))
-        return {static_cast<uint32_t>(linear_narrow_tokens(a.T)), kTileM, false};
-    return {kTileM, kPairN / 2, true};
+        return {static_cast<uint32_t>(linear_narrow_tokens(a.T)), kTileM, 0, false};
+    return a.recipe == 0 ? LinearBoxes{kTileM, kPairN0 / 2, kSubCols0, true} : LinearBoxes{kTileM, kPairNX / 2, kSubColsX, true};
 }
 
 cudaError_t launch_linear(const LinearArgs& a, const LinearMaps& m, int num_sms, cudaStream_t s) {

@@ -42,14 +42,24 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float* v) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// ---- A warp's output goes through shared memory of its own, in subtiles of 32 rows x 48 columns
-// bf16 (rows of 96 bytes, as a TMA box without swizzle lays them out; a quarter warp's 16-byte accesses
-// meet two at a time): the residual is fetched into it while the sums are still being made, each lane
-// replaces its row's residual by the result, and the subtile leaves by a TMA store (N a multiple of 8)
-// or by coalesced stores (any N).
-constexpr int kSubCols = 48;
-constexpr uint32_t kSubRow = kSubCols * 2;
-constexpr uint32_t kSubBytes = 32 * kSubRow;
+// ---- A warp's output goes through shared memory of its own, in subtiles of 32 rows x C columns bf16:
+// the residual is fetched into it while the sums are still being made, each lane replaces its row's
+// residual by the result, and the subtile leaves by a TMA store (N a multiple of 8) or by coalesced
+// stores (any N).  Laid out as the TMA box has it: C = 48, rows of 96 bytes as they are (a quarter warp's
+// 16-byte accesses meet two at a time); C = 32, rows of 64 bytes with the 64-byte swizzle (they do not
+// meet; 512-byte aligned).
+template <int C>
+struct Sub {
+    static_assert(C == 32 || C == 48, "subtile columns");
+    static constexpr int cols = C, chunks = C / 8, words = C / 2;
+    static constexpr uint32_t bytes = 32 * C * 2;
+    static __device__ __forceinline__ uint32_t chunk(int r, int j) {       // 8 columns of a row
+        return static_cast<uint32_t>(r * C * 2 + (C == 32 ? (j ^ ((r >> 1) & 3)) : j) * 16);
+    }
+    static __device__ __forceinline__ uint32_t word(int r, int w) {        // 2 columns
+        return chunk(r, w >> 2) + static_cast<uint32_t>((w & 3) * 4);
+    }
+};
 
 __device__ __forceinline__ uint4 lds_u4(uint32_t a) {
     uint4 v;
@@ -68,10 +78,11 @@ __device__ __forceinline__ void sts_u32(uint32_t a, uint32_t v) {
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 
-// Fetch the residual of rows t0 .. +31, columns c0 .. c0 + 48 SUBS - 1 into the warp's subtiles at sub.
+// Fetch the residual of rows t0 .. +31, columns c0 .. c0 + C SUBS - 1 into the warp's subtiles at sub.
 // N a multiple of 8: asynchronous, 16 bytes a lane (epilogue_residual_wait before use).
-template <int SUBS>
+template <int C, int SUBS>
 __device__ __forceinline__ void epilogue_residual(const LinearArgs& p, uint32_t sub, int t0, int c0) {
+    using S = Sub<C>;
     if (!p.res) return;
     const int lane = threadIdx.x & 31;
     if (p.N % 8 == 0) {
@@ -79,11 +90,11 @@ __device__ __forceinline__ void epilogue_residual(const LinearArgs& p, uint32_t 
         if (t < p.T) {
             const __nv_bfloat16* row = p.res + static_cast<size_t>(t) * p.N;
 #pragma unroll
-            for (int j = 0; j < 6 * SUBS; ++j) {
+            for (int j = 0; j < S::chunks * SUBS; ++j) {
                 const int c = c0 + 8 * j;
                 if (c < p.N)
                     asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(
-                                     sub + (j / 6) * kSubBytes + lane * kSubRow + (j % 6) * 16),
+                                     sub + (j / S::chunks) * S::bytes + S::chunk(lane, j % S::chunks)),
                                  "l"(row + c)
                                  : "memory");
             }
@@ -91,7 +102,7 @@ __device__ __forceinline__ void epilogue_residual(const LinearArgs& p, uint32_t 
         asm volatile("cp.async.commit_group;" ::: "memory");
         return;
     }
-    constexpr int kWords = 24 * SUBS;                   // of a row
+    constexpr int kWords = S::words * SUBS;             // of a row
     const bool even = p.N % 2 == 0;
 #pragma unroll 8
     for (int i = lane; i < 32 * kWords; i += 32) {
@@ -106,7 +117,7 @@ __device__ __forceinline__ void epilogue_residual(const LinearArgs& p, uint32_t 
             const uint16_t hi = c + 1 < p.N ? *reinterpret_cast<const uint16_t*>(q + 1) : uint16_t(0);
             v = lo | (static_cast<uint32_t>(hi) << 16);
         }
-        sts_u32(sub + (w / 24) * kSubBytes + r * kSubRow + (w % 24) * 4, v);
+        sts_u32(sub + (w / S::words) * S::bytes + S::word(r, w % S::words), v);
     }
 }
 __device__ __forceinline__ void epilogue_residual_wait(const LinearArgs& p) {
@@ -114,12 +125,12 @@ __device__ __forceinline__ void epilogue_residual_wait(const LinearArgs& p) {
     __syncwarp();
 }
 
-// Columns c0 .. c0 + 8 CH - 1 of the lane's row, chunk j0 of the subtile on, from acc.
-template <int ACT, int CH>
-__device__ __forceinline__ void epilogue_chunks_t(const LinearArgs& p, uint32_t sub, float* acc, int c0, int j0) {
+// The lane's row of one subtile, columns c0 .., from acc.
+template <int ACT, int C>
+__device__ __forceinline__ void epilogue_sub_t(const LinearArgs& p, uint32_t sub, float* acc, int c0) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int j = 0; j < CH; ++j) {
+    for (int j = 0; j < Sub<C>::chunks; ++j) {
         float* v = acc + 8 * j;
         const int c = c0 + 8 * j;
         if (p.bias) {
@@ -133,26 +144,27 @@ __device__ __forceinline__ void epilogue_chunks_t(const LinearArgs& p, uint32_t 
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = linear_act_t<ACT>(v[i]);
-        const uint32_t at = sub + lane * kSubRow + (j0 + j) * 16;
+        const uint32_t at = sub + Sub<C>::chunk(lane, j);
         if (p.res) add_bias8(v, lds_u4(at));
         sts_u4(at, pack_bf16x8(v));
     }
 }
-template <int CH>
-__device__ __forceinline__ void epilogue_chunks(const LinearArgs& p, uint32_t sub, float* acc, int c0, int j0) {
+template <int C>
+__device__ __forceinline__ void epilogue_sub(const LinearArgs& p, uint32_t sub, float* acc, int c0) {
     switch (p.act) {
-        case 1: return epilogue_chunks_t<1, CH>(p, sub, acc, c0, j0);
-        case 2: return epilogue_chunks_t<2, CH>(p, sub, acc, c0, j0);
-        case 3: return epilogue_chunks_t<3, CH>(p, sub, acc, c0, j0);
-        case 4: return epilogue_chunks_t<4, CH>(p, sub, acc, c0, j0);
-        default: return epilogue_chunks_t<0, CH>(p, sub, acc, c0, j0);
+        case 1: return epilogue_sub_t<1, C>(p, sub, acc, c0);
+        case 2: return epilogue_sub_t<2, C>(p, sub, acc, c0);
+        case 3: return epilogue_sub_t<3, C>(p, sub, acc, c0);
+        case 4: return epilogue_sub_t<4, C>(p, sub, acc, c0);
+        default: return epilogue_sub_t<0, C>(p, sub, acc, c0);
     }
 }
 
-// Store the warp's SUBS subtiles (rows t0 .., columns c0 ..) to y.  tmY: y [T, N] bf16, box 48 x 32; used
+// Store the warp's SUBS subtiles (rows t0 .., columns c0 ..) to y.  tmY: y [T, N] bf16, box C x 32; used
 // when N is a multiple of 8, and then asynchronous (epilogue_store_wait).
-template <int SUBS>
+template <int C, int SUBS>
 __device__ __forceinline__ void epilogue_store(const LinearArgs& p, const CUtensorMap* tmY, uint32_t sub, int t0, int c0) {
+    using S = Sub<C>;
     const int lane = threadIdx.x & 31;
     if (p.N % 8 == 0) {
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -160,22 +172,22 @@ __device__ __forceinline__ void epilogue_store(const LinearArgs& p, const CUtens
         if (lane == 0 && t0 < p.T) {
 #pragma unroll
             for (int k = 0; k < SUBS; ++k)
-                if (c0 + kSubCols * k < p.N)
+                if (c0 + C * k < p.N)
                     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
                                      reinterpret_cast<uint64_t>(tmY)),
-                                 "r"(sub + k * kSubBytes), "r"(c0 + kSubCols * k), "r"(t0)
+                                 "r"(sub + k * S::bytes), "r"(c0 + C * k), "r"(t0)
                                  : "memory");
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
         return;
     }
     __syncwarp();
-    constexpr int kWords = 24 * SUBS;
+    constexpr int kWords = S::words * SUBS;
     const bool even = p.N % 2 == 0;
 #pragma unroll 8
     for (int i = lane; i < 32 * kWords; i += 32) {
         const int r = i / kWords, w = i % kWords, t = t0 + r, c = c0 + 2 * w;
-        const uint32_t v = lds_u32(sub + (w / 24) * kSubBytes + r * kSubRow + (w % 24) * 4);
+        const uint32_t v = lds_u32(sub + (w / S::words) * S::bytes + S::word(r, w % S::words));
         if (t >= p.T || c >= p.N) continue;
         __nv_bfloat16* q = p.y + static_cast<size_t>(t) * p.N + c;
         if (even) {
@@ -196,6 +208,16 @@ __device__ __forceinline__ void epilogue_store_wait() {
 __device__ __forceinline__ void epilogue_drain() {
     asm volatile("cp.async.wait_all;" ::: "memory");
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+// ---- single-thread roles: the whole warp runs the loop, so that addresses and descriptors stay in uniform
+// registers, and one elected lane issues.  (With the loop in one lane of a divergent branch, issuing a
+// stage's four MMAs and its commits took 350-550 cycles of moves to uniform registers.)
+__device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0); }
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // ---- CTA pairs (cta_group::2): the even CTA issues the MMAs of both
@@ -241,9 +263,11 @@ __device__ __forceinline__ void arrive_pair(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Tiles of the pair kernels: 256 tokens x 192 columns.
+// Tiles of the pair kernels: 256 tokens x 128 columns (fp32 scales) or 192 (block-scaled).
 constexpr int kPairM = 2 * kTileM;
-constexpr int kPairN = 192;
+constexpr int kPairN0 = 128, kPairNX = 192;
+// Columns of an output subtile.
+constexpr int kSubCols0 = 32, kSubColsX = 48;
 
 // Launch a pair kernel: one CTA an SM, clusters of two.
 template <typename K>

@@ -26,8 +26,8 @@ namespace {
 constexpr int kXStages = 6;
 constexpr int kXThreads = 384;
 constexpr int kXEpiWarps = 8;
-constexpr int kXN = kPairN, kXM = kPairM;
-constexpr int kXSubs = kXN / 2 / kSubCols;        // subtiles of an epilogue warp
+constexpr int kXN = kPairNX, kXM = kPairM;
+constexpr int kXSubs = kXN / 2 / kSubColsX;        // subtiles of an epilogue warp
 constexpr uint32_t kXA = kTileM * kTileK;         // 16 KB
 constexpr uint32_t kXB = kXN / 2 * kTileK;        // 12 KB
 constexpr uint32_t kXSf = 512;
@@ -41,7 +41,7 @@ static_assert(kXStage % 1024 == 0 && kXA % 1024 == 0, "stage alignment");
 struct XL {
     static constexpr uint32_t b = kXA;
     static constexpr uint32_t out = kXStages * kXStage;                       // the epilogue's subtiles
-    static constexpr uint32_t sf = out + kXEpiWarps * kXSubs * kSubBytes;
+    static constexpr uint32_t sf = out + kXEpiWarps * kXSubs * Sub<kSubColsX>::bytes;
     static constexpr uint32_t bars = sf + kXStages * kXSfStage;
     static constexpr uint32_t nbars = 3 * kXStages + 5;   // full, sfready, empty, tfull[2], tempty[2], drain
     static constexpr uint32_t misc = bars + nbars * 8;
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + XL::misc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + XL::misc + 4);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kXStages; ++s) {
             mbar_init(&full[s], 1);
@@ -197,10 +197,12 @@ __global__ void __launch_bounds__(kXThreads, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             // ------------------------------------------------------------------ MMA issuer, for the pair
             const uint32_t bfmt = p.recipe == 2 ? 5u : 0u;
-            uint32_t it = 0, tile = 0;
+            const uint64_t a_desc0 = sw128_kmajor_desc(smem_u32(smem)), b_desc0 = sw128_kmajor_desc(smem_u32(smem + XL::b));
+            const uint64_t sf_desc0 = sf_atom_desc(smem_u32(smem + XL::sf));
+            uint32_t s = 0, ph = 0, tile = 0;
             bool ok = true;
             for (int u = pair; u < total_units && ok; u += pairs, ++tile) {
                 const int b = tile & 1;
@@ -208,43 +210,50 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 tc_fence_after();
                 const uint32_t d = tmem_base + static_cast<uint32_t>(b * kXN);
                 const uint32_t sfb_off = 4 + (u / mt & 1) * 2;
-                for (int kb = 0; kb < KB; ++kb, ++it) {
-                    const int s = it % kXStages;
-                    if (!mbar_wait<kIssuerSleepNs>(&full[s], (it / kXStages) & 1, abort_flag, p.status) ||
-                        !mbar_wait<kIssuerSleepNs>(&sfready[s], (it / kXStages) & 1, abort_flag, p.status)) {
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!mbar_wait<kIssuerSleepNs>(&full[s], ph, abort_flag, p.status) ||
+                        !mbar_wait<kIssuerSleepNs>(&sfready[s], ph, abort_flag, p.status)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t st = smem_u32(smem + s * kXStage), sf = smem_u32(smem + XL::sf + s * kXSfStage);
-                    const uint32_t sf_t = tmem_base + kXSfCol0 + static_cast<uint32_t>(s * 12);
-                    sf_copy2(sf_t, sf_atom_desc(sf));
-                    sf_copy2(sf_t + 4, sf_atom_desc(sf + kXSf));
-                    sf_copy2(sf_t + 8, sf_atom_desc(sf + 2 * kXSf));
+                    const uint64_t ad = a_desc0 + s * (kXStage >> 4), bd = b_desc0 + s * (kXStage >> 4);
+                    const uint64_t sfd = sf_desc0 + s * (kXSfStage >> 4);
+                    const uint32_t sf_t = tmem_base + kXSfCol0 + s * 12;
+                    if (elect_one()) {
+                        sf_copy2(sf_t, sfd);
+                        sf_copy2(sf_t + 4, sfd + (kXSf >> 4));
+                        sf_copy2(sf_t + 8, sfd + 2 * (kXSf >> 4));
 #pragma unroll
-                    for (uint32_t k = 0; k < 4; ++k)
-                        mma_mx2(d, sw128_kmajor_desc(st + k * 32), sw128_kmajor_desc(st + XL::b + k * 32),
-                                mx_block_idesc(k, 0u, bfmt, kXM, kXN), sf_t, sf_t + sfb_off, (kb > 0 || k > 0) ? 1u : 0u);
-                    mma_commit2(&empty[s]);
+                        for (uint32_t k = 0; k < 4; ++k)
+                            mma_mx2(d, ad + 2 * k, bd + 2 * k, mx_block_idesc(k, 0u, bfmt, kXM, kXN), sf_t, sf_t + sfb_off,
+                                    (kb > 0 || k > 0) ? 1u : 0u);
+                        mma_commit2(&empty[s]);
+                        if (kb == KB - 1) mma_commit2(&tfull[b]);
+                    }
+                    __syncwarp();
+                    if (++s == kXStages) {
+                        s = 0;
+                        ph ^= 1;
+                    }
                 }
-                if (!ok) break;
-                mma_commit2(&tfull[b]);
             }
-            mma_commit2_own(drain);
+            if (elect_one()) mma_commit2_own(drain);
+            __syncwarp();
             drain_wait(drain, 0);
         }
     } else if (warp >= 4) {
         // ---------------------------------------------------------------------- epilogue
         const int quad = warp & 3;
         const int h = (warp - 4) >> 2;             // columns h*96 .. h*96+95 of the tile
-        const uint32_t sub = smem_u32(smem + XL::out) + static_cast<uint32_t>(warp - 4) * kXSubs * kSubBytes;
+        const uint32_t sub = smem_u32(smem + XL::out) + static_cast<uint32_t>(warp - 4) * kXSubs * Sub<kSubColsX>::bytes;
         uint32_t tile = 0;
         for (int u = pair; u < total_units; u += pairs, ++tile) {
             const int nb = u / mt, mb = u - nb * mt;
             const int t0 = mb * kXM + static_cast<int>(rank) * kTileM + quad * 32, c0 = nb * kXN + h * (kXN / 2);
             const int b = tile & 1;
             epilogue_store_wait();                 // the last tile's stores have read the subtiles
-            epilogue_residual<kXSubs>(p, sub, t0, c0);
+            epilogue_residual<kSubColsX, kXSubs>(p, sub, t0, c0);
             const bool ok = mbar_wait(&tfull[b], (tile >> 1) & 1, abort_flag, p.status);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
@@ -252,7 +261,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
 #pragma unroll 1
             for (int k = 0; k < kXSubs; ++k) {
                 const uint32_t at = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
-                                    static_cast<uint32_t>(b * kXN + h * (kXN / 2) + kSubCols * k);
+                                    static_cast<uint32_t>(b * kXN + h * (kXN / 2) + kSubColsX * k);
                 uint32_t v[32], w[16];
                 MOE_TMEM_LD32(at, v);
                 MOE_TMEM_LD16(at + 32, w);
@@ -263,14 +272,14 @@ __global__ void __launch_bounds__(kXThreads, 1)
                     __syncwarp();
                     if (lane == 0) arrive_pair(pair_addr(smem_u32(&tempty[b]), 0));
                 }
-                float acc[kSubCols];
+                float acc[kSubColsX];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) acc[i] = __uint_as_float(v[i]);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[32 + i] = __uint_as_float(w[i]);
-                epilogue_chunks<6>(p, sub + k * kSubBytes, acc, c0 + kSubCols * k, 0);
+                epilogue_sub<kSubColsX>(p, sub + k * Sub<kSubColsX>::bytes, acc, c0 + kSubColsX * k);
             }
-            epilogue_store<kXSubs>(p, &tmY, sub, t0, c0);
+            epilogue_store<kSubColsX, kXSubs>(p, &tmY, sub, t0, c0);
         }
         epilogue_drain();
     }

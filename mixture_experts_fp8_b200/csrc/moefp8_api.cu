@@ -210,16 +210,18 @@ int make_atom_map(CUtensorMap* m, const void* base, uint64_t k_blocks, uint64_t 
     return MOE_OK;
 }
 
-// 2D map over a dense product's bf16 output [rows, cols] (cols a multiple of 8), box 32 rows x 48 columns.
-int make_output_map(CUtensorMap* m, void* base, uint64_t rows, uint64_t cols) {
+// 2D map over a dense product's bf16 output [rows, cols] (cols a multiple of 8), box 32 rows x box_cols columns
+// (32: with the 64-byte swizzle).
+int make_output_map(CUtensorMap* m, void* base, uint64_t rows, uint64_t cols, uint32_t box_cols) {
     auto fn = encode_fn();
     if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
     cuuint64_t dims[2] = {cols, rows};
     cuuint64_t strides[1] = {2 * cols};
-    cuuint32_t box[2] = {48, 32};
+    cuuint32_t box[2] = {box_cols, 32};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                    box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
     return MOE_OK;
 }
@@ -867,7 +869,7 @@ int moe_linear(const moe_linear_config_t* cfg, const void* x, const void* codes,
     if ((rc = make_kmajor_map(&m.x, x ? ws + q_at : codes, T, K, box.x))) return rc;
     if ((rc = make_kmajor_map(&m.w, w_t, N, K, box.w, cfg->recipe == 2))) return rc;
     if (box.pair && cfg->recipe != 0 && (rc = make_atom_map(&m.sf, ws_t, K / 128, moe::linear_n_pad(N) / 128))) return rc;
-    if (box.pair && N % 8 == 0 && (rc = make_output_map(&m.y, y, T, N))) return rc;
+    if (box.pair && N % 8 == 0 && (rc = make_output_map(&m.y, y, T, N, box.y))) return rc;
     if (x) {
         moe::QuantRowsArgs q{static_cast<const __nv_bfloat16*>(x), ws + q_at, reinterpret_cast<uint32_t*>(ws + s_at),
                              a.status, T, K, cfg->recipe, a.a_pad};
