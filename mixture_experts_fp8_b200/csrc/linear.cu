@@ -146,24 +146,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < kFirstEpiWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
-        if (warp == 0 && lane == 0) {
+        if (warp == 0) {
             // -------------------------------------------------------------- TMA producer
-            uint32_t it = 0;
+            uint32_t it = 0, s = 0, ph = 1;
             bool ok = true;
             for (int u = pair; u < total_units && ok; u += pairs) {
                 const int nb = u / mt, mb = u - nb * mt;
                 const int row0 = mb * kPairM + static_cast<int>(rank) * kTileM;
                 const int brow0 = nb * kN + static_cast<int>(rank) * (kN / 2);
                 for (int kb = 0; kb < KB; ++kb, ++it) {
-                    const int s = it % kStages;
-                    if (!mbar_wait<kProducerSleepNs>(&empty[s], ((it / kStages) & 1) ^ 1, abort_flag, p.status)) {
+                    if (!mbar_wait<kProducerSleepNs>(&empty[s], ph, abort_flag, p.status)) {
                         ok = false;
                         break;
                     }
                     const uint32_t bar = pair_addr(smem_u32(&full[s]), 0);
-                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
-                    tma_load_2d_pair(smem + s * kStageBytes, &tmA, kb * kTileK, row0, bar);
-                    tma_load_2d_pair(smem + s * kStageBytes + kABytes, &tmB, kb * kTileK, brow0, bar);
+                    if (elect_one()) {
+                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
+                        tma_load_2d_pair(smem + s * kStageBytes, &tmA, kb * kTileK, row0, bar);
+                        tma_load_2d_pair(smem + s * kStageBytes + kABytes, &tmB, kb * kTileK, brow0, bar);
+                    }
+                    __syncwarp();
+                    if (++s == kStages) {
+                        s = 0;
+                        ph ^= 1;
+                    }
                 }
             }
             // after an abort: the copies already issued land (the even CTA's barriers count both CTAs')
@@ -172,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t n = it < static_cast<uint32_t>(kStages) ? it : kStages;
                 for (uint32_t i = it - n; i < it; ++i) drain_wait(&full[i % kStages], (i / kStages) & 1);
             }
-        } else if (warp == 2 && lane == 0) {
+        } else if (warp == 2) {
             // -------------------------------------------------------------- scales
             // Step g's scales go to slot g % kSteps and count on that slot's barrier.  The slot was last
             // read for step g - kSteps; the MMAs of step g - kAhead are issued only when every epilogue
@@ -197,13 +203,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     const int s = it % kSteps, n = min(2, KB - kb);
-                    mbar_arrive_expect_tx(&tfull[s], static_cast<uint32_t>(n) * (kWsBytes + a_bytes));
-                    for (int i = 0; i < n; ++i) {
-                        uint8_t* slot = smem + L::sc + s * kScSlot + i * kGroupScales;
-                        bulk_load(slot, ws_src + static_cast<size_t>(kb + i) * n_pad, kWsBytes, &tfull[s]);
-                        if (a_bytes)
-                            bulk_load(slot + kWsBytes, sa_src + static_cast<size_t>(kb + i) * p.a_pad, a_bytes, &tfull[s]);
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&tfull[s], static_cast<uint32_t>(n) * (kWsBytes + a_bytes));
+                        for (int i = 0; i < n; ++i) {
+                            uint8_t* slot = smem + L::sc + s * kScSlot + i * kGroupScales;
+                            bulk_load(slot, ws_src + static_cast<size_t>(kb + i) * n_pad, kWsBytes, &tfull[s]);
+                            if (a_bytes)
+                                bulk_load(slot + kWsBytes, sa_src + static_cast<size_t>(kb + i) * p.a_pad, a_bytes, &tfull[s]);
+                        }
                     }
+                    __syncwarp();
                 }
             }
             if (!ok) {   // let the copies already issued land: their steps' barriers may never complete

@@ -116,35 +116,39 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const uint32_t tmem_base = *tmem_holder;
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ------------------------------------------------------------------ TMA producer
-            const uint32_t b_bytes = p.recipe == 2 ? kXB / 2 : kXB;   // E2M1 weights arrive packed
-            uint32_t it = 0;
-            bool ok = true;
-            for (int u = pair; u < total_units && ok; u += pairs) {
-                const int nb = u / mt, mb = u - nb * mt;
-                const int row0 = mb * kXM + static_cast<int>(rank) * kTileM;
-                const int brow0 = nb * kXN + static_cast<int>(rank) * (kXN / 2);
-                for (int kb = 0; kb < KB; ++kb, ++it) {
-                    const int s = it % kXStages;
-                    if (!mbar_wait<kProducerSleepNs>(&empty[s], ((it / kXStages) & 1) ^ 1, abort_flag, p.status)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t* st = smem + s * kXStage;
-                    const uint32_t bar = pair_addr(smem_u32(&full[s]), 0);
+        // ---------------------------------------------------------------------- TMA producer
+        const uint32_t b_bytes = p.recipe == 2 ? kXB / 2 : kXB;   // E2M1 weights arrive packed
+        uint32_t it = 0, s = 0, ph = 1;
+        bool ok = true;
+        for (int u = pair; u < total_units && ok; u += pairs) {
+            const int nb = u / mt, mb = u - nb * mt;
+            const int row0 = mb * kXM + static_cast<int>(rank) * kTileM;
+            const int brow0 = nb * kXN + static_cast<int>(rank) * (kXN / 2);
+            for (int kb = 0; kb < KB; ++kb, ++it) {
+                if (!mbar_wait<kProducerSleepNs>(&empty[s], ph, abort_flag, p.status)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t* st = smem + s * kXStage;
+                const uint32_t bar = pair_addr(smem_u32(&full[s]), 0);
+                if (elect_one()) {
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (kXA + b_bytes + 2 * kXSf));
                     tma_load_2d_pair(st, &tmA, kb * kTileK, row0, bar);
                     tma_load_2d_pair(st + XL::b, &tmB, kb * kTileK, brow0, bar);
                     tma_load_3d_pair(smem + XL::sf + s * kXSfStage + kXSf, &tmSf, 0, kb, nb * kXN / 128, bar);
                 }
+                __syncwarp();
+                if (++s == kXStages) {
+                    s = 0;
+                    ph ^= 1;
+                }
             }
-            // after an abort: the copies already issued land (the even CTA's barriers count both CTAs')
-            // before either CTA passes the cluster barrier below
-            if (!ok && rank == 0) {
-                const uint32_t n = it < static_cast<uint32_t>(kXStages) ? it : kXStages;
-                for (uint32_t i = it - n; i < it; ++i) drain_wait(&full[i % kXStages], (i / kXStages) & 1);
-            }
+        }
+        // after an abort: the copies already issued land (the even CTA's barriers count both CTAs') before
+        // either CTA passes the cluster barrier below
+        if (!ok && rank == 0) {
+            const uint32_t n = it < static_cast<uint32_t>(kXStages) ? it : kXStages;
+            for (uint32_t i = it - n; i < it; ++i) drain_wait(&full[i % kXStages], (i / kXStages) & 1);
         }
     } else if (warp == 2) {
         // ---------------------------------------------------------------------- token-scale atoms

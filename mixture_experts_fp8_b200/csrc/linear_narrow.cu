@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kSThreads, 2)
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + S::misc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::misc + 4);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const int split = gridDim.x, rank = blockIdx.x;
     const int n0 = blockIdx.y * kTileM, t0 = blockIdx.z * NT;
     const int KB = p.K / kTileK;
@@ -136,19 +136,20 @@ __global__ void __launch_bounds__(kSThreads, 2)
     for (int j = 0; j < NT; ++j) acc[j] = 0.0f;
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ------------------------------------------------------------------ TMA producer
-            const uint32_t a_bytes = p.recipe == 2 ? kSA / 2 : kSA;   // E2M1 weights arrive packed
-            const int n_pad = (p.N + kLinearPad - 1) / kLinearPad * kLinearPad;
-            int it = 0;
-            bool ok = true;
-            for (; it < n; ++it) {
-                const int s = it % ST, kb = g0 + it;
-                if (it >= ST && !mbar_wait(&empty[s], ((it / ST) & 1) ^ 1, abort_flag, p.status)) {
-                    ok = false;
-                    break;
-                }
-                uint8_t* st = smem + s * S::stage;
+        // ---------------------------------------------------------------------- TMA producer
+        const uint32_t a_bytes = p.recipe == 2 ? kSA / 2 : kSA;   // E2M1 weights arrive packed
+        const int n_pad = (p.N + kLinearPad - 1) / kLinearPad * kLinearPad;
+        int it = 0;
+        uint32_t s = 0, ph = 1;
+        bool ok = true;
+        for (; it < n; ++it) {
+            const int kb = g0 + it;
+            if (!mbar_wait(&empty[s], ph, abort_flag, p.status)) {
+                ok = false;
+                break;
+            }
+            uint8_t* st = smem + s * S::stage;
+            if (elect_one()) {
                 mbar_arrive_expect_tx(&full[s], a_bytes + S::bytes_b + kSSf + (MX ? 0 : NT * 4));
                 tma_load_2d(st, &tmW, kb * kTileK, n0, &full[s]);
                 tma_load_2d(st + S::b, &tmT, kb * kTileK, t0, &full[s]);
@@ -162,9 +163,14 @@ __global__ void __launch_bounds__(kSThreads, 2)
                               NT * 4, &full[s]);
                 }
             }
-            if (!ok) {   // let the copies already issued land before the CTA leaves
-                for (int i = it > ST ? it - ST : 0; i < it; ++i) drain_wait(&full[i % ST], (i / ST) & 1);
+            __syncwarp();
+            if (++s == ST) {
+                s = 0;
+                ph ^= 1;
             }
+        }
+        if (!ok) {   // let the copies already issued land before the CTA leaves
+            for (int i = it > ST ? it - ST : 0; i < it; ++i) drain_wait(&full[i % ST], (i / ST) & 1);
         }
     } else if (warp == 2) {
         if (MX) {
@@ -199,43 +205,50 @@ __global__ void __launch_bounds__(kSThreads, 2)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            // ------------------------------------------------------------------ MMA issuer
-            const uint32_t idesc = f8_idesc(kTileM, NT);
-            const uint32_t afmt = p.recipe == 2 ? 5u : 0u;
-            bool ok = true;
-            for (int it = 0; it < n; ++it) {
-                const int s = it % ST, b = it % kSBuf;
-                if (!mbar_wait(&full[s], (it / ST) & 1, abort_flag, p.status) ||
-                    (MX && !mbar_wait(&sfready[s], (it / ST) & 1, abort_flag, p.status)) ||
-                    (!MX && it >= kSBuf && !mbar_wait(&tempty[b], ((it / kSBuf) & 1) ^ 1, abort_flag, p.status))) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t st = smem_u32(smem + s * S::stage);
+        // ---------------------------------------------------------------------- MMA issuer
+        const uint32_t idesc = f8_idesc(kTileM, NT);
+        const uint32_t afmt = p.recipe == 2 ? 5u : 0u;
+        const uint64_t a_desc0 = sw128_kmajor_desc(smem_u32(smem)), b_desc0 = sw128_kmajor_desc(smem_u32(smem + S::b));
+        const uint64_t sfa_desc0 = sf_atom_desc(smem_u32(smem + S::ws)), sfb_desc0 = sf_atom_desc(smem_u32(smem + S::ts));
+        uint32_t s = 0, ph = 0, buf = 0, bph = 1;
+        for (int it = 0; it < n; ++it) {
+            if (!mbar_wait(&full[s], ph, abort_flag, p.status) || (MX && !mbar_wait(&sfready[s], ph, abort_flag, p.status)) ||
+                (!MX && !mbar_wait(&tempty[buf], bph, abort_flag, p.status)))
+                break;
+            tc_fence_after();
+            const uint32_t at = s * (S::stage >> 4);
+            const uint64_t ad = a_desc0 + at, bd = b_desc0 + at;
+            if (elect_one()) {
                 if (MX) {
-                    const uint32_t sfa_t = tmem_base + S::sf_col0 + static_cast<uint32_t>(s * 8), sfb_t = sfa_t + 4;
-                    sf_copy(sfa_t, sf_atom_desc(st + S::ws));
-                    sf_copy(sfb_t, sf_atom_desc(st + S::ts));
+                    const uint32_t sfa_t = tmem_base + S::sf_col0 + s * 8, sfb_t = sfa_t + 4;
+                    sf_copy(sfa_t, sfa_desc0 + at);
+                    sf_copy(sfb_t, sfb_desc0 + at);
 #pragma unroll
                     for (uint32_t k = 0; k < 4; ++k)
-                        mma_mx(tmem_base, sw128_kmajor_desc(st + k * 32), sw128_kmajor_desc(st + S::b + k * 32),
-                               mx_block_idesc(k, afmt, 0u, kTileM, NT), sfa_t, sfb_t, (it > 0 || k > 0) ? 1u : 0u);
+                        mma_mx(tmem_base, ad + 2 * k, bd + 2 * k, mx_block_idesc(k, afmt, 0u, kTileM, NT), sfa_t, sfb_t,
+                               (it > 0 || k > 0) ? 1u : 0u);
+                    if (it == n - 1) mma_commit(&tfull[0]);
                 } else {
-                    const uint32_t d = tmem_base + static_cast<uint32_t>(b * NT);
+                    const uint32_t d = tmem_base + buf * NT;
 #pragma unroll
-                    for (uint32_t k = 0; k < 4; ++k)
-                        mma_f8(d, sw128_kmajor_desc(st + k * 32), sw128_kmajor_desc(st + S::b + k * 32), idesc,
-                               k > 0 ? 1u : 0u);
-                    mma_commit(&tfull[b]);
+                    for (uint32_t k = 0; k < 4; ++k) mma_f8(d, ad + 2 * k, bd + 2 * k, idesc, k > 0 ? 1u : 0u);
+                    mma_commit(&tfull[buf]);
                 }
                 mma_commit(&empty[s]);
             }
-            if (MX && ok && n > 0) mma_commit(&tfull[0]);
-            mma_commit(drain);          // all MMAs issued by this thread have finished
-            drain_wait(drain, 0);
+            __syncwarp();
+            if (++s == ST) {
+                s = 0;
+                ph ^= 1;
+            }
+            if (++buf == kSBuf) {
+                buf = 0;
+                bph ^= 1;
+            }
         }
+        if (elect_one()) mma_commit(drain);   // all MMAs issued by this warp have finished
+        __syncwarp();
+        drain_wait(drain, 0);
     } else if (warp >= 4) {
         // ---------------------------------------------------------------------- epilogue: the share's sums
         const int quad = warp & 3;      // TMEM lanes 32*quad .. = weight rows of the tile
