@@ -14,8 +14,8 @@
 // 512-byte atom = the four scale bytes of row 32c + i.  A tile's columns start in the middle of a
 // weight atom when its index is odd: SFB then starts two TMEM columns in.
 //
-// Threads (384): warp 0 TMA producer, warp 1 MMA issuer (the even CTA's, for both), warp 2 the tokens'
-// scale atoms, warp 3 idle, warps 4-11 epilogue (TMEM lanes 32 (w % 4).., 96 of the columns each).
+// Threads (640): warp 0 TMA producer, warp 1 MMA issuer (the even CTA's, for both), warp 2 the tokens'
+// scale atoms, warp 3 idle, warps 4-19 epilogue (TMEM lanes 32 (w % 4).., 48 of the columns each).
 // Units go column block by column block, token blocks fastest.  Every wait is bounded.
 #include "linear_common.cuh"
 
@@ -24,10 +24,10 @@ namespace moe {
 namespace {
 
 constexpr int kXStages = 6;
-constexpr int kXThreads = 384;
-constexpr int kXEpiWarps = 8;
+constexpr int kXThreads = 640;
+constexpr int kXEpiWarps = 16;
 constexpr int kXN = kPairNX, kXM = kPairM;
-constexpr int kXSubs = kXN / 2 / kSubColsX;        // subtiles of an epilogue warp
+static_assert(4 * kSubColsX == kXN, "an epilogue warp has one subtile");
 constexpr uint32_t kXA = kTileM * kTileK;         // 16 KB
 constexpr uint32_t kXB = kXN / 2 * kTileK;        // 12 KB
 constexpr uint32_t kXSf = 512;
@@ -41,7 +41,7 @@ static_assert(kXStage % 1024 == 0 && kXA % 1024 == 0, "stage alignment");
 struct XL {
     static constexpr uint32_t b = kXA;
     static constexpr uint32_t out = kXStages * kXStage;                       // the epilogue's subtiles
-    static constexpr uint32_t sf = out + kXEpiWarps * kXSubs * Sub<kSubColsX>::bytes;
+    static constexpr uint32_t sf = out + kXEpiWarps * Sub<kSubColsX>::bytes;
     static constexpr uint32_t bars = sf + kXStages * kXSfStage;
     static constexpr uint32_t nbars = 3 * kXStages + 5;   // full, sfready, empty, tfull[2], tempty[2], drain
     static constexpr uint32_t misc = bars + nbars * 8;
@@ -249,41 +249,36 @@ __global__ void __launch_bounds__(kXThreads, 1)
     } else if (warp >= 4) {
         // ---------------------------------------------------------------------- epilogue
         const int quad = warp & 3;
-        const int h = (warp - 4) >> 2;             // columns h*96 .. h*96+95 of the tile
-        const uint32_t sub = smem_u32(smem + XL::out) + static_cast<uint32_t>(warp - 4) * kXSubs * Sub<kSubColsX>::bytes;
+        const int qtr = (warp - 4) >> 2;           // columns 48 qtr .. of the tile
+        const uint32_t sub = smem_u32(smem + XL::out) + static_cast<uint32_t>(warp - 4) * Sub<kSubColsX>::bytes;
         uint32_t tile = 0;
         for (int u = pair; u < total_units; u += pairs, ++tile) {
             const int nb = u / mt, mb = u - nb * mt;
-            const int t0 = mb * kXM + static_cast<int>(rank) * kTileM + quad * 32, c0 = nb * kXN + h * (kXN / 2);
+            const int t0 = mb * kXM + static_cast<int>(rank) * kTileM + quad * 32, c0 = nb * kXN + kSubColsX * qtr;
             const int b = tile & 1;
-            epilogue_store_wait();                 // the last tile's stores have read the subtiles
-            epilogue_residual<kSubColsX, kXSubs>(p, sub, t0, c0);
+            epilogue_store_wait();                 // the last tile's store has read the subtile
+            epilogue_residual<kSubColsX, 1>(p, sub, t0, c0);
             const bool ok = mbar_wait(&tfull[b], (tile >> 1) & 1, abort_flag, p.status);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
+            const uint32_t at = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
+                                static_cast<uint32_t>(b * kXN + kSubColsX * qtr);
+            uint32_t v[32], w[16];
+            MOE_TMEM_LD32(at, v);
+            MOE_TMEM_LD16(at + 32, w);
+            MOE_TMEM_WAIT_LD(v);
+            MOE_TMEM_WAIT_LD16(w);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_pair(pair_addr(smem_u32(&tempty[b]), 0));   // the accumulator may be refilled now
+            float acc[kSubColsX];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[i] = __uint_as_float(v[i]);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[32 + i] = __uint_as_float(w[i]);
             epilogue_residual_wait(p);
-#pragma unroll 1
-            for (int k = 0; k < kXSubs; ++k) {
-                const uint32_t at = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
-                                    static_cast<uint32_t>(b * kXN + h * (kXN / 2) + kSubColsX * k);
-                uint32_t v[32], w[16];
-                MOE_TMEM_LD32(at, v);
-                MOE_TMEM_LD16(at + 32, w);
-                MOE_TMEM_WAIT_LD(v);
-                MOE_TMEM_WAIT_LD16(w);
-                if (k == kXSubs - 1) {             // the accumulator may be refilled now
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive_pair(pair_addr(smem_u32(&tempty[b]), 0));
-                }
-                float acc[kSubColsX];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) acc[i] = __uint_as_float(v[i]);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) acc[32 + i] = __uint_as_float(w[i]);
-                epilogue_sub<kSubColsX>(p, sub + k * Sub<kSubColsX>::bytes, acc, c0 + kSubColsX * k);
-            }
-            epilogue_store<kSubColsX, kXSubs>(p, &tmY, sub, t0, c0);
+            epilogue_sub<kSubColsX>(p, sub, acc, c0);
+            epilogue_store<kSubColsX, 1>(p, &tmY, sub, t0, c0);
         }
         epilogue_drain();
     }

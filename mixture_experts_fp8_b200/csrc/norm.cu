@@ -170,29 +170,41 @@ __global__ void __launch_bounds__(1024) k_add_rms_norm(NormArgs a) {
     }
 }
 
-// The codes and scales of bf16 rows: a thread per eight columns.  Clears the status word of the call (its first kernel).
+// The codes and scales of bf16 rows: a thread takes eight columns at two places, both loads first.
+// Clears the status word of the call (its first kernel).
 __global__ void __launch_bounds__(256) k_quant_rows(QuantRowsArgs a) {
     pdl_wait_then_release();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = MOE_OK;
-    const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
     const int per_row = a.K >> 3;                      // a multiple of 16: a scale block stays in a half warp
-    const long long t = i / per_row;
-    const int col = static_cast<int>(i - t * per_row) * 8;
-    const bool ok = t < a.T;
-    float v[8];
-    unpack8(ok ? __ldg(reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(t) * a.K + col)) : make_uint4(0, 0, 0, 0), v);
-    uint2 q;
-    uint32_t word;
-    if (a.recipe == 0) {
-        float s;
-        q = quant_fp32(v, group16_max(absmax8(v)), s);
-        word = __float_as_uint(s);
-    } else {
-        q = quant_mx(v, word);
+    const long long n = static_cast<long long>(a.T) * per_row;
+    const long long i0 = static_cast<long long>(blockIdx.x) * 512 + threadIdx.x;
+    uint4 raw[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const long long i = i0 + 256 * h;
+        raw[h] = i < n ? __ldg(reinterpret_cast<const uint4*>(a.x) + i) : make_uint4(0, 0, 0, 0);
     }
-    if (!ok) return;
-    *reinterpret_cast<uint2*>(a.xq + static_cast<size_t>(t) * a.K + col) = q;
-    if ((threadIdx.x & 15) == 0) a.xs[static_cast<size_t>(col >> 7) * a.a_pad + t] = word;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const long long i = i0 + 256 * h;
+        float v[8];
+        unpack8(raw[h], v);
+        uint2 q;
+        uint32_t word;
+        if (a.recipe == 0) {
+            float s;
+            q = quant_fp32(v, group16_max(absmax8(v)), s);
+            word = __float_as_uint(s);
+        } else {
+            q = quant_mx(v, word);
+        }
+        if (i >= n) continue;
+        reinterpret_cast<uint2*>(a.xq)[i] = q;
+        if ((threadIdx.x & 15) == 0) {
+            const int t = static_cast<int>(i / per_row), blk = static_cast<int>(i - static_cast<long long>(t) * per_row) >> 4;
+            a.xs[static_cast<size_t>(blk) * a.a_pad + t] = word;
+        }
+    }
 }
 
 template <int CH>
@@ -214,7 +226,7 @@ cudaError_t launch_add_rms_norm(NormArgs a, cudaStream_t s) {
 
 cudaError_t launch_quant_rows(const QuantRowsArgs& a, cudaStream_t s) {
     const long long n = static_cast<long long>(a.T) * (a.K >> 3);
-    return launch_pdl(k_quant_rows, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, s, a);
+    return launch_pdl(k_quant_rows, dim3(static_cast<unsigned>((n + 511) / 512)), dim3(256), 0, s, a);
 }
 
 }  // namespace moe
