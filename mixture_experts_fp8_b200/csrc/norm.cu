@@ -53,11 +53,19 @@ __device__ __forceinline__ float group16_max(float m) {
 // fp32 scale of a block with maximum amax, and its codes.  The scale is amax times the rounded 1/448,
 // as a torch program on the GPU computes amax / 448.0, so that its codes are these; the layer's own
 // quantizer divides, which can differ by one ulp of the scale.
+// v / s is v times the reciprocal of s and the reciprocal's own remainder, v ih + v il: within 2^-46 of the
+// quotient before its one rounding, in two instructions where an IEEE division takes about ten.
 __device__ __forceinline__ uint2 quant_fp32(const float* v, float amax, float& s) {
     s = amax > 0.0f ? __fmul_rn(amax, 1.0f / 448.0f) : 1.0f;
     float q[8];
+    if (s > 1e-30f && s < 1e30f) {                     // the reciprocal and its remainder are normal numbers
+        const float ih = __frcp_rn(s), il = fmaf(-ih, s, 1.0f) * ih;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(v[i], s);
+        for (int i = 0; i < 8; ++i) q[i] = fmaf(v[i], ih, v[i] * il);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(v[i], s);
+    }
     return codes8(q);
 }
 
@@ -86,8 +94,8 @@ __device__ __forceinline__ uint2 quant_mx(const float* v, uint32_t& word) {
 // in registers between the sum and the scaling and is read once.  Rows of a block are independent.
 // The thread count and the chunks follow from H alone, and the sum is taken in a fixed order: a
 // row's bits do not depend on the batch.  RES: 0 no residual, 1 bf16, 2 fp32.
-template <int CH, int RES>
-__global__ void __launch_bounds__(1024) k_add_rms_norm(NormArgs a) {
+template <int CH, int RES, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? (CH <= 2 ? 6 : 4) : 1) k_add_rms_norm(NormArgs a) {
     __shared__ float s_sum[32];
     pdl_wait_then_release();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -207,21 +215,24 @@ __global__ void __launch_bounds__(256) k_quant_rows(QuantRowsArgs a) {
     }
 }
 
-template <int CH>
+template <int CH, int MAXT>
 static cudaError_t launch_norm_ch(const NormArgs& a, int rows, cudaStream_t s) {
     const dim3 grid(static_cast<unsigned>((a.T + rows - 1) / rows)), block(a.tpr * rows);
-    if (!a.res) return launch_pdl(k_add_rms_norm<CH, 0>, grid, block, 0, s, a);
-    return a.res_fp32 ? launch_pdl(k_add_rms_norm<CH, 2>, grid, block, 0, s, a)
-                      : launch_pdl(k_add_rms_norm<CH, 1>, grid, block, 0, s, a);
+    if (!a.res) return launch_pdl(k_add_rms_norm<CH, 0, MAXT>, grid, block, 0, s, a);
+    return a.res_fp32 ? launch_pdl(k_add_rms_norm<CH, 2, MAXT>, grid, block, 0, s, a)
+                      : launch_pdl(k_add_rms_norm<CH, 1, MAXT>, grid, block, 0, s, a);
 }
 
 cudaError_t launch_add_rms_norm(NormArgs a, cudaStream_t s) {
-    // The fewest chunks a thread that keep a row within 256 threads (1024 for the longest rows).
+    // The fewest chunks a thread that keep a row within 256 threads (1024 for the longest rows); short
+    // rows share a block of 256.
     const int chunks = a.H / 8;
     const int ch = chunks <= 256 ? 1 : chunks <= 512 ? 2 : 4;
     a.tpr = ((chunks + ch - 1) / ch + 31) / 32 * 32;
     const int rows = a.tpr >= 256 ? 1 : 256 / a.tpr;
-    return ch == 1 ? launch_norm_ch<1>(a, rows, s) : ch == 2 ? launch_norm_ch<2>(a, rows, s) : launch_norm_ch<4>(a, rows, s);
+    if (a.tpr > 256) return launch_norm_ch<4, 1024>(a, rows, s);
+    return ch == 1 ? launch_norm_ch<1, 256>(a, rows, s) : ch == 2 ? launch_norm_ch<2, 256>(a, rows, s)
+                                                                  : launch_norm_ch<4, 256>(a, rows, s);
 }
 
 cudaError_t launch_quant_rows(const QuantRowsArgs& a, cudaStream_t s) {
