@@ -366,7 +366,7 @@ int moe_quantized_size(int32_t rows, int32_t cols, size_t *codes_bytes, size_t *
  *   codes, scales  device, quantized rows of the unrounded y, or both NULL; out
  * At least one output.  residual_out may be the residual or (bf16) x buffer itself, and y the x
  * buffer or (bf16) the residual buffer; buffers may not overlap in any other way.  Every buffer
- * 16-byte aligned.  One launch.  Inf or NaN in a row makes y, or the values its codes stand for,
+ * 16-byte aligned, an fp32 residual and its residual_out 32-byte.  One launch.  Inf or NaN in a row makes y, or the values its codes stand for,
  * non-finite in that row only. */
 int moe_add_rms_norm(const moe_config_t *cfg, const void *x, const void *residual, int residual_fp32,
                      const float *norm_weight, float rms_eps, void *residual_out, void *y, void *codes,

@@ -772,6 +772,8 @@ int moe_add_rms_norm(const moe_config_t* cfg, const void* x, const void* residua
     if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(norm_weight, 16) || !aligned(residual_out, 16) ||
         !aligned(y, 16) || !aligned(codes, 16) || !aligned(scales, 16))
         return fail(MOE_ERR_INVALID_ARG, "moe_add_rms_norm: buffers need 16-byte alignment");
+    if (residual_fp32 && (!aligned(residual, 32) || !aligned(residual_out, 32)))
+        return fail(MOE_ERR_INVALID_ARG, "moe_add_rms_norm: an fp32 residual needs 32-byte alignment");
     if (!(rms_eps >= 0.0f)) return fail(MOE_ERR_INVALID_ARG, "moe_add_rms_norm: rms_eps must be >= 0");
     if (cfg->hidden > 32768)
         return fail(MOE_ERR_UNSUPPORTED, "moe_add_rms_norm: hidden (%d) exceeds 32768", cfg->hidden);

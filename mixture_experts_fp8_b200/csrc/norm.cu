@@ -32,6 +32,17 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Eight fp32 values in one 32-byte access (p 32-byte aligned): a whole sector a lane.
+__device__ __forceinline__ void load8_f32(const float* p, float* v) {
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]) : "l"(p));
+}
+__device__ __forceinline__ void store8_f32(float* p, const float* v) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ float absmax8(const float* v) {
     float m = 0.0f;
 #pragma unroll
@@ -119,10 +130,10 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (CH <= 2 ? 6 : 4) : 1) k_a
 #pragma unroll
                 for (int i = 0; i < 8; ++i) h[c][i] += r[i];
             } else if (RES == 2) {
-                const float4* r4 = reinterpret_cast<const float4*>(static_cast<const float*>(a.res) + base + col);
-                const float4 r0 = r4[0], r1 = r4[1];
-                h[c][0] += r0.x, h[c][1] += r0.y, h[c][2] += r0.z, h[c][3] += r0.w;
-                h[c][4] += r1.x, h[c][5] += r1.y, h[c][6] += r1.z, h[c][7] += r1.w;
+                float r[8];
+                load8_f32(static_cast<const float*>(a.res) + base + col, r);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[c][i] += r[i];
             }
         } else {
 #pragma unroll
@@ -146,11 +157,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (CH <= 2 ? 6 : 4) : 1) k_a
         const bool ok = row_ok && col < a.H;
         if (RES == 1 && ok && a.res_out)
             *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.res_out) + base + col) = pack8(h[c]);
-        if (RES == 2 && ok && a.res_out) {
-            float4* o4 = reinterpret_cast<float4*>(static_cast<float*>(a.res_out) + base + col);
-            o4[0] = make_float4(h[c][0], h[c][1], h[c][2], h[c][3]);
-            o4[1] = make_float4(h[c][4], h[c][5], h[c][6], h[c][7]);
-        }
+        if (RES == 2 && ok && a.res_out) store8_f32(static_cast<float*>(a.res_out) + base + col, h[c]);
         float y[8];
         float4 w0 = make_float4(0.f, 0.f, 0.f, 0.f), w1 = w0;
         if (ok) {

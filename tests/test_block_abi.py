@@ -60,6 +60,7 @@ def test_norm_refusals():
     for name in ("x", "res", "w", "y"):
         refused(call(**{name: AL | 8}), BAD, b"16-byte")
     refused(call(q=AL | 4, s=AL), BAD, b"16-byte")
+    refused(lambda: lib.moe_add_rms_norm(c, AL, AL | 16, 1, AL, f(1e-6), None, AL, None, None, None), BAD, b"32-byte")
     for eps in (-1.0, float("nan")):
         refused(call(eps=eps), BAD, b"rms_eps")
     refused(call(c=ctypes.byref(cfg(hidden=32768 + 128).c())), UNS, b"32768")
