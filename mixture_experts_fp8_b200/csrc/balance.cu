@@ -294,13 +294,13 @@ __global__ void __launch_bounds__(kRWarps * 32) k_route_backward(RouteBackwardAr
     using R = Row<NE, G, VEC>;
     constexpr int TPW = 32 / G, W = NE * G;
     __shared__ __align__(16) float s_add[kRWarps * TPW][W];
-    __shared__ float s_scale[kRWarps][W];
+    __shared__ float s_scale[kRWarps * TPW][W];        // a group's sums of dscale
     pdl_wait_then_release();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gl = lane % G, grp = lane / G;
+    const unsigned group_mask = (G == 32 ? 0xffffffffu : (1u << G) - 1u) << (grp * G);
     float* add = s_add[warp * TPW + grp];
-    float* dscale = s_scale[warp];
-    for (int e = gl; e < W; e += G) add[e] = 0.0f;
-    for (int e = lane; e < W; e += 32) dscale[e] = 0.0f;
+    float* dscale = s_scale[warp * TPW + grp];
+    for (int e = gl; e < W; e += G) add[e] = dscale[e] = 0.0f;
     __syncwarp();
     const int c0 = blockIdx.x * a.chunk, c1 = min(a.T, c0 + a.chunk);
     const float gloss = a.dloss ? __ldg(a.dloss) * a.coef : 0.0f;
@@ -341,10 +341,10 @@ __global__ void __launch_bounds__(kRWarps * 32) k_route_backward(RouteBackwardAr
         if (e0 >= a.E) e0 = -1;
         const float l0 = e0 >= 0 ? __ldg(row + e0) : -INFINITY;
         const float scale0 = e0 >= 0 && a.pes ? __ldg(a.pes + e0) : 1.0f;
-        float nz = x0 != 0.0f ? 1.0f : 0.0f;           // NaN counts
+        bool nz = x0 != 0.0f;                          // NaN counts
         if (in && a.dw)
-            for (int j = gl + G; j < a.K; j += G) nz = __ldg(dw + j) != 0.0f ? 1.0f : nz;
-        const bool wts = group_max<G>(nz) != 0.0f;
+            for (int j = gl + G; j < a.K; j += G) nz |= __ldg(dw + j) != 0.0f;
+        const bool wts = __ballot_sync(0xffffffffu, nz) & group_mask;
         float z = 0.0f, m = -INFINITY;
         if (MODE == kSigmoid) {
 #pragma unroll
@@ -434,24 +434,17 @@ __global__ void __launch_bounds__(kRWarps * 32) k_route_backward(RouteBackwardAr
         }
         if (in) R::store(a.dl + tr * a.E, a.E, gl, p);
         __syncwarp();
-        // ---- back to zero; the scale's gradient, the warp's tokens one after the other
-        if (wts && e0 >= 0) add[e0] = 0.0f;
-        if (more)
+        // ---- back to zero, and the scale's gradient
+        if (wts && e0 >= 0) {
+            add[e0] = 0.0f;
+            if (a.dpes) dscale[e0] += x0 * (u0 * sz);
+        }
+        if (more) {
             for (int j = gl + G; j < a.K; j += G) {
                 const int e = __ldg(idx + j);
-                if (e >= 0 && e < a.E) add[e] = 0.0f;
-            }
-        if (a.dpes) {
-            for (int w = 0; w < TPW; ++w) {
-                if (w == grp && wts) {
-                    if (e0 >= 0) dscale[e0] += x0 * (u0 * sz);
-                    if (more)
-                        for (int j = gl + G; j < a.K; j += G) {
-                            const int e = __ldg(idx + j);
-                            if (e >= 0 && e < a.E) dscale[e] += __ldg(dw + j) * a.rsf * (raw(__ldg(row + e)) * sz);
-                        }
-                }
-                __syncwarp();
+                if (e < 0 || e >= a.E) continue;
+                add[e] = 0.0f;
+                if (a.dpes) dscale[e] += __ldg(dw + j) * a.rsf * (raw(__ldg(row + e)) * sz);
             }
         }
         __syncwarp();
@@ -460,7 +453,7 @@ __global__ void __launch_bounds__(kRWarps * 32) k_route_backward(RouteBackwardAr
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
         float v = 0.0f;
-        for (int w = 0; w < kRWarps; ++w) v += s_scale[w][e];
+        for (int w = 0; w < kRWarps * TPW; ++w) v += s_scale[w][e];
         a.part[static_cast<size_t>(blockIdx.x) * a.E + e] = v;
     }
 }
@@ -527,8 +520,8 @@ cudaError_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t s) {
     const bool vec = a.E % 4 == 0 && rows16(a.logits) && rows16(a.dl) && rows16(a.counts);
     const cudaError_t e = a.E <= 32    ? backward_t<4, 8>(a, vec, s)
                           : a.E <= 64  ? backward_t<8, 8>(a, vec, s)
-                          : a.E <= 128 ? backward_t<8, 16>(a, vec, s)
-                                       : backward_t<8, 32>(a, vec, s);
+                          : a.E <= 128 ? backward_t<16, 8>(a, vec, s)
+                                       : backward_t<16, 16>(a, vec, s);
     if (e != cudaSuccess || !a.dpes) return e;
     return launch_pdl(k_join_scale_grad, dim3((a.E + 31) / 32), dim3(1024), 0, s, a);
 }

@@ -88,13 +88,13 @@ inline int balance_chunk(int T) {
     return c < 32 ? 32 : c;
 }
 inline int balance_chunks(int T) { return (T + balance_chunk(T) - 1) / balance_chunk(T); }
-// The gradients' chunks: a block of 8 warps each, four blocks on an SM at 64 registers a thread.
-constexpr int kBackwardChunks = 592;
-inline int backward_chunk(int T) {
-    const int c = (T + kBackwardChunks - 1) / kBackwardChunks;
+// The gradients' chunks: a block of 8 warps each, as many as run at once (up to 64 experts four blocks an SM
+// at 64 registers a thread, above two at 120).
+inline int backward_chunk(int T, int E) {
+    const int blocks = E <= 64 ? 592 : 296, c = (T + blocks - 1) / blocks;
     return c < 16 ? 16 : c;
 }
-inline int backward_chunks(int T) { return (T + backward_chunk(T) - 1) / backward_chunk(T); }
+inline int backward_chunks(int T, int E) { return (T + backward_chunk(T, E) - 1) / backward_chunk(T, E); }
 
 struct BalanceArgs {
     const float* logits;        // [T, E]

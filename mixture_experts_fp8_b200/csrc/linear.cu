@@ -343,18 +343,23 @@ cudaError_t launch_linear_fp32(const LinearArgs& a, const LinearMaps& m, int num
     return launch_pair(k_linear_fp32, kThreads, kSmemBytes, a, m, num_sms, s);
 }
 
-// The narrow kernel takes a product when its estimated time is below the pair kernel's: both are
-// (rounds of CTAs over the SMs) x (K groups of a CTA) x (cycles of a group).
+// The narrow kernel takes a product when its estimated time is below the pair kernel's.  Both estimates
+// (ns) are a start and a time per K group of the busiest SM, fitted to products of 16 to 2048 tokens with
+// K 512 to 7168 and N 512 to 12288 in a graph: narrow 3.3 us (32 tokens) or 5 us (64) for each round of two
+// CTAs an SM, 0.32 us a group (block-scaled 0.26); pair 3.2 us and 0.28 us a group (4.2 us, 0.225 us).  At
+// 64 x 2816 x 2816 that is 6.9 against 9.4 us (measured 7.8 and 9.5), at 256 tokens 12 against 9.4 (12.6
+// and 9.8).
 bool linear_is_narrow(int T, int N, int K, int recipe, int num_sms) {
     const long long KB = K / kTileK;
     const int nt = linear_narrow_tokens(T), split = linear_narrow_split(T, N, K, num_sms);
-    const long long tiles = static_cast<long long>((N + kTileM - 1) / kTileM) * ((T + nt - 1) / nt);
+    const long long ctas = static_cast<long long>((N + kTileM - 1) / kTileM) * ((T + nt - 1) / nt) * split;
     if ((T + nt - 1) / nt > 65535) return false;       // grid.z
     const int wn = recipe == 0 ? kPairN0 : kPairNX;
     const long long units = static_cast<long long>((N + wn - 1) / wn) * ((T + kPairM - 1) / kPairM);
     const long long pairs = num_sms / 2;
-    const long long narrow = (tiles * split + num_sms - 1) / num_sms * ((KB + split - 1) / split) * 700;
-    const long long wide = (units + pairs - 1) / pairs * KB * (recipe == 0 ? 900 : 700);
+    const long long narrow = (ctas + 2 * num_sms - 1) / (2 * num_sms) * (nt == 32 ? 3300 : 5000) +
+                             (ctas + num_sms - 1) / num_sms * ((KB + split - 1) / split) * (recipe == 0 ? 320 : 260);
+    const long long wide = (recipe == 0 ? 3200 : 4200) + (units + pairs - 1) / pairs * KB * (recipe == 0 ? 280 : 225);
     return narrow < wide;
 }
 

@@ -722,7 +722,7 @@ int balance_layout(const moe_config_t* c, int32_t num_seqs, const char* who, Bal
     L->ticket = 256;                                    // the status word comes first
     L->seq_loss = 512;
     L->part_p = align_up(L->seq_loss + 4 * static_cast<size_t>(num_seqs) * ((E + 31) / 32), 256);
-    L->part_n = align_up(L->part_p + 4 * std::max(slots, static_cast<size_t>(moe::backward_chunks(c->num_tokens))) * E, 256);
+    L->part_n = align_up(L->part_p + 4 * std::max(slots, static_cast<size_t>(moe::backward_chunks(c->num_tokens, c->num_experts))) * E, 256);
     L->total = align_up(L->part_n + 4 * slots * (E + 2), 256);
     return MOE_OK;
 }
@@ -958,7 +958,7 @@ int moe_route_backward(const moe_config_t* cfg, const float* router_logits, cons
                              seq_tokens, token_mask, seq_offsets, d_logits, d_per_expert_scale,
                              d_per_expert_scale ? reinterpret_cast<float*>(ws + L.part_p) : nullptr, T,
                              cfg->num_experts, cfg->top_k, num_seqs, cfg->routing, cfg->renormalize != 0,
-                             moe::backward_chunk(T), moe::backward_chunks(T), cfg->routed_scaling_factor, coef};
+                             moe::backward_chunk(T, cfg->num_experts), moe::backward_chunks(T, cfg->num_experts), cfg->routed_scaling_factor, coef};
     MOE_CUDA_TRY(moe::launch_route_backward(a, static_cast<cudaStream_t>(stream)));
     return ok();
 }
