@@ -344,7 +344,8 @@ int moe_combine_rows(const moe_config_t *cfg, const float *o_rows, int32_t num_r
  * Around the layer.  These entry points have no counterpart on the pages; they are what a user of
  * the layer calls next to it: the residual addition and RMS norm in front of it, the dense FP8
  * products of the same block, and what its router is trained with.  They follow the conventions
- * above; a row's output does not depend on the other rows' values.
+ * above; a row's output does not depend on the other rows' values.  Buffers do not overlap unless an
+ * entry point says that they may.
  *
  * Quantized rows: E4M3 codes [rows, cols] and K-block-major scales, one 4-byte word per (128-column
  * block, row), [cols/128][scale_rows]: the fp32 scale (recipe 0), or the block's four UE8M0 bytes,

@@ -454,6 +454,22 @@ def _arg(t, name: str, shape, dtype, dev):
             f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
+def _new(like, shape, dtype, stream):
+    """A tensor that the call allocates; on a stream other than the current one the allocator is told."""
+    t = like.new_empty(shape, dtype=dtype)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _like(t, stream, dtype=None):
+    """_new of t's shape (and type)."""
+    t = torch.empty_like(t, dtype=dtype)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 def _workspace_arg(t, dev):
     if t.get_device() != dev or not t.is_contiguous():
         _refuse(f"workspace must be a contiguous tensor on cuda:{dev}")
@@ -495,12 +511,11 @@ def add_rms_norm(cfg: Config, x, norm_weight, rms_eps: float, residual=None, res
     elif residual.dtype not in (torch.bfloat16, torch.float32):
         _refuse(f"residual must be bfloat16 or float32, got {residual.dtype}")
     elif residual_out is None:
-        residual_out = torch.empty_like(residual)
+        residual_out = _like(residual, stream)
     if y is None and want_y:
-        y = torch.empty_like(x)
+        y = _like(x, stream)
     if quantized is None and want_quantized:
-        quantized = (torch.empty_like(x, dtype=torch.uint8),
-                     norm_weight.new_empty((H // 128, (T + 135) // 4 * 4), dtype=torch.int32))
+        quantized = (_like(x, stream, torch.uint8), _new(x, (H // 128, (T + 135) // 4 * 4), torch.int32, stream))
     rt = None if residual is None else residual.dtype
     c = cfg.c()
     _check(_load().moe_add_rms_norm(
@@ -523,7 +538,7 @@ def transform_linear_weights(cfg: LinearConfig, w, w_scale, stream=None):
     [K/32, N]) -> (w_t, ws_t) uint8 device tensors, for any num_tokens."""
     dev = _device_of(w, "w")
     K, N, g = cfg.in_features, cfg.out_features, 128 if cfg.recipe == 0 else 32
-    outs = [w.new_empty(n, dtype=torch.uint8) for n in transformed_linear_size(cfg)]
+    outs = [_new(w, n, torch.uint8, stream) for n in transformed_linear_size(cfg)]
     c = cfg.c()
     _check(_load().moe_transform_linear_weights(
         ctypes.byref(c), _arg(w, "w", (K, N // 2 if cfg.recipe == 2 else N), torch.uint8, dev),
@@ -553,10 +568,10 @@ def linear(cfg: LinearConfig, weights, x=None, quantized=None, bias=None, residu
     dev = _device_of(x if quantized is None else quantized[0], "x")
     T, K, N = cfg.num_tokens, cfg.in_features, cfg.out_features
     if y is None:
-        y = weights[0].new_empty((T, N), dtype=torch.bfloat16)
+        y = _new(weights[0], (T, N), torch.bfloat16, stream)
     if workspace is None:
         n = linear_workspace_size(cfg) if quantized is None else MOE_LINEAR_STATUS_BYTES
-        workspace = y.new_empty(n, dtype=torch.uint8)
+        workspace = _new(y, n, torch.uint8, stream)
     c = cfg.c()
     w_t, ws_t = weights
     w_bytes = K * N // (2 if cfg.recipe == 2 else 1)
@@ -602,10 +617,11 @@ def balance_loss(cfg: Config, router_logits, topk_idx, coef: float, seq_offsets=
     dev = _device_of(router_logits, "router_logits")
     T, E = cfg.num_tokens, cfg.num_experts
     mask, off, S = _seq_args(cfg, token_mask, seq_offsets, dev)
-    counts, tokens = topk_idx.new_empty((S, E)), topk_idx.new_empty(S + 1)
-    mean, loss = router_logits.new_empty((S, E)), router_logits.new_empty(1)
+    i32, f32 = torch.int32, torch.float32
+    counts, tokens = _new(router_logits, (S, E), i32, stream), _new(router_logits, S + 1, i32, stream)
+    mean, loss = _new(router_logits, (S, E), f32, stream), _new(router_logits, 1, f32, stream)
     if workspace is None:
-        workspace = new_balance_workspace(cfg, S, router_logits.device)
+        workspace = _new(router_logits, balance_workspace_size(cfg, S), torch.uint8, stream)
     c = cfg.c()
     _check(_load().moe_balance_loss(
         ctypes.byref(c), _arg(router_logits, "router_logits", (T, E), torch.float32, dev),
@@ -625,12 +641,12 @@ def route_backward(cfg: Config, router_logits, topk_idx, d_topk_weights=None, pe
     f32 = torch.float32
     mask, off, S = _seq_args(cfg, token_mask, seq_offsets, dev)
     if d_logits is None:
-        d_logits = torch.empty_like(router_logits)
+        d_logits = _like(router_logits, stream)
     d_scale, ws = None, (None, 0)
     if per_expert_scale is not None:
-        d_scale = torch.empty_like(per_expert_scale)
+        d_scale = _like(per_expert_scale, stream)
         if workspace is None:
-            workspace = new_balance_workspace(cfg, S, router_logits.device)
+            workspace = _new(router_logits, balance_workspace_size(cfg, S), torch.uint8, stream)
         ws = _workspace_arg(workspace, dev)
     c = cfg.c()
     _check(_load().moe_route_backward(
