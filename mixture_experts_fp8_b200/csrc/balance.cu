@@ -375,31 +375,37 @@ __global__ void __launch_bounds__(kRWarps * 32) k_route_backward(RouteBackwardAr
             return MODE == kSigmoid ? sigmoid(l, s) : MODE == kRenorm ? exp_neg(l - sm) : exp_neg(l - m) * rz;
         };
         x0 *= a.rsf;
-        const float u0 = e0 >= 0 ? raw(l0) : 0.0f, du0 = x0 * scale0;
-        float sz = u0, sd = u0 * du0;
+        const float v0 = e0 >= 0 ? raw(l0) : 0.0f, du0 = x0 * scale0;
+        float sz = v0;
         if (more)
             for (int j = gl + G; j < a.K; j += G) {
                 const int e = __ldg(idx + j);
-                if (e < 0 || e >= a.E) continue;
-                const float v = raw(__ldg(row + e));
-                sz += v;
-                sd += v * (__ldg(dw + j) * a.rsf * (a.pes ? __ldg(a.pes + e) : 1.0f));
+                if (e >= 0 && e < a.E) sz += raw(__ldg(row + e));
             }
-        if (MODE == kDirect) {
-            sz = 1.0f;
-        } else {
-            sz = 1.0f / group_sum<G>(sz);
-            sd = group_sum<G>(sd) * sz;
+        // u = v / sz by division: a single slot has exactly u = 1 and no gradient through its weight
+        sz = MODE == kDirect ? 1.0f : group_sum<G>(sz);
+        auto weight = [&](float v) { return MODE == kDirect ? v : __fdiv_rn(v, sz); };
+        const float u0 = weight(v0);
+        float sd = 0.0f;
+        if (MODE != kDirect) {
+            sd = e0 >= 0 ? u0 * du0 : 0.0f;
+            if (more)
+                for (int j = gl + G; j < a.K; j += G) {
+                    const int e = __ldg(idx + j);
+                    if (e >= 0 && e < a.E)
+                        sd += weight(raw(__ldg(row + e))) * (__ldg(dw + j) * a.rsf * (a.pes ? __ldg(a.pes + e) : 1.0f));
+                }
+            sd = group_sum<G>(sd);
         }
-        auto term = [&](float v, float du) {           // what a slot adds to its expert
-            return MODE == kDirect ? du : MODE == kSigmoid ? (du - sd) * sz : v * sz * (du - sd);
+        auto term = [&](float u, float du) {           // what a slot adds to its expert
+            return MODE == kDirect ? du : MODE == kSigmoid ? (du - sd) / sz : u * (du - sd);
         };
         if (wts && e0 >= 0) add[e0] = term(u0, du0);   // ids of a token are distinct: plain stores
         if (more)
             for (int j = gl + G; j < a.K; j += G) {
                 const int e = __ldg(idx + j);
                 if (e >= 0 && e < a.E)
-                    add[e] = term(raw(__ldg(row + e)), __ldg(dw + j) * a.rsf * (a.pes ? __ldg(a.pes + e) : 1.0f));
+                    add[e] = term(weight(raw(__ldg(row + e))), __ldg(dw + j) * a.rsf * (a.pes ? __ldg(a.pes + e) : 1.0f));
             }
         __syncwarp();
 
@@ -437,14 +443,14 @@ __global__ void __launch_bounds__(kRWarps * 32) k_route_backward(RouteBackwardAr
         // ---- back to zero, and the scale's gradient
         if (wts && e0 >= 0) {
             add[e0] = 0.0f;
-            if (a.dpes) dscale[e0] += x0 * (u0 * sz);
+            if (a.dpes) dscale[e0] += x0 * u0;
         }
         if (more) {
             for (int j = gl + G; j < a.K; j += G) {
                 const int e = __ldg(idx + j);
                 if (e < 0 || e >= a.E) continue;
                 add[e] = 0.0f;
-                if (a.dpes) dscale[e] += __ldg(dw + j) * a.rsf * (raw(__ldg(row + e)) * sz);
+                if (a.dpes) dscale[e] += __ldg(dw + j) * a.rsf * weight(raw(__ldg(row + e)));
             }
         }
         __syncwarp();

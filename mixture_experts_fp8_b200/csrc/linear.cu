@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int nb = u / mt, mb = u - nb * mt;
             const int t0 = mb * kPairM + static_cast<int>(rank) * kTileM + quad * 32, c0 = nb * kN + 32 * qtr;
             epilogue_store_wait();                     // the last tile's store has read the subtile
-            epilogue_residual<kSubCols0, 1>(p, sub, t0, c0);
+            epilogue_residual<kSubCols0>(p, sub, t0, c0);
             float2 acc2[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc2[i] = make_float2(0.0f, 0.0f);
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             epilogue_residual_wait(p);
             epilogue_sub<kSubCols0>(p, sub, reinterpret_cast<float*>(acc2), c0);
-            epilogue_store<kSubCols0, 1>(p, &tmY, sub, t0, c0);
+            epilogue_store<kSubCols0>(p, &tmY, sub, t0, c0);
         }
         epilogue_drain();
     }

@@ -78,9 +78,36 @@ __device__ __forceinline__ void sts_u32(uint32_t a, uint32_t v) {
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 
-// Fetch the residual of rows t0 .. +31, columns c0 .. c0 + C SUBS - 1 into the warp's subtiles at sub.
+__device__ __forceinline__ void sts_u16(uint32_t a, uint16_t v) {
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(v) : "memory");
+}
+
+// A lane's way over the 32-bit words of a subtile, every 32nd of its row-by-row order: row r, word w.
+template <int C>
+struct SubWalk {
+    int r, w, lane, i = 0;
+    __device__ __forceinline__ explicit SubWalk(int lane_) : r(lane_ / (C / 2)), w(lane_ % (C / 2)), lane(lane_) {}
+    __device__ __forceinline__ uint32_t offset() const {
+        return C == 48 ? static_cast<uint32_t>(lane * 4 + 128 * i) : Sub<C>::word(r, w);   // 48: rows lie end to end
+    }
+    __device__ __forceinline__ void next() {
+        ++i;
+        if (C == 48) {                                  // 32 = 24 + 8 words on
+            w += 8;
+            r += 1;
+            if (w >= 24) {
+                w -= 24;
+                r += 1;
+            }
+        } else {
+            r += 2;
+        }
+    }
+};
+
+// Fetch the residual of rows t0 .. +31, columns c0 .. c0 + C - 1 into the warp's subtile at sub.
 // N a multiple of 8: asynchronous, 16 bytes a lane (epilogue_residual_wait before use).
-template <int C, int SUBS>
+template <int C>
 __device__ __forceinline__ void epilogue_residual(const LinearArgs& p, uint32_t sub, int t0, int c0) {
     using S = Sub<C>;
     if (!p.res) return;
@@ -90,34 +117,44 @@ __device__ __forceinline__ void epilogue_residual(const LinearArgs& p, uint32_t 
         if (t < p.T) {
             const __nv_bfloat16* row = p.res + static_cast<size_t>(t) * p.N;
 #pragma unroll
-            for (int j = 0; j < S::chunks * SUBS; ++j) {
+            for (int j = 0; j < S::chunks; ++j) {
                 const int c = c0 + 8 * j;
                 if (c < p.N)
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(
-                                     sub + (j / S::chunks) * S::bytes + S::chunk(lane, j % S::chunks)),
-                                 "l"(row + c)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(sub + S::chunk(lane, j)), "l"(row + c)
                                  : "memory");
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         return;
     }
-    constexpr int kWords = S::words * SUBS;             // of a row
-    const bool even = p.N % 2 == 0;
-#pragma unroll 8
-    for (int i = lane; i < 32 * kWords; i += 32) {
-        const int r = i / kWords, w = i % kWords, t = t0 + r, c = c0 + 2 * w;
-        if (t >= p.T || c >= p.N) continue;
-        const __nv_bfloat16* q = p.res + static_cast<size_t>(t) * p.N + c;
-        uint32_t v;
-        if (even) {
-            v = *reinterpret_cast<const uint32_t*>(q);
-        } else {
-            const uint16_t lo = *reinterpret_cast<const uint16_t*>(q);
-            const uint16_t hi = c + 1 < p.N ? *reinterpret_cast<const uint16_t*>(q + 1) : uint16_t(0);
-            v = lo | (static_cast<uint32_t>(hi) << 16);
+    const __nv_bfloat16* base = p.res + static_cast<size_t>(t0) * p.N + c0;
+    SubWalk<C> at(lane);
+#pragma unroll 1
+    for (int i = 0; i < S::words; i += 8) {            // eight words a lane in flight
+        uint32_t v[8];
+        SubWalk<C> to = at;
+#pragma unroll
+        for (int k = 0; k < 8; ++k, at.next()) {
+            v[k] = 0;
+            // a row that starts at an odd element is read a column further on, so that its words are aligned
+            const int odd = p.N & (t0 + at.r) & 1, c = c0 + 2 * at.w + odd;
+            if (t0 + at.r >= p.T || c >= p.N) continue;
+            const __nv_bfloat16* q = base + at.r * p.N + 2 * at.w + odd;
+            if (c + 1 < p.N && (!odd || at.w + 1 < S::words)) v[k] = *reinterpret_cast<const uint32_t*>(q);
+            else v[k] = *reinterpret_cast<const uint16_t*>(q);
         }
-        sts_u32(sub + (w / S::words) * S::bytes + S::word(r, w % S::words), v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k, to.next()) {
+            const uint32_t off = to.offset();
+            if (p.N & (t0 + to.r) & 1) {
+                sts_u16(sub + off + 2, static_cast<uint16_t>(v[k]));
+                if (to.w + 1 < S::words) sts_u16(sub + S::word(to.r, to.w + 1), static_cast<uint16_t>(v[k] >> 16));
+                if (to.w == 0 && t0 + to.r < p.T)
+                    sts_u16(sub + off, *reinterpret_cast<const uint16_t*>(base + to.r * p.N));
+            } else {
+                sts_u32(sub + off, v[k]);
+            }
+        }
     }
 }
 __device__ __forceinline__ void epilogue_residual_wait(const LinearArgs& p) {
@@ -160,42 +197,43 @@ __device__ __forceinline__ void epilogue_sub(const LinearArgs& p, uint32_t sub, 
     }
 }
 
-// Store the warp's SUBS subtiles (rows t0 .., columns c0 ..) to y.  tmY: y [T, N] bf16, box C x 32; used
-// when N is a multiple of 8, and then asynchronous (epilogue_store_wait).
-template <int C, int SUBS>
+// Store the warp's subtile (rows t0 .., columns c0 ..) to y.  tmY: y [T, N] bf16, box C x 32; used when N is
+// a multiple of 8, and then asynchronous (epilogue_store_wait).
+template <int C>
 __device__ __forceinline__ void epilogue_store(const LinearArgs& p, const CUtensorMap* tmY, uint32_t sub, int t0, int c0) {
-    using S = Sub<C>;
     const int lane = threadIdx.x & 31;
     if (p.N % 8 == 0) {
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0 && t0 < p.T) {
-#pragma unroll
-            for (int k = 0; k < SUBS; ++k)
-                if (c0 + C * k < p.N)
-                    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                                     reinterpret_cast<uint64_t>(tmY)),
-                                 "r"(sub + k * S::bytes), "r"(c0 + C * k), "r"(t0)
-                                 : "memory");
+        if (lane == 0 && t0 < p.T && c0 < p.N) {
+            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                             reinterpret_cast<uint64_t>(tmY)),
+                         "r"(sub), "r"(c0), "r"(t0)
+                         : "memory");
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
         return;
     }
+    using S = Sub<C>;
     __syncwarp();
-    constexpr int kWords = S::words * SUBS;
-    const bool even = p.N % 2 == 0;
+    __nv_bfloat16* base = p.y + static_cast<size_t>(t0) * p.N + c0;
+    SubWalk<C> at(lane);
 #pragma unroll 8
-    for (int i = lane; i < 32 * kWords; i += 32) {
-        const int r = i / kWords, w = i % kWords, t = t0 + r, c = c0 + 2 * w;
-        const uint32_t v = lds_u32(sub + (w / S::words) * S::bytes + S::word(r, w % S::words));
-        if (t >= p.T || c >= p.N) continue;
-        __nv_bfloat16* q = p.y + static_cast<size_t>(t) * p.N + c;
-        if (even) {
-            *reinterpret_cast<uint32_t*>(q) = v;
-        } else {
-            *reinterpret_cast<uint16_t*>(q) = static_cast<uint16_t>(v);
-            if (c + 1 < p.N) *reinterpret_cast<uint16_t*>(q + 1) = static_cast<uint16_t>(v >> 16);
+    for (int i = 0; i < S::words; ++i, at.next()) {
+        // a row that starts at an odd element is written a column further on, so that its words are aligned
+        // (two halves of a word apart would make every sector a partial write)
+        const int odd = p.N & (t0 + at.r) & 1, c = c0 + 2 * at.w + odd;
+        uint32_t v = lds_u32(sub + at.offset());
+        __nv_bfloat16* q = base + at.r * p.N + 2 * at.w + odd;
+        if (t0 + at.r >= p.T || c - odd >= p.N) continue;
+        if (odd) {
+            if (at.w == 0) *reinterpret_cast<uint16_t*>(q - 1) = static_cast<uint16_t>(v);
+            if (c >= p.N) continue;
+            v >>= 16;
+            if (at.w + 1 < S::words) v |= lds_u32(sub + S::word(at.r, at.w + 1)) << 16;
         }
+        if (c + 1 < p.N && (!odd || at.w + 1 < S::words)) *reinterpret_cast<uint32_t*>(q) = v;
+        else *reinterpret_cast<uint16_t*>(q) = static_cast<uint16_t>(v);
     }
     __syncwarp();
 }

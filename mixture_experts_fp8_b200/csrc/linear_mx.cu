@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
             const int t0 = mb * kXM + static_cast<int>(rank) * kTileM + quad * 32, c0 = nb * kXN + kSubColsX * qtr;
             const int b = tile & 1;
             epilogue_store_wait();                 // the last tile's store has read the subtile
-            epilogue_residual<kSubColsX, 1>(p, sub, t0, c0);
+            epilogue_residual<kSubColsX>(p, sub, t0, c0);
             const bool ok = mbar_wait(&tfull[b], (tile >> 1) & 1, abort_flag, p.status);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
             for (int i = 0; i < 16; ++i) acc[32 + i] = __uint_as_float(w[i]);
             epilogue_residual_wait(p);
             epilogue_sub<kSubColsX>(p, sub, acc, c0);
-            epilogue_store<kSubColsX, 1>(p, &tmY, sub, t0, c0);
+            epilogue_store<kSubColsX>(p, &tmY, sub, t0, c0);
         }
         epilogue_drain();
     }

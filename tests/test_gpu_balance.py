@@ -245,3 +245,18 @@ def test_training_step_of_the_router():
     assert abs(float(loss) - float(want)) <= REL * float(want) and int(counts.sum()) == T * k
     (want + (rw * dw.cpu().to(F64)).sum()).backward()
     assert torch.all((dl.cpu().to(F64) - ld.grad).abs() <= 64 * U * 2.5 * dw.cpu().abs().sum(1, keepdim=True))
+
+
+def test_one_slot_has_no_gradient_through_its_normalized_weight():
+    """k = 1: the normalized weight is 1 whatever the logit, so only the balance loss moves the logits."""
+    T, E = 300, 24
+    for routing, renorm in ((1, 0), (0, 1)):
+        l, idx, off, mask = problem(T, E, 1, 1, False, 10)
+        cfg = moe.Config(T, 128, 128, E, 1, routing=routing, renormalize=renorm)
+        (_, counts, tokens, _), _ = run_balance(cfg, l, idx, off, mask)
+        args = dict(d_loss=torch.ones(1).cuda(), coef=COEF, expert_counts=counts, seq_tokens=tokens)
+        dw = torch.randn((T, 1), generator=torch.Generator().manual_seed(3)).cuda()
+        a, _ = moe.route_backward(cfg, l.cuda(), idx.cuda(), **args)
+        b, _ = moe.route_backward(cfg, l.cuda(), idx.cuda(), d_topk_weights=dw, **args)
+        c, _ = moe.route_backward(cfg, l.cuda(), idx.cuda(), d_topk_weights=dw)
+        assert torch.equal(a, b) and not c.any()

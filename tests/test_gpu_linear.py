@@ -28,7 +28,8 @@ def check(y, want, off):
 # N: a multiple of 128 and of 256, of 8 only, even, odd, one; T around the tiles
 SHAPES = [(1, 128, 16), (1, 7168, 2048), (2, 256, 1), (31, 384, 250), (33, 512, 96), (64, 2816, 2816), (65, 128, 333),
           (127, 640, 1000), (129, 256, 130), (300, 768, 514), (700, 256, 264), (1237, 768, 1152), (1500, 384, 2050),
-          (1111, 128, 3333), (3000, 256, 1000), (2600, 640, 2112), (520, 1152, 5000)]
+          (1111, 128, 3333), (3000, 256, 1000), (2600, 640, 2112), (520, 1152, 5000),
+          (1301, 256, 4965), (2049, 384, 2227)]
 
 
 @pytest.mark.parametrize("recipe", [0, 1, 2])
