@@ -264,7 +264,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------------ epilogue
         const int quad = warp & 3;                     // TMEM lanes 32*quad .. 32*quad+31
         const int qtr = (warp - kFirstEpiWarp) >> 2;
-        const uint32_t sub = smem_u32(smem + L::out) + static_cast<uint32_t>(warp - kFirstEpiWarp) * Sub<kSubCols0>::bytes;
+        EpiAt at;
+        at.qtr = qtr;
+        at.quad = quad;
+        at.quad_sub = smem_u32(smem + L::out) + static_cast<uint32_t>(quad) * Sub<kSubCols0>::bytes;
+        at.sub = at.quad_sub + static_cast<uint32_t>(4 * qtr) * Sub<kSubCols0>::bytes;
         const uint32_t abort_at = smem_u32(smem + L::misc + 4);
         // the step's barrier, weight scales, TMEM and TMEM barrier (256 columns and 8 bytes apart)
         const uint32_t tf0 = smem_u32(tfull), tf_end = tf0 + 8 * kSteps;
@@ -276,9 +280,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int u = pair; u < total_units && ok; u += pairs) {
             const int nb = u / mt, mb = u - nb * mt;
-            const int t0 = mb * kPairM + static_cast<int>(rank) * kTileM + quad * 32, c0 = nb * kN + 32 * qtr;
+            at.t0 = mb * kPairM + static_cast<int>(rank) * kTileM + quad * 32;
+            at.tile_c0 = nb * kN;
+            at.c0 = at.tile_c0 + 32 * qtr;
+            uint32_t last;
             epilogue_store_wait();                     // the last tile's store has read the subtile
-            epilogue_residual<kSubCols0>(p, sub, t0, c0);
+            epilogue_residual<kSubCols0>(p, at, last);
             float2 acc2[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc2[i] = make_float2(0.0f, 0.0f);
@@ -313,11 +320,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 t_at ^= kStepCols;
                 te_at ^= 8;
             }
-            ok = __all_sync(0xffffffffu, ok);
+            ok = epilogue_residual_wait(p, at, ok);
             if (!ok) break;
-            epilogue_residual_wait(p);
-            epilogue_sub<kSubCols0>(p, sub, reinterpret_cast<float*>(acc2), c0);
-            epilogue_store<kSubCols0>(p, &tmY, sub, t0, c0);
+            epilogue_sub<kSubCols0>(p, at, last, reinterpret_cast<float*>(acc2));
+            epilogue_store<kSubCols0>(p, &tmY, at);
         }
         epilogue_drain();
     }

@@ -42,12 +42,19 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float* v) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// ---- A warp's output goes through shared memory of its own, in subtiles of 32 rows x C columns bf16:
-// the residual is fetched into it while the sums are still being made, each lane replaces its row's
-// residual by the result, and the subtile leaves by a TMA store (N a multiple of 8) or by coalesced
+// ---- The output goes through shared memory, a subtile of 32 rows x C columns bf16 a warp: the residual is
+// fetched into it while the sums are still being made, each lane replaces its row's residual by the
+// result, and the tile leaves by TMA stores (N a multiple of 8; each warp on its own) or by coalesced
 // stores (any N).  Laid out as the TMA box has it: C = 48, rows of 96 bytes as they are (a quarter warp's
 // 16-byte accesses meet two at a time); C = 32, rows of 64 bytes with the 64-byte swizzle (they do not
 // meet; 512-byte aligned).
+//
+// Any N: the four warps with the same 32 rows (a quad, kQuarters subtiles side by side) fetch and store
+// whole tile rows together, 8 rows a warp, by aligned words: a row that starts at an odd element is
+// handled one column apart.  (With each warp storing its own C columns, and odd rows by halves of words,
+// most sectors were partial writes: 12900 cycles to fetch and 8500 to store a 128 x 192 tile.)
+constexpr int kQuarters = 4;
+
 template <int C>
 struct Sub {
     static_assert(C == 32 || C == 48, "subtile columns");
@@ -82,94 +89,91 @@ __device__ __forceinline__ void sts_u16(uint32_t a, uint16_t v) {
     asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(v) : "memory");
 }
 
-// A lane's way over the 32-bit words of a subtile, every 32nd of its row-by-row order: row r, word w.
-template <int C>
-struct SubWalk {
-    int r, w, lane, i = 0;
-    __device__ __forceinline__ explicit SubWalk(int lane_) : r(lane_ / (C / 2)), w(lane_ % (C / 2)), lane(lane_) {}
-    __device__ __forceinline__ uint32_t offset() const {
-        return C == 48 ? static_cast<uint32_t>(lane * 4 + 128 * i) : Sub<C>::word(r, w);   // 48: rows lie end to end
-    }
-    __device__ __forceinline__ void next() {
-        ++i;
-        if (C == 48) {                                  // 32 = 24 + 8 words on
-            w += 8;
-            r += 1;
-            if (w >= 24) {
-                w -= 24;
-                r += 1;
-            }
-        } else {
-            r += 2;
-        }
-    }
+// Where an epilogue warp stands: its subtile and the quad's first (quarters are 4 subtiles apart), its
+// quarter and quad, the rows' first token and the tile's and its own first column.
+struct EpiAt {
+    uint32_t sub, quad_sub;
+    int qtr, quad, t0, tile_c0, c0;
 };
 
-// Fetch the residual of rows t0 .. +31, columns c0 .. c0 + C - 1 into the warp's subtile at sub.
-// N a multiple of 8: asynchronous, 16 bytes a lane (epilogue_residual_wait before use).
+// All four warps of the quad; true when every one says so.  (Each warp calls it once a tile until they
+// leave together, so that none waits for one that has left.)
+__device__ __forceinline__ bool quad_all(const EpiAt& at, bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.cta.red.and.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r) : "r"(1 + at.quad), "r"(static_cast<uint32_t>(ok)) : "memory");
+    return r != 0;
+}
+
+// Word W of tile row r (the quad's 32 rows, 2 columns a word).
 template <int C>
-__device__ __forceinline__ void epilogue_residual(const LinearArgs& p, uint32_t sub, int t0, int c0) {
+__device__ __forceinline__ uint32_t quad_word(const EpiAt& at, int r, int W) {
+    return at.quad_sub + static_cast<uint32_t>(W / Sub<C>::words) * (4 * Sub<C>::bytes) + Sub<C>::word(r, W % Sub<C>::words);
+}
+
+// Begin to fetch the residual (epilogue_residual_wait before use).  The subtiles are free: their stores have
+// read them.  Rows that start at an odd element are fetched one column to the left; `last` then is the
+// lane's row's last element, which that leaves out.
+template <int C>
+__device__ __forceinline__ void epilogue_residual(const LinearArgs& p, const EpiAt& at, uint32_t& last) {
     using S = Sub<C>;
+    last = 0;
     if (!p.res) return;
     const int lane = threadIdx.x & 31;
     if (p.N % 8 == 0) {
-        const int t = t0 + lane;
+        const int t = at.t0 + lane;
         if (t < p.T) {
             const __nv_bfloat16* row = p.res + static_cast<size_t>(t) * p.N;
 #pragma unroll
             for (int j = 0; j < S::chunks; ++j) {
-                const int c = c0 + 8 * j;
+                const int c = at.c0 + 8 * j;
                 if (c < p.N)
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(sub + S::chunk(lane, j)), "l"(row + c)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(at.sub + S::chunk(lane, j)), "l"(row + c)
                                  : "memory");
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         return;
     }
-    const __nv_bfloat16* base = p.res + static_cast<size_t>(t0) * p.N + c0;
-    SubWalk<C> at(lane);
-#pragma unroll 1
-    for (int i = 0; i < S::words; i += 8) {            // eight words a lane in flight
-        uint32_t v[8];
-        SubWalk<C> to = at;
+    constexpr int kLanes = kQuarters * S::words / 32;   // words of a row a lane
+#pragma unroll 2
+    for (int i = 0; i < 8; ++i) {
+        const int r = 8 * at.qtr + i, t = at.t0 + r;
+        if (t >= p.T) break;
+        const int odd = p.N & t & 1;
+        const __nv_bfloat16* row = p.res + static_cast<size_t>(t) * p.N + (at.tile_c0 - odd);
 #pragma unroll
-        for (int k = 0; k < 8; ++k, at.next()) {
-            v[k] = 0;
-            // a row that starts at an odd element is read a column further on, so that its words are aligned
-            const int odd = p.N & (t0 + at.r) & 1, c = c0 + 2 * at.w + odd;
-            if (t0 + at.r >= p.T || c >= p.N) continue;
-            const __nv_bfloat16* q = base + at.r * p.N + 2 * at.w + odd;
-            if (c + 1 < p.N && (!odd || at.w + 1 < S::words)) v[k] = *reinterpret_cast<const uint32_t*>(q);
-            else v[k] = *reinterpret_cast<const uint16_t*>(q);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k, to.next()) {
-            const uint32_t off = to.offset();
-            if (p.N & (t0 + to.r) & 1) {
-                sts_u16(sub + off + 2, static_cast<uint16_t>(v[k]));
-                if (to.w + 1 < S::words) sts_u16(sub + S::word(to.r, to.w + 1), static_cast<uint16_t>(v[k] >> 16));
-                if (to.w == 0 && t0 + to.r < p.T)
-                    sts_u16(sub + off, *reinterpret_cast<const uint16_t*>(base + to.r * p.N));
-            } else {
-                sts_u32(sub + off, v[k]);
-            }
+        for (int k = 0; k < kLanes; ++k) {
+            const int W = 32 * k + lane, c = at.tile_c0 - odd + 2 * W;     // -1: the row before's last element
+            const uint32_t dst = quad_word<C>(at, r, W);
+            if (c + 1 < p.N)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(row + 2 * W) : "memory");
+            else if (c < p.N)
+                sts_u16(dst, *reinterpret_cast<const uint16_t*>(row + 2 * W));
         }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    const int t = at.t0 + lane, c = at.c0 + C - 1;
+    if (t < p.T && (p.N & t & 1) && c < p.N)
+        last = *reinterpret_cast<const uint16_t*>(p.res + static_cast<size_t>(t) * p.N + c);
 }
-__device__ __forceinline__ void epilogue_residual_wait(const LinearArgs& p) {
-    if (p.res && p.N % 8 == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncwarp();
+// The residual is there, and (any N) the quad's warps are; false when one of them gave up.
+__device__ __forceinline__ bool epilogue_residual_wait(const LinearArgs& p, const EpiAt& at, bool ok) {
+    if (p.res) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (p.N % 8) return quad_all(at, ok);
+    return __all_sync(0xffffffffu, ok);
 }
 
-// The lane's row of one subtile, columns c0 .., from acc.
+// The lane's row of the warp's subtile from acc.
 template <int ACT, int C>
-__device__ __forceinline__ void epilogue_sub_t(const LinearArgs& p, uint32_t sub, float* acc, int c0) {
+__device__ __forceinline__ void epilogue_sub_t(const LinearArgs& p, const EpiAt& at, uint32_t last, float* acc) {
     const int lane = threadIdx.x & 31;
+    const bool odd = p.N & (at.t0 + lane) & 1;
 #pragma unroll
     for (int j = 0; j < Sub<C>::chunks; ++j) {
         float* v = acc + 8 * j;
-        const int c = c0 + 8 * j;
+        const int c = at.c0 + 8 * j;
         if (p.bias) {
             if (c + 8 <= p.N) {
                 add_bias8(v, ld_nc_u4(reinterpret_cast<const uint4*>(p.bias + c)));
@@ -181,61 +185,69 @@ __device__ __forceinline__ void epilogue_sub_t(const LinearArgs& p, uint32_t sub
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = linear_act_t<ACT>(v[i]);
-        const uint32_t at = sub + Sub<C>::chunk(lane, j);
-        if (p.res) add_bias8(v, lds_u4(at));
-        sts_u4(at, pack_bf16x8(v));
+        const uint32_t to = at.sub + Sub<C>::chunk(lane, j);
+        if (p.res) {
+            uint4 r = lds_u4(to);
+            if (odd) {                                  // one column to the left: the next chunk's first word has the last
+                const uint32_t n = j + 1 < Sub<C>::chunks ? lds_u32(at.sub + Sub<C>::chunk(lane, j + 1)) : last;
+                r = make_uint4(__funnelshift_r(r.x, r.y, 16), __funnelshift_r(r.y, r.z, 16), __funnelshift_r(r.z, r.w, 16),
+                               __funnelshift_r(r.w, n, 16));
+            }
+            add_bias8(v, r);
+        }
+        sts_u4(to, pack_bf16x8(v));
     }
 }
 template <int C>
-__device__ __forceinline__ void epilogue_sub(const LinearArgs& p, uint32_t sub, float* acc, int c0) {
+__device__ __forceinline__ void epilogue_sub(const LinearArgs& p, const EpiAt& at, uint32_t last, float* acc) {
     switch (p.act) {
-        case 1: return epilogue_sub_t<1, C>(p, sub, acc, c0);
-        case 2: return epilogue_sub_t<2, C>(p, sub, acc, c0);
-        case 3: return epilogue_sub_t<3, C>(p, sub, acc, c0);
-        case 4: return epilogue_sub_t<4, C>(p, sub, acc, c0);
-        default: return epilogue_sub_t<0, C>(p, sub, acc, c0);
+        case 1: return epilogue_sub_t<1, C>(p, at, last, acc);
+        case 2: return epilogue_sub_t<2, C>(p, at, last, acc);
+        case 3: return epilogue_sub_t<3, C>(p, at, last, acc);
+        case 4: return epilogue_sub_t<4, C>(p, at, last, acc);
+        default: return epilogue_sub_t<0, C>(p, at, last, acc);
     }
 }
 
-// Store the warp's subtile (rows t0 .., columns c0 ..) to y.  tmY: y [T, N] bf16, box C x 32; used when N is
-// a multiple of 8, and then asynchronous (epilogue_store_wait).
+// Store to y.  tmY: y [T, N] bf16, box C x 32; used when N is a multiple of 8, and then asynchronous.
 template <int C>
-__device__ __forceinline__ void epilogue_store(const LinearArgs& p, const CUtensorMap* tmY, uint32_t sub, int t0, int c0) {
+__device__ __forceinline__ void epilogue_store(const LinearArgs& p, const CUtensorMap* tmY, const EpiAt& at) {
+    using S = Sub<C>;
     const int lane = threadIdx.x & 31;
     if (p.N % 8 == 0) {
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0 && t0 < p.T && c0 < p.N) {
+        if (lane == 0 && at.t0 < p.T && at.c0 < p.N) {
             asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
                              reinterpret_cast<uint64_t>(tmY)),
-                         "r"(sub), "r"(c0), "r"(t0)
+                         "r"(at.sub), "r"(at.c0), "r"(at.t0)
                          : "memory");
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
         return;
     }
-    using S = Sub<C>;
-    __syncwarp();
-    __nv_bfloat16* base = p.y + static_cast<size_t>(t0) * p.N + c0;
-    SubWalk<C> at(lane);
-#pragma unroll 8
-    for (int i = 0; i < S::words; ++i, at.next()) {
-        // a row that starts at an odd element is written a column further on, so that its words are aligned
-        // (two halves of a word apart would make every sector a partial write)
-        const int odd = p.N & (t0 + at.r) & 1, c = c0 + 2 * at.w + odd;
-        uint32_t v = lds_u32(sub + at.offset());
-        __nv_bfloat16* q = base + at.r * p.N + 2 * at.w + odd;
-        if (t0 + at.r >= p.T || c - odd >= p.N) continue;
-        if (odd) {
-            if (at.w == 0) *reinterpret_cast<uint16_t*>(q - 1) = static_cast<uint16_t>(v);
-            if (c >= p.N) continue;
-            v >>= 16;
-            if (at.w + 1 < S::words) v |= lds_u32(sub + S::word(at.r, at.w + 1)) << 16;
+    quad_all(at, true);                                 // the quad's rows are whole
+    constexpr int kLanes = kQuarters * S::words / 32, kRowWords = kQuarters * S::words;
+#pragma unroll 2
+    for (int i = 0; i < 8; ++i) {
+        const int r = 8 * at.qtr + i, t = at.t0 + r;
+        if (t >= p.T) break;
+        const int odd = p.N & t & 1;
+        __nv_bfloat16* row = p.y + static_cast<size_t>(t) * p.N + at.tile_c0;
+#pragma unroll
+        for (int k = 0; k < kLanes; ++k) {
+            const int W = 32 * k + lane, c = at.tile_c0 + 2 * W + odd;
+            uint32_t v = lds_u32(quad_word<C>(at, r, W));
+            if (odd) {
+                if (W == 0 && at.tile_c0 < p.N) *reinterpret_cast<uint16_t*>(row) = static_cast<uint16_t>(v);
+                v >>= 16;
+                if (W + 1 < kRowWords) v |= lds_u32(quad_word<C>(at, r, W + 1)) << 16;
+            }
+            if (c + 1 < p.N && (!odd || W + 1 < kRowWords)) *reinterpret_cast<uint32_t*>(row + 2 * W + odd) = v;
+            else if (c < p.N) *reinterpret_cast<uint16_t*>(row + 2 * W + odd) = static_cast<uint16_t>(v);
         }
-        if (c + 1 < p.N && (!odd || at.w + 1 < S::words)) *reinterpret_cast<uint32_t*>(q) = v;
-        else *reinterpret_cast<uint16_t*>(q) = static_cast<uint16_t>(v);
     }
-    __syncwarp();
+    quad_all(at, true);                                 // the subtiles are free again
 }
 // Before the subtiles are written again: the stores have read them.
 __device__ __forceinline__ void epilogue_store_wait() {

@@ -250,22 +250,29 @@ __global__ void __launch_bounds__(kXThreads, 1)
         // ---------------------------------------------------------------------- epilogue
         const int quad = warp & 3;
         const int qtr = (warp - 4) >> 2;           // columns 48 qtr .. of the tile
-        const uint32_t sub = smem_u32(smem + XL::out) + static_cast<uint32_t>(warp - 4) * Sub<kSubColsX>::bytes;
+        EpiAt at;
+        at.qtr = qtr;
+        at.quad = quad;
+        at.quad_sub = smem_u32(smem + XL::out) + static_cast<uint32_t>(quad) * Sub<kSubColsX>::bytes;
+        at.sub = at.quad_sub + static_cast<uint32_t>(4 * qtr) * Sub<kSubColsX>::bytes;
         uint32_t tile = 0;
         for (int u = pair; u < total_units; u += pairs, ++tile) {
             const int nb = u / mt, mb = u - nb * mt;
-            const int t0 = mb * kXM + static_cast<int>(rank) * kTileM + quad * 32, c0 = nb * kXN + kSubColsX * qtr;
+            at.t0 = mb * kXM + static_cast<int>(rank) * kTileM + quad * 32;
+            at.tile_c0 = nb * kXN;
+            at.c0 = at.tile_c0 + kSubColsX * qtr;
             const int b = tile & 1;
-            epilogue_store_wait();                 // the last tile's store has read the subtile
-            epilogue_residual<kSubColsX>(p, sub, t0, c0);
+            uint32_t last;
+            epilogue_store_wait();                 // the last tile's stores have read the subtile
+            epilogue_residual<kSubColsX>(p, at, last);
             const bool ok = mbar_wait(&tfull[b], (tile >> 1) & 1, abort_flag, p.status);
-            if (!__all_sync(0xffffffffu, ok)) break;
+            if (!epilogue_residual_wait(p, at, ok)) break;
             tc_fence_after();
-            const uint32_t at = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
-                                static_cast<uint32_t>(b * kXN + kSubColsX * qtr);
+            const uint32_t from = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
+                                  static_cast<uint32_t>(b * kXN + kSubColsX * qtr);
             uint32_t v[32], w[16];
-            MOE_TMEM_LD32(at, v);
-            MOE_TMEM_LD16(at + 32, w);
+            MOE_TMEM_LD32(from, v);
+            MOE_TMEM_LD16(from + 32, w);
             MOE_TMEM_WAIT_LD(v);
             MOE_TMEM_WAIT_LD16(w);
             tc_fence_before();
@@ -276,9 +283,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
             for (int i = 0; i < 32; ++i) acc[i] = __uint_as_float(v[i]);
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[32 + i] = __uint_as_float(w[i]);
-            epilogue_residual_wait(p);
-            epilogue_sub<kSubColsX>(p, sub, acc, c0);
-            epilogue_store<kSubColsX>(p, &tmY, sub, t0, c0);
+            epilogue_sub<kSubColsX>(p, at, last, acc);
+            epilogue_store<kSubColsX>(p, &tmY, at);
         }
         epilogue_drain();
     }
