@@ -2,8 +2,10 @@
 
 Thin Python binding over ``libmoefp8.so`` (C ABI in ``include/moefp8.h``).  This module only
 marshals arguments: every step of the layer runs in the library's sm_100a kernels.  PyTorch
-supplies device memory and streams.  There is no CPU fallback: if the library is missing it is
-built in-tree with nvcc, and if that is impossible, importing this package fails.
+supplies device memory and streams.  The operators around the layer run in a few microseconds
+each, so theirs are marshalled by ``_binding.so`` (``csrc/binding.cpp``).  There is no CPU
+fallback: if the library is missing it is built in-tree with nvcc, and if that is impossible,
+importing this package fails.
 
 Entry points (same names as the C ABI):
     check_config, transformed_weights_size, transform_weights, workspace_size,
@@ -195,6 +197,27 @@ def _load():
 
 def lib():
     return _load()
+
+
+_bound = None
+
+
+def _bind():
+    """The module that marshals the operators around the layer, given the loaded library's entry points."""
+    global _bound
+    L = _load()
+    with _lock:
+        if _bound is None:
+            path = os.path.join(_PKG, "_binding.so")
+            if not os.path.exists(path):
+                from . import build as _build
+                _build.build_binding()
+            from . import _binding as m
+            m.init(MoeError, *[ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
+                "moe_last_error", "moe_add_rms_norm", "moe_linear", "moe_linear_workspace_size", "moe_balance_loss",
+                "moe_balance_workspace_size", "moe_route_backward")])
+            _bound = m
+    return _bound
 
 
 def _check(rc: int):
@@ -462,20 +485,6 @@ def _new(like, shape, dtype, stream):
     return t
 
 
-def _like(t, stream, dtype=None):
-    """_new of t's shape (and type)."""
-    t = torch.empty_like(t, dtype=dtype)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
-
-
-def _workspace_arg(t, dev):
-    if t.get_device() != dev or not t.is_contiguous():
-        _refuse(f"workspace must be a contiguous tensor on cuda:{dev}")
-    return t.data_ptr(), t.nbytes
-
-
 def quantized_size(rows: int, cols: int):
     """(bytes of the codes, bytes of the scales, scale_rows) of quantized rows."""
     out = [ctypes.c_size_t() for _ in range(3)]
@@ -490,40 +499,13 @@ def new_quantized(rows: int, cols: int, device="cuda"):
             torch.empty((cols // 128, scale_rows), dtype=torch.int32, device=device))
 
 
-def _quantized_args(q, rows, cols, dev):
-    if q is None:
-        return None, None
-    return (_arg(q[0], "codes", (rows, cols), torch.uint8, dev),
-            _arg(q[1], "scales", (cols // 128, (rows + 135) // 4 * 4), torch.int32, dev))
-
-
 def add_rms_norm(cfg: Config, x, norm_weight, rms_eps: float, residual=None, residual_out=None, y=None,
                  quantized=None, want_y=True, want_quantized=True, stream=None):
     """h = x + residual; y = h / sqrt(mean h^2 + rms_eps) * norm_weight; quantized = the codes and scales of y.
     x bf16 [T, H], residual bf16 or fp32 [T, H] or None.  Outputs that are not passed are allocated.
     -> (h in the residual's type, or x without one; y bf16 or None; (codes, scale words) or None)."""
-    dev = _device_of(x, "x")
-    T, H = cfg.num_tokens, cfg.hidden
-    shape = (T, H)
-    if residual is None:
-        if residual_out is not None:
-            _refuse("residual_out needs a residual")
-    elif residual.dtype not in (torch.bfloat16, torch.float32):
-        _refuse(f"residual must be bfloat16 or float32, got {residual.dtype}")
-    elif residual_out is None:
-        residual_out = _like(residual, stream)
-    if y is None and want_y:
-        y = _like(x, stream)
-    if quantized is None and want_quantized:
-        quantized = (_like(x, stream, torch.uint8), _new(x, (H // 128, (T + 135) // 4 * 4), torch.int32, stream))
-    rt = None if residual is None else residual.dtype
-    c = cfg.c()
-    _check(_load().moe_add_rms_norm(
-        ctypes.byref(c), _arg(x, "x", shape, torch.bfloat16, dev), _arg(residual, "residual", shape, rt, dev),
-        1 if rt == torch.float32 else 0, _arg(norm_weight, "norm_weight", (H,), torch.float32, dev), rms_eps,
-        _arg(residual_out, "residual_out", shape, rt, dev), _arg(y, "y", shape, torch.bfloat16, dev),
-        *_quantized_args(quantized, T, H, dev), _raw_stream(stream, dev)))
-    return (x if residual is None else residual_out), y, quantized
+    return (_bound or _bind()).add_rms_norm(cfg, x, norm_weight, rms_eps, residual, residual_out, y, quantized,
+                                              want_y, want_quantized, stream)
 
 
 def transformed_linear_size(cfg: LinearConfig):
@@ -563,26 +545,7 @@ def linear(cfg: LinearConfig, weights, x=None, quantized=None, bias=None, residu
            stream=None):
     """y = act(x W + bias) + residual, bf16 [T, N].  Exactly one of x (bf16 [T, K], quantized by the call) and
     quantized (codes and scale words, as add_rms_norm returns them); weights from transform_linear_weights."""
-    if (x is None) == (quantized is None):
-        _refuse("pass exactly one of x and quantized")
-    dev = _device_of(x if quantized is None else quantized[0], "x")
-    T, K, N = cfg.num_tokens, cfg.in_features, cfg.out_features
-    if y is None:
-        y = _new(weights[0], (T, N), torch.bfloat16, stream)
-    if workspace is None:
-        n = linear_workspace_size(cfg) if quantized is None else MOE_LINEAR_STATUS_BYTES
-        workspace = _new(y, n, torch.uint8, stream)
-    c = cfg.c()
-    w_t, ws_t = weights
-    w_bytes = K * N // (2 if cfg.recipe == 2 else 1)
-    ws_bytes = K // 128 * ((N + 255) // 256 * 256) * 4
-    bf16 = torch.bfloat16
-    _check(_load().moe_linear(
-        ctypes.byref(c), _arg(x, "x", (T, K), bf16, dev), *_quantized_args(quantized, T, K, dev),
-        _arg(w_t, "w_t", (w_bytes,), torch.uint8, dev), _arg(ws_t, "ws_t", (ws_bytes,), torch.uint8, dev),
-        _arg(bias, "bias", (N,), bf16, dev), _arg(residual, "residual", (T, N), bf16, dev),
-        _arg(y, "y", (T, N), bf16, dev), *_workspace_arg(workspace, dev), _raw_stream(stream, dev)))
-    return y
+    return (_bound or _bind()).linear(cfg, weights, x, quantized, bias, residual, y, workspace, stream)
 
 
 def balance_workspace_size(cfg: Config, num_seqs: int = 1) -> int:
@@ -596,38 +559,13 @@ def new_balance_workspace(cfg: Config, num_seqs: int = 1, device="cuda"):
     return torch.empty(balance_workspace_size(cfg, num_seqs), dtype=torch.uint8, device=device)
 
 
-def _seq_args(cfg, token_mask, seq_offsets, dev):
-    """(mask pointer, offsets pointer, number of sequences)."""
-    n = 1
-    if seq_offsets is not None:
-        n = seq_offsets.numel() - 1
-        if n < 1:
-            _refuse("seq_offsets must hold at least two offsets")
-    if token_mask is not None and token_mask.dtype == torch.bool:
-        token_mask = token_mask.view(torch.uint8)
-    return (_arg(token_mask, "token_mask", (cfg.num_tokens,), torch.uint8, dev),
-            _arg(seq_offsets, "seq_offsets", (n + 1,), torch.int32, dev), n)
-
-
 def balance_loss(cfg: Config, router_logits, topk_idx, coef: float, seq_offsets=None, token_mask=None,
                  workspace=None, stream=None):
     """The router's balance loss over the sequences of seq_offsets (int32 [S + 1]; None: one sequence),
     of the tokens whose token_mask (uint8 or bool [T]) is set.
     -> (loss fp32 [1], expert_counts int32 [S, E], seq_tokens int32 [S + 1], mean_probs fp32 [S, E])."""
-    dev = _device_of(router_logits, "router_logits")
-    T, E = cfg.num_tokens, cfg.num_experts
-    mask, off, S = _seq_args(cfg, token_mask, seq_offsets, dev)
-    i32, f32 = torch.int32, torch.float32
-    counts, tokens = _new(router_logits, (S, E), i32, stream), _new(router_logits, S + 1, i32, stream)
-    mean, loss = _new(router_logits, (S, E), f32, stream), _new(router_logits, 1, f32, stream)
-    if workspace is None:
-        workspace = _new(router_logits, balance_workspace_size(cfg, S), torch.uint8, stream)
-    c = cfg.c()
-    _check(_load().moe_balance_loss(
-        ctypes.byref(c), _arg(router_logits, "router_logits", (T, E), torch.float32, dev),
-        _arg(topk_idx, "topk_idx", (T, cfg.top_k), torch.int32, dev), mask, off, S, coef, counts.data_ptr(),
-        tokens.data_ptr(), mean.data_ptr(), loss.data_ptr(), *_workspace_arg(workspace, dev), _raw_stream(stream, dev)))
-    return loss, counts, tokens, mean
+    return (_bound or _bind()).balance_loss(cfg, router_logits, topk_idx, coef, seq_offsets, token_mask, workspace,
+                                              stream)
 
 
 def route_backward(cfg: Config, router_logits, topk_idx, d_topk_weights=None, per_expert_scale=None, d_loss=None,
@@ -636,28 +574,9 @@ def route_backward(cfg: Config, router_logits, topk_idx, d_topk_weights=None, pe
     """The gradient of the router logits from the routing weights (d_topk_weights fp32 [T, k]) and from the
     balance loss (d_loss fp32 [1], with balance_loss's arguments and its expert_counts and seq_tokens).
     -> (d_logits fp32 [T, E], d_per_expert_scale fp32 [E] or None without per_expert_scale)."""
-    dev = _device_of(router_logits, "router_logits")
-    T, E, k = cfg.num_tokens, cfg.num_experts, cfg.top_k
-    f32 = torch.float32
-    mask, off, S = _seq_args(cfg, token_mask, seq_offsets, dev)
-    if d_logits is None:
-        d_logits = _like(router_logits, stream)
-    d_scale, ws = None, (None, 0)
-    if per_expert_scale is not None:
-        d_scale = _like(per_expert_scale, stream)
-        if workspace is None:
-            workspace = _new(router_logits, balance_workspace_size(cfg, S), torch.uint8, stream)
-        ws = _workspace_arg(workspace, dev)
-    c = cfg.c()
-    _check(_load().moe_route_backward(
-        ctypes.byref(c), _arg(router_logits, "router_logits", (T, E), f32, dev),
-        _arg(per_expert_scale, "per_expert_scale", (E,), f32, dev),
-        _arg(topk_idx, "topk_idx", (T, k), torch.int32, dev), _arg(d_topk_weights, "d_topk_weights", (T, k), f32, dev),
-        _arg(d_loss, "d_loss", (1,), f32, dev), coef, _arg(expert_counts, "expert_counts", (S, E), torch.int32, dev),
-        _arg(seq_tokens, "seq_tokens", (S + 1,), torch.int32, dev), mask, off, S,
-        _arg(d_logits, "d_logits", (T, E), f32, dev), None if d_scale is None else d_scale.data_ptr(), *ws,
-        _raw_stream(stream, dev)))
-    return d_logits, d_scale
+    return (_bound or _bind()).route_backward(cfg, router_logits, topk_idx, d_topk_weights, per_expert_scale,
+                                                d_loss, coef, expert_counts, seq_tokens, seq_offsets, token_mask,
+                                                d_logits, workspace, stream)
 
 
 class Profile:

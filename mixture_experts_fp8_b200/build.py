@@ -8,6 +8,9 @@ date) and linked with the static CUDA runtime into mixture_experts_fp8_b200/libm
 MOE_FAULT_INJECTION, the library the failure-detection tests inject faults through.  The
 driver API entry point used for TMA descriptors is fetched at run time, so the library does not
 link libcuda.
+
+csrc/binding.cpp, the Python module that marshals the operators around the layer, is compiled by the
+host compiler against PyTorch's headers into mixture_experts_fp8_b200/_binding.so.
 """
 from __future__ import annotations
 
@@ -18,6 +21,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -25,6 +29,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoefp8.so")
+BINDING = os.path.join(PKG, "_binding.so")
 # The debug library: the same sources with MOE_FAULT_INJECTION, for failure-detection tests.
 BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libmoefp8_debug.so")
@@ -85,9 +90,31 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     return lib
 
 
+def build_binding(force: bool = False) -> str:
+    """Build _binding.so (host code only) and return its path."""
+    src = os.path.join(CSRC, "binding.cpp")
+    deps = [src, os.path.join(INCLUDE, "moefp8.h")]
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, deps)):
+        return BINDING
+    import torch
+    base = os.path.dirname(torch.__file__)
+    includes = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    tmp = BINDING + f".{os.getpid()}.tmp"
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           *[f for p in includes for f in ("-isystem", p)], src, "-o", tmp, "-L", os.path.join(base, "lib"),
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for {src}:\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build_all(force: bool = False, verbose: bool = False) -> list:
-    """The release library and the fault-injection debug library."""
-    return [build(force, verbose), build(force, False, debug=True)]
+    """The release library, the fault-injection debug library and the Python module."""
+    return [build(force, verbose), build(force, False, debug=True), build_binding(force)]
 
 
 if __name__ == "__main__":
@@ -96,4 +123,5 @@ if __name__ == "__main__":
     ap.add_argument("--verbose", action="store_true", help="print ptxas register/spill usage")
     ap.add_argument("--debug", action="store_true", help="also build libmoefp8_debug.so")
     a = ap.parse_args()
-    print(build_all(a.force, a.verbose) if a.debug else build(force=a.force, verbose=a.verbose))
+    print(build_all(a.force, a.verbose) if a.debug else
+          [build(force=a.force, verbose=a.verbose), build_binding(a.force)])
