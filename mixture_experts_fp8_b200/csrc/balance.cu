@@ -22,19 +22,19 @@ namespace moe {
 
 namespace {
 
-// Sequence s's first token (s <= S), kept inside [0, T].
-__device__ __forceinline__ int seq_at(const int32_t* off, int S, int T, int s) {
-    if (!off) return s == 0 ? 0 : T;
-    return min(max(__ldg(off + s), 0), T);
-}
+// Offset i of the sequences, kept inside [0, T].
+__device__ __forceinline__ int offset_at(const int32_t* off, int T, int i) { return min(max(__ldg(off + i), 0), T); }
 
-// The first sequence that ends behind token t (S if none does).
-__device__ __forceinline__ int seq_after(const int32_t* off, int S, int T, int t) {
+// How many i of 0 .. S - 1 have pred(i), true up to some i and false behind it: all at once with a thread for
+// each, where a search makes log2 S loads that wait for one another, or by that search above THREADS.
+template <int THREADS, typename F>
+__device__ __forceinline__ int block_count(int S, F pred) {
+    if (S <= THREADS) return __syncthreads_count(static_cast<int>(threadIdx.x) < S && pred(threadIdx.x));
     int lo = 0, hi = S;
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        if (seq_at(off, S, T, mid + 1) > t) hi = mid;
-        else lo = mid + 1;
+        if (pred(mid)) lo = mid + 1;
+        else hi = mid;
     }
     return lo;
 }
@@ -129,128 +129,184 @@ __device__ __forceinline__ void row_probs(float (&v)[NE]) {
 }
 
 constexpr int kBWarps = 32;                            // k_balance
+constexpr int kJThreads = 512;                         // k_balance_join
 constexpr int kRWarps = 8;                             // k_route_backward
 
 }  // namespace
 
-// Block c takes the tokens of chunk c, sequence by sequence; the sums of p stay in registers and are
-// joined over the lanes and warps in order at a sequence's end.
+// Block c + s takes the tokens of chunk c that are in sequence s.  The sums of p stay in registers and are joined
+// over the lanes and warps in order at the end.
 template <int NE, int G, bool VEC, bool SIG>
 __global__ void __launch_bounds__(kBWarps * 32) k_balance(BalanceArgs a) {
     using R = Row<NE, G, VEC>;
     constexpr int TPW = 32 / G, W = NE * G;
     __shared__ float s_p[kBWarps][W];
     __shared__ int s_n[W + 2];                         // counts, counted tokens, ids out of range
+    const int slot = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gl = lane % G;
+    for (int e = threadIdx.x; e < W + 2; e += blockDim.x) s_n[e] = 0;
     pdl_wait_then_release();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gl = lane % G;
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (slot == 0 && threadIdx.x == 0) {
         *a.status = MOE_OK;
         *a.ticket = 0;
     }
-    const int c0 = blockIdx.x * a.chunk, c1 = min(a.T, c0 + a.chunk);
-    for (int s = seq_after(a.off, a.S, a.T, c0); s < a.S; ++s) {
-        const int s0 = seq_at(a.off, a.S, a.T, s);
-        if (s0 >= c1) break;
-        const int b0 = max(c0, s0), b1 = min(c1, seq_at(a.off, a.S, a.T, s + 1));
-        if (b0 >= b1) continue;
-        const int warps = min(kBWarps, (b1 - b0 + TPW - 1) / TPW);   // warps with a token
-        for (int e = threadIdx.x; e < a.E + 2; e += blockDim.x) s_n[e] = 0;
-        __syncthreads();
-        if (warp < warps) {
-            float acc[NE];
-#pragma unroll
-            for (int i = 0; i < NE; ++i) acc[i] = 0.0f;
-            for (int tb = b0 + warp * TPW; tb < b1; tb += kBWarps * TPW) {
-                const int t = tb + lane / G;
-                const bool ok = t < b1 && !(a.mask && !__ldg(a.mask + t));
-                float p[NE];
-                R::template load<float4>(a.logits + static_cast<size_t>(ok ? t : 0) * a.E, a.E, gl, ok, p, -INFINITY);
-                if (ok) {
-                    for (int j = gl; j < a.K; j += G) {
-                        const int e = __ldg(a.idx + static_cast<size_t>(t) * a.K + j);
-                        atomicAdd(&s_n[e >= 0 && e < a.E ? e : a.E + 1], 1);
-                    }
-                    if (gl == 0) atomicAdd(&s_n[a.E], 1);
-                }
-                row_probs<NE, G, SIG>(p);
-#pragma unroll
-                for (int i = 0; i < NE; ++i) acc[i] += ok ? p[i] : 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < NE; ++i) {
-#pragma unroll
-                for (int o = G; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-                if (lane < G) s_p[warp][R::expert(i, gl)] = acc[i];
-            }
-        }
-        __syncthreads();
-        const size_t slot = static_cast<size_t>(blockIdx.x) + s;
-        for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-            float v = 0.0f;
-            for (int w = 0; w < warps; ++w) v += s_p[w][e];
-            a.part_p[slot * a.E + e] = v;
-        }
-        for (int e = threadIdx.x; e < a.E + 2; e += blockDim.x) a.part_n[slot * (a.E + 2) + e] = s_n[e];
+    int s = 0, b0 = 0, b1 = a.T;
+    if (a.off) {                                       // the first sequence whose last slot is not before this one
+        s = block_count<kBWarps * 32>(a.S, [&](int i) {
+            return (offset_at(a.off, a.T, i + 1) + a.chunk - 1) / a.chunk - 1 + i < slot;
+        });
+        if (s == a.S) return;
+        b0 = offset_at(a.off, a.T, s);
+        b1 = offset_at(a.off, a.T, s + 1);
+    } else {
         __syncthreads();
     }
+    if (s > slot || slot - s > (a.T - 1) / a.chunk) return;
+    const int c0 = (slot - s) * a.chunk;
+    b0 = max(b0, c0);
+    b1 = min(b1, min(a.T - c0, a.chunk) + c0);
+    if (b0 >= b1) return;
+    if (a.off && a.S > kBWarps * 32) __syncthreads();  // s_n
+    const int warps = min(kBWarps, (b1 - b0 + TPW - 1) / TPW);   // warps with a token
+    if (warp < warps) {
+        float acc[NE];
+#pragma unroll
+        for (int i = 0; i < NE; ++i) acc[i] = 0.0f;
+        for (int tb = b0 + warp * TPW; tb < b1; tb += kBWarps * TPW) {
+            const int t = tb + lane / G;
+            const bool in = t < b1;
+            const int32_t* idx = a.idx + static_cast<size_t>(in ? t : b0) * a.K;
+            float p[NE];                               // the loads do not wait for the mask's
+            R::template load<float4>(a.logits + static_cast<size_t>(in ? t : b0) * a.E, a.E, gl, in, p, -INFINITY);
+            const int e0 = gl < a.K ? __ldg(idx + gl) : 0;
+            const bool ok = in && !(a.mask && !__ldg(a.mask + t));
+            if (ok) {
+                if (gl < a.K) atomicAdd(&s_n[e0 >= 0 && e0 < a.E ? e0 : W + 1], 1);
+                for (int j = gl + G; j < a.K; j += G) {
+                    const int e = __ldg(idx + j);
+                    atomicAdd(&s_n[e >= 0 && e < a.E ? e : W + 1], 1);
+                }
+                if (gl == 0) atomicAdd(&s_n[W], 1);
+            }
+            row_probs<NE, G, SIG>(p);
+#pragma unroll
+            for (int i = 0; i < NE; ++i) acc[i] += ok ? p[i] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+#pragma unroll
+            for (int o = G; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+            if (lane < G) s_p[warp][R::expert(i, gl)] = acc[i];
+        }
+    }
+    __syncthreads();
+    const int row = balance_row(a.E);                  // <= W; the sums past E are zero
+    for (int e = threadIdx.x; e < row; e += blockDim.x) {
+        float v = 0.0f;
+        for (int w = 0; w < warps; ++w) v += s_p[w][e];
+        a.part_p[static_cast<size_t>(slot) * row + e] = v;
+        a.part_n[static_cast<size_t>(slot) * row + e] = s_n[e];
+    }
+    if (threadIdx.x == 0) a.part_t[slot] = make_int2(s_n[W], s_n[W + 1]);
 }
 
-// Block (s, b) joins sequence s's chunks for experts 32 b .. 32 b + 31: a lane an expert, a warp every
-// 32nd chunk, then the warps in order.  The last block to finish adds the losses.
-__global__ void __launch_bounds__(1024) k_balance_join(BalanceArgs a) {
-    __shared__ float s_p[32][33];
-    __shared__ int s_n[32][33], s_tok[32], s_bad, s_last;
-    __shared__ float s_red[32];
+// Block s joins sequence s's slots: Q threads (a power of two) take a slot's row, four experts each, the block
+// kJThreads / Q slots at a time and five times that in flight, then the threads of an expert in order.  The last
+// block to finish adds the losses.
+template <int Q>
+__global__ void __launch_bounds__(kJThreads) k_balance_join(BalanceArgs a) {
+    constexpr int W = 4 * Q, ROWS = kJThreads / Q, PARTS = Q < 32 ? kJThreads / 32 : ROWS, BATCH = 5;
+    __shared__ __align__(16) float s_p[PARTS][W];
+    __shared__ __align__(16) int s_n[PARTS][W];
+    __shared__ int s_tok[kJThreads / 32];
+    __shared__ float s_red[kJThreads / 32];
+    __shared__ int s_last;
     pdl_wait_then_release();
-    const int s = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int e = blockIdx.y * 32 + lane;
-    const int b0 = seq_at(a.off, a.S, a.T, s), b1 = seq_at(a.off, a.S, a.T, s + 1);
-    if (threadIdx.x == 0) s_bad = a.off && (a.off[s] < 0 || a.off[s + 1] > a.T || a.off[s] > a.off[s + 1]);
-    __syncthreads();
-    const int lo = b0 / a.chunk, hi = b0 < b1 ? (b1 - 1) / a.chunk : lo - 1;
-    float v = 0.0f;
-    int n = 0, tok = 0, bad = 0;
-#pragma unroll 4
-    for (int c = lo + warp; c <= hi; c += 32) {
-        const size_t slot = static_cast<size_t>(c) + s;
-        const int32_t* cnt = a.part_n + slot * (a.E + 2);
-        if (e < a.E) {
-            v += __ldcg(a.part_p + slot * a.E + e);
-            n += __ldcg(cnt + e);
-        }
-        tok += __ldcg(cnt + a.E);                      // one address for the warp
-        bad |= __ldcg(cnt + a.E + 1);
+    const int s = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = threadIdx.x % Q;
+    const int row = balance_row(a.E);
+    int b0 = 0, b1 = a.T;
+    bool bad = false;
+    if (a.off) {
+        const int r0 = __ldg(a.off + s), r1 = __ldg(a.off + s + 1);
+        bad = r0 < 0 || r1 > a.T || r0 > r1;
+        b0 = min(max(r0, 0), a.T);
+        b1 = min(max(r1, 0), a.T);
     }
-    s_p[warp][lane] = v;
-    s_n[warp][lane] = n;
-    if (lane == 0) {
-        s_tok[warp] = tok;
-        if (bad) s_bad = 1;
+    const int lo = s + b0 / a.chunk, hi = b0 < b1 ? s + (b1 - 1) / a.chunk : lo - 1;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    int4 n = make_int4(0, 0, 0, 0);
+    int tok = 0;
+    for (int c = lo + threadIdx.x; c <= hi; c += kJThreads) {
+        const int2 t = __ldcg(a.part_t + c);
+        tok += t.x;
+        bad |= t.y != 0;
     }
+    if (4 * col < row) {
+        for (int c = lo + static_cast<int>(threadIdx.x) / Q; c <= hi; c += BATCH * ROWS) {
+            float4 x[BATCH];
+            int4 y[BATCH];
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) {
+                x[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                y[u] = make_int4(0, 0, 0, 0);
+                if (c + u * ROWS <= hi) {
+                    const size_t at = static_cast<size_t>(c + u * ROWS) * row + 4 * col;
+                    x[u] = __ldcg(reinterpret_cast<const float4*>(a.part_p + at));
+                    y[u] = __ldcg(reinterpret_cast<const int4*>(a.part_n + at));
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) {
+                v.x += x[u].x, v.y += x[u].y, v.z += x[u].z, v.w += x[u].w;
+                n.x += y[u].x, n.y += y[u].y, n.z += y[u].z, n.w += y[u].w;
+            }
+        }
+    }
+#pragma unroll
+    for (int o = Q; o < 32; o <<= 1) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, o), v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+        v.z += __shfl_xor_sync(0xffffffffu, v.z, o), v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
+        n.x += __shfl_xor_sync(0xffffffffu, n.x, o), n.y += __shfl_xor_sync(0xffffffffu, n.y, o);
+        n.z += __shfl_xor_sync(0xffffffffu, n.z, o), n.w += __shfl_xor_sync(0xffffffffu, n.w, o);
+    }
+    if (Q >= 32 || lane < Q) {
+        const int part = Q < 32 ? warp : threadIdx.x / Q;
+        *reinterpret_cast<float4*>(&s_p[part][4 * col]) = v;
+        *reinterpret_cast<int4*>(&s_n[part][4 * col]) = n;
+    }
+    tok = __reduce_add_sync(0xffffffffu, tok);
+    if (lane == 0) s_tok[warp] = tok;
+    if (__syncthreads_or(bad) && threadIdx.x == 0) set_status(a.status, MOE_ERR_BOUNDS);
+    tok = 0;
+    for (int w = 0; w < kJThreads / 32; ++w) tok += s_tok[w];
+    float term = 0.0f;
+    if (threadIdx.x < a.E) {
+        const int e = threadIdx.x;
+        float p = 0.0f;
+        int k = 0;
+        for (int w = 0; w < PARTS; ++w) {
+            p += s_p[w][e];
+            k += s_n[w][e];
+        }
+        const float mean = tok ? p / static_cast<float>(tok) : 0.0f;
+        a.mean[static_cast<size_t>(s) * a.E + e] = mean;
+        a.counts[static_cast<size_t>(s) * a.E + e] = k;
+        if (tok) term = static_cast<float>(k) * (static_cast<float>(a.E) / (static_cast<float>(a.K) * static_cast<float>(tok))) * mean;
+    }
+    term = warp_sum(term);
+    if (lane == 0) s_red[warp] = term;
     __syncthreads();
-    if (warp == 0) {
-        tok = __reduce_add_sync(0xffffffffu, s_tok[lane]);
-        v = 0.0f;
-        n = 0;
-        for (int w = 0; w < 32; ++w) {
-            v += s_p[w][lane];
-            n += s_n[w][lane];
-        }
-        float term = 0.0f;
-        if (e < a.E) {
-            const float mean = tok ? v / static_cast<float>(tok) : 0.0f;
-            a.mean[static_cast<size_t>(s) * a.E + e] = mean;
-            a.counts[static_cast<size_t>(s) * a.E + e] = n;
-            if (tok)
-                term = static_cast<float>(n) * (static_cast<float>(a.E) / (static_cast<float>(a.K) * static_cast<float>(tok))) * mean;
-        }
-        term = warp_sum(term);
-        if (lane == 0) {
-            a.seq_loss[static_cast<size_t>(s) * gridDim.y + blockIdx.y] = term;
-            if (blockIdx.y == 0) a.tokens[s] = tok;
-            if (s_bad) set_status(a.status, MOE_ERR_BOUNDS);
+    if (threadIdx.x == 0) {
+        term = 0.0f;
+        for (int w = 0; w < kJThreads / 32; ++w) term += s_red[w];
+        a.tokens[s] = tok;
+        if (a.S == 1) {
+            a.tokens[1] = tok > 0;
+            a.loss[0] = tok ? a.coef * term : 0.0f;
+            s_last = 0;
+        } else {
+            a.seq_loss[s] = term;
             __threadfence();
-            s_last = atomicAdd(a.ticket, 1) == static_cast<int>(gridDim.x * gridDim.y) - 1;
+            s_last = atomicAdd(a.ticket, 1) == a.S - 1;
         }
     }
     __syncthreads();
@@ -258,8 +314,10 @@ __global__ void __launch_bounds__(1024) k_balance_join(BalanceArgs a) {
     __threadfence();
     float l = 0.0f;
     int full = 0;
-    for (int i = threadIdx.x; i < a.S * static_cast<int>(gridDim.y); i += 1024) l += __ldcg(a.seq_loss + i);
-    for (int i = threadIdx.x; i < a.S; i += 1024) full += __ldcg(a.tokens + i) > 0;
+    for (int i = threadIdx.x; i < a.S; i += kJThreads) {
+        l += __ldcg(a.seq_loss + i);
+        full += __ldcg(a.tokens + i) > 0;
+    }
     l = warp_sum(l);
     full = __reduce_add_sync(0xffffffffu, full);
     if (lane == 0) {
@@ -270,7 +328,7 @@ __global__ void __launch_bounds__(1024) k_balance_join(BalanceArgs a) {
     if (threadIdx.x == 0) {
         l = 0.0f;
         full = 0;
-        for (int w = 0; w < 32; ++w) {
+        for (int w = 0; w < kJThreads / 32; ++w) {
             l += s_red[w];
             full += s_tok[w];
         }
@@ -304,6 +362,11 @@ __global__ void __launch_bounds__(kRWarps * 32) k_route_backward(RouteBackwardAr
     __syncwarp();
     const int c0 = blockIdx.x * a.chunk, c1 = min(a.T, c0 + a.chunk);
     const float gloss = a.dloss ? __ldg(a.dloss) * a.coef : 0.0f;
+    int s_lo = 0, s_hi = 0;                            // the first sequences to end behind the block's first and last token
+    if (a.dloss && a.off) {
+        s_lo = block_count<kRWarps * 32>(a.S, [&](int i) { return offset_at(a.off, a.T, i + 1) <= c0; });
+        s_hi = block_count<kRWarps * 32>(a.S, [&](int i) { return offset_at(a.off, a.T, i + 1) < c1; });
+    }
     int q = -1, q0 = 0, q1 = 0;                        // the sequence whose gradient is in g, its tokens
     float g[NE];
 #pragma unroll
@@ -323,9 +386,14 @@ __global__ void __launch_bounds__(kRWarps * 32) k_route_backward(RouteBackwardAr
         float x0 = in && a.dw && gl < a.K ? __ldg(dw + gl) : 0.0f;
         bool bal = in && a.dloss && !(a.mask && !__ldg(a.mask + t));
         if (bal && !(t >= q0 && t < q1)) {             // another sequence than the last token's
-            q = seq_after(a.off, a.S, a.T, t);
-            q0 = seq_at(a.off, a.S, a.T, q);           // q = S: no sequence ends behind t
-            q1 = q < a.S ? seq_at(a.off, a.S, a.T, q + 1) : 0;
+            q = s_lo;
+            for (int hi = s_hi; q < hi;) {
+                const int mid = (q + hi) >> 1;
+                if (offset_at(a.off, a.T, mid + 1) <= t) q = mid + 1;
+                else hi = mid;
+            }
+            q0 = a.off ? offset_at(a.off, a.T, q) : 0;   // q = S: no sequence ends behind t
+            q1 = !a.off ? a.T : q < a.S ? offset_at(a.off, a.T, q + 1) : 0;
             if (t >= q0 && t < q1) {
                 const float n = static_cast<float>(__ldg(a.tokens + q)), full = static_cast<float>(__ldg(a.tokens + a.S));
                 const float f = n > 0.0f ? gloss / full * static_cast<float>(a.E) / (static_cast<float>(a.K) * n * n) : 0.0f;
@@ -470,9 +538,12 @@ __global__ void __launch_bounds__(1024) k_join_scale_grad(RouteBackwardArgs a) {
     pdl_wait_then_release();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.x * 32 + lane;
     float v = 0.0f;
-    if (e < a.E) {
-#pragma unroll 4
-        for (int c = warp; c < a.chunks; c += 32) v += __ldcg(a.part + static_cast<size_t>(c) * a.E + e);
+    for (int c = warp; c < a.chunks && e < a.E; c += 320) {
+        float x[10];                                   // in flight
+#pragma unroll
+        for (int u = 0; u < 10; ++u) x[u] = c + 32 * u < a.chunks ? __ldcg(a.part + static_cast<size_t>(c + 32 * u) * a.E + e) : 0.0f;
+#pragma unroll
+        for (int u = 0; u < 10; ++u) v += x[u];
     }
     s_p[warp][lane] = v;
     __syncthreads();
@@ -486,7 +557,7 @@ namespace {
 
 template <int NE, int G>
 cudaError_t balance_t(const BalanceArgs& a, bool vec, cudaStream_t s) {
-    const dim3 grid(a.chunks), block(kBWarps * 32);
+    const dim3 grid(a.slots), block(kBWarps * 32);
     if (a.routing)
         return vec ? launch_pdl(k_balance<NE, G, true, true>, grid, block, 0, s, a)
                    : launch_pdl(k_balance<NE, G, false, true>, grid, block, 0, s, a);
@@ -519,7 +590,11 @@ cudaError_t launch_balance(const BalanceArgs& a, cudaStream_t s) {
                           : a.E <= 128 ? balance_t<16, 8>(a, vec, s)
                                        : balance_t<16, 16>(a, vec, s);
     if (e != cudaSuccess) return e;
-    return launch_pdl(k_balance_join, dim3(a.S, (a.E + 31) / 32), dim3(1024), 0, s, a);
+    const dim3 grid(a.S), block(kJThreads);
+    return a.E <= 32    ? launch_pdl(k_balance_join<8>, grid, block, 0, s, a)
+           : a.E <= 64  ? launch_pdl(k_balance_join<16>, grid, block, 0, s, a)
+           : a.E <= 128 ? launch_pdl(k_balance_join<32>, grid, block, 0, s, a)
+                        : launch_pdl(k_balance_join<64>, grid, block, 0, s, a);
 }
 
 cudaError_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t s) {

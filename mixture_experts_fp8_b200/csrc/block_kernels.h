@@ -80,14 +80,18 @@ cudaError_t launch_linear_narrow(const LinearArgs& a, const LinearMaps& m, int n
 cudaError_t launch_linear_fp32(const LinearArgs& a, const LinearMaps& m, int num_sms, cudaStream_t s);
 cudaError_t launch_linear_mx(const LinearArgs& a, const LinearMaps& m, int num_sms, cudaStream_t s);
 
-// Tokens are taken in chunks; chunk c and sequence s that meet have the partial sums of slot c + s:
-// walking the tokens in order raises c or s at every step, so no two pairs share a slot.
-constexpr int kBalanceChunks = 148;
-inline int balance_chunk(int T) {
-    const int c = (T + kBalanceChunks - 1) / kBalanceChunks;
+// The balance loss takes the tokens in chunks, and a block the part of chunk c that is in sequence s, whose sums
+// are slot c + s: walking the tokens in order raises c or s at every step, so no two parts share a slot.  As
+// many slots as SMs (a block of 1024 threads each) while the sequences leave at least half of them to chunks.
+inline int balance_chunk(int T, int S) {
+    const int n = S <= 74 ? 149 - S : 75, c = (T + n - 1) / n;
     return c < 32 ? 32 : c;
 }
-inline int balance_chunks(int T) { return (T + balance_chunk(T) - 1) / balance_chunk(T); }
+inline int balance_slots(int T, int S) { return (T + balance_chunk(T, S) - 1) / balance_chunk(T, S) + S - 1; }
+// No fewer than balance_slots, and more for more sequences: a workspace for S of them serves a smaller number.
+inline int balance_max_slots(int T, int S) { return (T < 148 * 32 ? (T + 31) / 32 : 148) + S; }
+// A slot's row of sums: its experts in groups of four.
+inline __host__ __device__ int balance_row(int E) { return (E + 3) & ~3; }
 // The gradients' chunks: a block of 8 warps each, as many as run at once (up to 64 experts four blocks an SM
 // at 64 registers a thread, above two at 120).
 inline int backward_chunk(int T, int E) {
@@ -101,16 +105,17 @@ struct BalanceArgs {
     const int32_t* idx;         // [T, K]
     const uint8_t* mask;        // [T] or null: 0 = not counted
     const int32_t* off;         // [S + 1] or null (one sequence of all tokens)
-    float* part_p;              // [chunks + S][E]
-    int32_t* part_n;            // [chunks + S][E + 2] counts, counted tokens, ids out of range
-    float* seq_loss;            // [S][ceil(E / 32)]
+    float* part_p;              // [slots][row] sums of p
+    int32_t* part_n;            // [slots][row] counts
+    int2* part_t;               // [slots] counted tokens, ids out of range
+    float* seq_loss;            // [S]
     int32_t* ticket;
     int32_t* counts;            // [S, E]
     int32_t* tokens;            // [S + 1]
     float* mean;                // [S, E]
     float* loss;                // [1]
     int32_t* status;
-    int T, E, K, S, routing, chunk, chunks;
+    int T, E, K, S, routing, chunk, slots;
     float coef;
 };
 

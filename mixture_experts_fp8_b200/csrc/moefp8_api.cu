@@ -712,18 +712,20 @@ namespace {
 
 // Regions of the balance workspace.
 struct BalanceLayout {
-    size_t ticket, seq_loss, part_p, part_n, total;
+    size_t ticket, seq_loss, part_p, part_n, part_t, total;
 };
 
 int balance_layout(const moe_config_t* c, int32_t num_seqs, const char* who, BalanceLayout* L) {
     if (num_seqs < 1 || num_seqs > (1 << 24))
         return fail(MOE_ERR_INVALID_ARG, "%s: num_seqs must be in [1, 2^24], got %d", who, num_seqs);
-    const size_t slots = static_cast<size_t>(moe::balance_chunks(c->num_tokens)) + num_seqs, E = c->num_experts;
+    const int T = c->num_tokens, E = c->num_experts;
+    const size_t slots = moe::balance_max_slots(T, num_seqs), row = moe::balance_row(E);
     L->ticket = 256;                                    // the status word comes first
     L->seq_loss = 512;
-    L->part_p = align_up(L->seq_loss + 4 * static_cast<size_t>(num_seqs) * ((E + 31) / 32), 256);
-    L->part_n = align_up(L->part_p + 4 * std::max(slots, static_cast<size_t>(moe::backward_chunks(c->num_tokens, c->num_experts))) * E, 256);
-    L->total = align_up(L->part_n + 4 * slots * (E + 2), 256);
+    L->part_p = align_up(L->seq_loss + 4 * static_cast<size_t>(num_seqs), 256);
+    L->part_n = align_up(L->part_p + 4 * std::max(slots * row, static_cast<size_t>(moe::backward_chunks(T, E)) * E), 256);
+    L->part_t = align_up(L->part_n + 4 * slots * row, 256);
+    L->total = align_up(L->part_t + 8 * slots, 256);
     return MOE_OK;
 }
 
@@ -914,10 +916,10 @@ int moe_balance_loss(const moe_config_t* cfg, const float* router_logits, const 
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const int T = cfg->num_tokens;
     moe::BalanceArgs a{router_logits, topk_idx, token_mask, seq_offsets, reinterpret_cast<float*>(ws + L.part_p),
-                       reinterpret_cast<int32_t*>(ws + L.part_n), reinterpret_cast<float*>(ws + L.seq_loss),
-                       reinterpret_cast<int32_t*>(ws + L.ticket), expert_counts, seq_tokens, mean_probs, loss,
+                       reinterpret_cast<int32_t*>(ws + L.part_n), reinterpret_cast<int2*>(ws + L.part_t),
+                       reinterpret_cast<float*>(ws + L.seq_loss), reinterpret_cast<int32_t*>(ws + L.ticket), expert_counts, seq_tokens, mean_probs, loss,
                        reinterpret_cast<int32_t*>(ws), T, cfg->num_experts, cfg->top_k, num_seqs, cfg->routing,
-                       moe::balance_chunk(T), moe::balance_chunks(T), coef};
+                       moe::balance_chunk(T, num_seqs), moe::balance_slots(T, num_seqs), coef};
     MOE_CUDA_TRY(moe::launch_balance(a, static_cast<cudaStream_t>(stream)));
     return ok();
 }
