@@ -367,8 +367,8 @@ int moe_quantized_size(int32_t rows, int32_t cols, size_t *codes_bytes, size_t *
  *   codes, scales  device, quantized rows of the unrounded y, or both NULL; out
  * At least one output.  residual_out may be the residual or (bf16) x buffer itself, and y the x
  * buffer or (bf16) the residual buffer; buffers may not overlap in any other way.  Every buffer
- * 16-byte aligned, an fp32 residual and its residual_out 32-byte.  One launch.  Inf or NaN in a row makes y, or the values its codes stand for,
- * non-finite in that row only. */
+ * 16-byte aligned, an fp32 residual and its residual_out 32-byte.  One launch.  Inf or NaN in a row
+ * makes y, or the values its codes stand for, non-finite in that row only. */
 int moe_add_rms_norm(const moe_config_t *cfg, const void *x, const void *residual, int residual_fp32,
                      const float *norm_weight, float rms_eps, void *residual_out, void *y, void *codes,
                      void *scales, void *stream);
@@ -450,8 +450,8 @@ int moe_balance_loss(const moe_config_t *cfg, const float *router_logits, const 
  *   d_per_expert_scale  device fp32 [E] or NULL; out (needs per_expert_scale)
  *   workspace       as for moe_balance_loss with the same num_seqs; only used (and may be NULL
  *                   otherwise) when d_per_expert_scale is wanted
- * An id outside [0, E) adds nothing; the others of a token are distinct, as moe_route's are.  One launch,
- * two with d_per_expert_scale. */
+ * An id outside [0, E) adds nothing; the others of a token are distinct, as moe_route's are (with an id
+ * twice the row's gradient is undefined).  One launch, two with d_per_expert_scale. */
 int moe_route_backward(const moe_config_t *cfg, const float *router_logits, const float *per_expert_scale,
                        const int32_t *topk_idx, const float *d_topk_weights, const float *d_loss, float coef,
                        const int32_t *expert_counts, const int32_t *seq_tokens, const uint8_t *token_mask,

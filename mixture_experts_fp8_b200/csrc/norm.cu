@@ -3,7 +3,7 @@
 // scales of bf16 rows as they are (the first launch of moe_linear on bf16 input).
 //
 //   h = x + residual (fp32),  r = 1 / sqrt(mean_h h^2 + eps),  y = h * r * w
-//   recipe 0:    s = amax * (1/448) per 128 columns, q = e4m3(y / s); amax 0 -> s = 1
+//   recipe 0:    s = amax * (1/448) per 128 columns, q = e4m3(y / s); s 0 -> 1
 //   recipes 1, 2: s = 2^e per 32 columns, e the smallest with amax <= 448 * 2^e; q = e4m3(y * 2^-e)
 // Scales are stored as every GEMM of the library reads them: [H/128][scale_rows] 4-byte words.
 #include "block_kernels.h"
@@ -67,7 +67,8 @@ __device__ __forceinline__ float group16_max(float m) {
 // v / s is v times the reciprocal of s and the reciprocal's own remainder, v ih + v il: within 2^-46 of the
 // quotient before its one rounding, in two instructions where an IEEE division takes about ten.
 __device__ __forceinline__ uint2 quant_fp32(const float* v, float amax, float& s) {
-    s = amax > 0.0f ? __fmul_rn(amax, 1.0f / 448.0f) : 1.0f;
+    s = __fmul_rn(amax, 1.0f / 448.0f);
+    if (!(s > 0.0f)) s = 1.0f;                         // nothing, or less than the smallest scale: codes of zero
     float q[8];
     if (s > 1e-30f && s < 1e30f) {                     // the reciprocal and its remainder are normal numbers
         const float ih = __frcp_rn(s), il = fmaf(-ih, s, 1.0f) * ih;

@@ -138,3 +138,13 @@ def test_captured_and_on_another_stream():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(outs[1], y.flip(0)) and torch.equal(outs[2][0], q[0].flip(0))
+
+
+@pytest.mark.parametrize("recipe", [0, 1])
+def test_values_below_the_smallest_scale(recipe):
+    # amax / 448 is under half the smallest fp32 number: no scale can hold it
+    T, H = 2, 256
+    x, w = torch.ones((T, H), dtype=torch.bfloat16), torch.zeros(H)
+    w[0] = 1e-44
+    codes, words = moe.add_rms_norm(cfg(T, H, recipe), x.cuda(), w.cuda(), EPS)[2]
+    assert float(dequantize(codes.cpu(), words, recipe).abs().max()) <= 1e-43      # NaN fails
