@@ -6,6 +6,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -104,7 +105,7 @@ struct Call {
 
     // A tensor that the call allocates; on a stream other than the current one the allocator is told.
     at::Tensor make(at::IntArrayRef shape, at::ScalarType type) const {
-        at::Tensor t = at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)));
+        at::Tensor t = at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)), c10::nullopt);
         if (other) t.record_stream(*other);
         return t;
     }
