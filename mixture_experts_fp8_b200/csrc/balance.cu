@@ -10,9 +10,16 @@
 //
 // Bound: one read of the logits (and one write of their gradient).  A token is taken by G = 8 lanes
 // (16 above 128 experts) with up to 16 experts each, so that a warp works on four tokens (two) at
-// once and a sum over a row takes three shuffles (four) for all of them.  Sums are fp32 in
-// registers, then per block and chunk in a fixed order without atomics on floats, so a result is the
-// same on every run.
+// once and a sum over a row takes three shuffles (four) for all of them.  (65536 x 128 gradients with 16
+// lanes of 8 experts: 24 us against 18.7, the instructions of a row's sums and slots are for half as many
+// tokens.)  Sums are fp32 in registers, then per block and chunk in a fixed order without atomics on
+// floats, so a result is the same on every run.
+//
+// Back to back: the loss of 65536 x 128 (36 MB) 14.7 us, of 4096 x 256 in nine sequences 9.2 us, of one
+// token 4.6 us; the gradients of 65536 x 128 with the scales' (73 MB) 21.7 us, 3.4 TB/s, of 4096 x 256
+// 6.5 us.  Small calls are the latency of two launches (one) with a read, a reduction and a write each;
+// large gradients the chain of sums from row to row (39% of the issue slots, 16 warps an SM at 110
+// registers).
 #include <math.h>
 
 #include "block_kernels.h"
@@ -216,20 +223,27 @@ __global__ void __launch_bounds__(kBWarps * 32) k_balance(BalanceArgs a) {
     if (threadIdx.x == 0) a.part_t[slot] = make_int2(s_n[W], s_n[W + 1]);
 }
 
-// Block s joins sequence s's slots: Q threads (a power of two) take a slot's row, four experts each, the block
-// kJThreads / Q slots at a time and five times that in flight, then the threads of an expert in order.  The last
-// block to finish adds the losses.
-template <int Q>
-__global__ void __launch_bounds__(kJThreads) k_balance_join(BalanceArgs a) {
-    constexpr int W = 4 * Q, ROWS = kJThreads / Q, PARTS = Q < 32 ? kJThreads / 32 : ROWS, BATCH = 5;
-    __shared__ __align__(16) float s_p[PARTS][W];
-    __shared__ __align__(16) int s_n[PARTS][W];
-    __shared__ int s_tok[kJThreads / 32];
-    __shared__ float s_red[kJThreads / 32];
+// The `split` blocks of a cluster join sequence s's slots, an equal share of the experts each: Q threads (a power of
+// two) take a share of a slot's row, four experts each, the block kJThreads / Q slots at a time and several times that
+// in flight, then the threads of an expert in order.  The shares of the loss meet in the first block; the last first
+// block to finish adds the losses of the sequences.
+// (It asks for as much shared memory as k_balance: with another amount an SM would have to be divided anew before it
+// starts, 65536 x 32 in 11.9 us instead of 8.8.)
+template <bool SPLIT>
+__global__ void __launch_bounds__(kJThreads) k_balance_join(BalanceArgs a, int lq) {
+    constexpr int kWarps = kJThreads / 32, BATCH = 5;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int s_tok[kWarps];
+    __shared__ float s_red[kWarps], s_term[8];
     __shared__ int s_last;
+    const int split = SPLIT ? gridDim.y : 1, share = SPLIT ? blockIdx.y : 0, Q = 1 << lq, W = 4 * Q, rows = kJThreads >> lq;
+    const int parts = Q < 32 ? kWarps : rows;
+    float* const s_p = reinterpret_cast<float*>(smem); // [part][4 Q]: a warp is a part, or (Q = 64) two are
+    int* const s_n = reinterpret_cast<int*>(s_p + parts * W);
+    if (SPLIT) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // this block has started
     pdl_wait_then_release();
-    const int s = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = threadIdx.x % Q;
-    const int row = balance_row(a.E);
+    const int s = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = threadIdx.x & (Q - 1);
+    const int row = balance_row(a.E), e0 = share * W;
     int b0 = 0, b1 = a.T;
     bool bad = false;
     if (a.off) {
@@ -247,16 +261,16 @@ __global__ void __launch_bounds__(kJThreads) k_balance_join(BalanceArgs a) {
         tok += t.x;
         bad |= t.y != 0;
     }
-    if (4 * col < row) {
-        for (int c = lo + static_cast<int>(threadIdx.x) / Q; c <= hi; c += BATCH * ROWS) {
+    if (e0 + 4 * col < row) {
+        for (int c = lo + (static_cast<int>(threadIdx.x) >> lq); c <= hi; c += BATCH * rows) {
             float4 x[BATCH];
             int4 y[BATCH];
 #pragma unroll
             for (int u = 0; u < BATCH; ++u) {
                 x[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 y[u] = make_int4(0, 0, 0, 0);
-                if (c + u * ROWS <= hi) {
-                    const size_t at = static_cast<size_t>(c + u * ROWS) * row + 4 * col;
+                if (c + u * rows <= hi) {
+                    const size_t at = static_cast<size_t>(c + u * rows) * row + e0 + 4 * col;
                     x[u] = __ldcg(reinterpret_cast<const float4*>(a.part_p + at));
                     y[u] = __ldcg(reinterpret_cast<const int4*>(a.part_n + at));
                 }
@@ -268,7 +282,6 @@ __global__ void __launch_bounds__(kJThreads) k_balance_join(BalanceArgs a) {
             }
         }
     }
-#pragma unroll
     for (int o = Q; o < 32; o <<= 1) {
         v.x += __shfl_xor_sync(0xffffffffu, v.x, o), v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
         v.z += __shfl_xor_sync(0xffffffffu, v.z, o), v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
@@ -276,23 +289,24 @@ __global__ void __launch_bounds__(kJThreads) k_balance_join(BalanceArgs a) {
         n.z += __shfl_xor_sync(0xffffffffu, n.z, o), n.w += __shfl_xor_sync(0xffffffffu, n.w, o);
     }
     if (Q >= 32 || lane < Q) {
-        const int part = Q < 32 ? warp : threadIdx.x / Q;
-        *reinterpret_cast<float4*>(&s_p[part][4 * col]) = v;
-        *reinterpret_cast<int4*>(&s_n[part][4 * col]) = n;
+        const int at = (Q < 32 ? warp : static_cast<int>(threadIdx.x) >> lq) * W + 4 * col;
+        *reinterpret_cast<float4*>(s_p + at) = v;
+        *reinterpret_cast<int4*>(s_n + at) = n;
     }
     tok = __reduce_add_sync(0xffffffffu, tok);
     if (lane == 0) s_tok[warp] = tok;
     if (__syncthreads_or(bad) && threadIdx.x == 0) set_status(a.status, MOE_ERR_BOUNDS);
     tok = 0;
-    for (int w = 0; w < kJThreads / 32; ++w) tok += s_tok[w];
+    for (int w = 0; w < kWarps; ++w) tok += s_tok[w];
     float term = 0.0f;
-    if (threadIdx.x < a.E) {
-        const int e = threadIdx.x;
+    if (threadIdx.x < W && e0 + static_cast<int>(threadIdx.x) < a.E) {
+        const int e = e0 + threadIdx.x;
         float p = 0.0f;
         int k = 0;
-        for (int w = 0; w < PARTS; ++w) {
-            p += s_p[w][e];
-            k += s_n[w][e];
+#pragma unroll 8
+        for (int w = 0; w < parts; ++w) {
+            p += s_p[w * W + threadIdx.x];
+            k += s_n[w * W + threadIdx.x];
         }
         const float mean = tok ? p / static_cast<float>(tok) : 0.0f;
         a.mean[static_cast<size_t>(s) * a.E + e] = mean;
@@ -304,7 +318,27 @@ __global__ void __launch_bounds__(kJThreads) k_balance_join(BalanceArgs a) {
     __syncthreads();
     if (threadIdx.x == 0) {
         term = 0.0f;
-        for (int w = 0; w < kJThreads / 32; ++w) term += s_red[w];
+        for (int w = 0; w < kWarps; ++w) term += s_red[w];
+    }
+    __syncwarp();
+    if (SPLIT) {                                   // the shares go to the first block
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        if (threadIdx.x == 0) {
+            uint32_t to;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to)
+                         : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(s_term + share))));
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(term) : "memory");
+        }
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        if (share) return;
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
+    if (threadIdx.x == 0) {
+        if (SPLIT) {
+            term = 0.0f;
+            for (int r = 0; r < split; ++r) term += s_term[r];
+        }
         a.tokens[s] = tok;
         if (a.S == 1) {
             a.tokens[1] = tok > 0;
@@ -335,7 +369,7 @@ __global__ void __launch_bounds__(kJThreads) k_balance_join(BalanceArgs a) {
     if (threadIdx.x == 0) {
         l = 0.0f;
         full = 0;
-        for (int w = 0; w < kJThreads / 32; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
             l += s_red[w];
             full += s_tok[w];
         }
@@ -629,11 +663,30 @@ cudaError_t launch_balance(const BalanceArgs& a, cudaStream_t s) {
                           : a.E <= 128 ? balance_t<16, 8>(a, vec, s)
                                        : balance_t<16, 16>(a, vec, s);
     if (e != cudaSuccess) return e;
-    const dim3 grid(a.S), block(kJThreads);
-    return a.E <= 32    ? launch_pdl(k_balance_join<8>, grid, block, 0, s, a)
-           : a.E <= 64  ? launch_pdl(k_balance_join<16>, grid, block, 0, s, a)
-           : a.E <= 128 ? launch_pdl(k_balance_join<32>, grid, block, 0, s, a)
-                        : launch_pdl(k_balance_join<64>, grid, block, 0, s, a);
+    // A sequence's experts over blocks of 32 where one block would read more than 96 KB of sums: one sequence of
+    // 4096 x 256 (264 KB) takes 11.8 us with one block and 7.8 with eight (8.6 with four), one of 65536 x 64 (76 KB)
+    // 11.1 with one and 15.4 with two, whose cluster does not start before the blocks of k_balance have left.
+    int lq = a.E <= 32 ? 3 : a.E <= 64 ? 4 : a.E <= 128 ? 5 : 6, split = 1;
+    if (8ll * balance_row(a.E) * a.slots / a.S > 96 * 1024) {
+        split = 1 << (lq - 3);
+        lq = 3;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.S, split);
+    cfg.blockDim = dim3(kJThreads);
+    cfg.dynamicSmemBytes = kBWarps * 4 * (a.E <= 32 ? 32 : a.E <= 64 ? 64 : a.E <= 128 ? 128 : 256);   // >= 32 Q parts
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1;
+    attr[1].val.clusterDim.y = split;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = split > 1 ? 2 : 1;
+    return split > 1 ? cudaLaunchKernelEx(&cfg, k_balance_join<true>, a, lq)
+                     : cudaLaunchKernelEx(&cfg, k_balance_join<false>, a, lq);
 }
 
 cudaError_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t s) {

@@ -40,7 +40,7 @@ def run_balance(cfg, l, idx, off, mask, ws=None):
 
 SHAPES = [(1, 8, 1, 1), (1, 8, 8, 3), (5, 9, 3, 2), (64, 32, 2, 1), (100, 33, 4, 7), (1000, 64, 8, 60), (777, 128, 8, 5),
           (4096, 256, 8, 9), (9000, 100, 6, 1), (500, 256, 40, 3),
-          (20000, 12, 3, 300), (6000, 40, 2, 2000), (300000, 8, 2, 40)]
+          (20000, 12, 3, 300), (6000, 40, 2, 2000), (300000, 8, 2, 40), (5000, 256, 8, 1)]
 
 
 @pytest.mark.parametrize("routing", [0, 1])
