@@ -212,18 +212,16 @@ bool get_linear_config(PyObject* o, moe_linear_config_t* c) {
 
 int64_t scale_rows(int64_t rows) { return (rows + 135) / 4 * 4; }
 
-// A pair (codes [rows, cols], scale words [cols/128, scale_rows]), or None.
-bool quantized_args(const Call& c, PyObject* q, int64_t rows, int64_t cols, void** codes, void** scales) {
+// A pair (codes [rows, cols], scale words [cols/128, scale_rows]), or None; held keeps the two.
+bool quantized_args(const Call& c, PyObject* q, int64_t rows, int64_t cols, void** codes, void** scales, Refs& held) {
     *codes = *scales = nullptr;
     if (q == Py_None) return true;
     if (!PyTuple_Check(q) && !PyList_Check(q)) return refuse("quantized must be a pair (codes, scale words)");
     if (PySequence_Size(q) != 2) return refuse("quantized must be a pair (codes, scale words)");
-    PyObject *a = PySequence_GetItem(q, 0), *b = PySequence_GetItem(q, 1);
-    const bool ok = a && b && c.arg(a, "codes", {rows, cols}, at::kByte, codes) &&
-                    c.arg(b, "scales", {cols / 128, scale_rows(rows)}, at::kInt, scales);
-    Py_XDECREF(a);
-    Py_XDECREF(b);
-    return ok;
+    held.p[0] = PySequence_GetItem(q, 0);
+    held.p[1] = PySequence_GetItem(q, 1);
+    return held.p[0] && held.p[1] && c.arg(held.p[0], "codes", {rows, cols}, at::kByte, codes) &&
+           c.arg(held.p[1], "scales", {cols / 128, scale_rows(rows)}, at::kInt, scales);
 }
 
 // The sequences' mask and offsets; n: how many sequences.
@@ -263,7 +261,7 @@ PyObject* add_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     PyObject *x = a[1], *res = a[4], *res_out = a[5], *quantized = a[7];
     moe_config_t cfg{};
     Call c;
-    Refs out;
+    Refs out, held;
     if (!get_config(a[0], &cfg) || !c.begin(x, "x", a[10])) return nullptr;
     const double eps = PyFloat_AsDouble(a[3]);
     if (eps == -1.0 && PyErr_Occurred()) return nullptr;
@@ -296,7 +294,7 @@ PyObject* add_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (!c.output(a[6], "y", {T, H}, at::kBFloat16, &py, &out.p[1])) return nullptr;
     }
     if (quantized != Py_None) {
-        if (!quantized_args(c, quantized, T, H, &pq, &ps)) return nullptr;
+        if (!quantized_args(c, quantized, T, H, &pq, &ps, held)) return nullptr;
         Py_INCREF(quantized);
         out.p[2] = quantized;
     } else if (want_q) {
@@ -346,12 +344,12 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
         refuse("weights must be the pair (w_t, ws_t) of transform_linear_weights");
         return nullptr;
     }
-    Refs w;
+    Refs w, held;
     w.p[0] = PySequence_GetItem(weights, 0);
     w.p[1] = PySequence_GetItem(weights, 1);
     void *px, *pq, *ps, *pw, *pws, *pb, *pr, *py, *pk;
     size_t have, need = MOE_LINEAR_STATUS_BYTES;
-    if (!c.arg(x, "x", {T, K}, at::kBFloat16, &px) || !quantized_args(c, quantized, T, K, &pq, &ps) ||
+    if (!c.arg(x, "x", {T, K}, at::kBFloat16, &px) || !quantized_args(c, quantized, T, K, &pq, &ps, held) ||
         !c.arg(w.p[0], "w_t", {K * N / (cfg.recipe == 2 ? 2 : 1)}, at::kByte, &pw) ||
         !c.arg(w.p[1], "ws_t", {K / 128 * ((N + 255) / 256 * 256) * 4}, at::kByte, &pws) ||
         !c.arg(a[4], "bias", {N}, at::kBFloat16, &pb) || !c.arg(a[5], "residual", {T, N}, at::kBFloat16, &pr))
