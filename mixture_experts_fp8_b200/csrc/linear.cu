@@ -7,11 +7,14 @@
 // leaves the tensor core and is promoted, acc += P * (a_s * w_s): two fp32 operations an element and
 // group, 256 cycles for 128 x 128 at 128 a cycle, as long as the MMAs themselves.
 //
-// CTA pairs (cta_group::2), persistent: a tile is 256 tokens x 128 columns; each CTA of the pair holds
-// 128 token rows and half of the weight rows (24 KB a stage) and promotes its own 128 x 128 sums.  Two
-// groups are handed over at a time (a step): four 128-column TMEM buffers make two steps, the epilogue
-// waits once, takes both partials into registers (64, beside 32 sums), hands the buffers back, and only
-// then computes, so that the MMAs of the step after next run meanwhile.  The scales have a ring of their
+// CTA pairs (cta_group::2), persistent: a tile is 128 columns of one or two row blocks of 256 tokens; each
+// CTA of the pair holds 128 token rows a block and half of the weight rows, and promotes its own sums.
+// Sums are handed over a step at a time: four 128-column TMEM buffers make two steps, and a step is two
+// groups of one row block (the epilogue waits once, takes both partials into registers, 64 beside 32 sums, hands the
+// buffers back, and only then computes) or one group of two.  What bounds it is shared memory: a group
+// of 128 x 128 sums reads the weight scales once a row (a broadcast to 32 rows a warp, 270 cycles of its
+// bandwidth), beside the operands' TMA writes (190) and the MMAs' reads (256).  Two row blocks share the
+// loads of the weight scales (a thread has a row of each) and the weights.  The scales have a ring of their
 // own, and an operand stage is free when its MMAs are done.
 //
 // Threads (640): warp 0 TMA producer, warp 1 MMA issuer (the even CTA's, for both), warp 2 scales,
@@ -25,7 +28,6 @@ namespace moe {
 namespace {
 
 constexpr int kN = kPairN0;
-constexpr int kStages = 7;
 constexpr int kSteps = 6;                              // scale slots, and barriers of finished steps
 constexpr int kAhead = 3;                              // steps that the scales are fetched ahead
 constexpr int kThreads = 640;
@@ -36,26 +38,31 @@ constexpr int kRegsLaunch = 96, kRegsLow = 32, kRegsHigh = 112;
 static_assert(128 * kRegsLow + 512 * kRegsHigh == kThreads * kRegsLaunch, "register split");
 constexpr uint32_t kABytes = kTileM * kTileK;
 constexpr uint32_t kBBytes = kN / 2 * kTileK;
-constexpr uint32_t kStageBytes = kABytes + kBBytes;
 constexpr uint32_t kWsBytes = kN * 4;
-constexpr uint32_t kGroupScales = kWsBytes + kTileM * 4;   // a group's weight scales, then the rows' own
-constexpr uint32_t kScSlot = 2 * kGroupScales;
+constexpr uint32_t kSaBytes = kTileM * 4;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kStepCols = 2 * kN;
 
+// RB: row blocks of a tile, 256 tokens each.
+template <int RB>
 struct L {
-    static constexpr uint32_t out = kStages * kStageBytes;
+    static constexpr int stages = RB == 1 ? 7 : 4;
+    static constexpr uint32_t stage = RB * kABytes + kBBytes;
+    // a step's scales: the weights' of its groups and the rows' (RB 1: [weights, rows] of two groups; 2: [weights, rows, rows])
+    static constexpr uint32_t group_scales = kWsBytes + kSaBytes;
+    static constexpr uint32_t slot = RB == 1 ? 2 * group_scales : kWsBytes + 2 * kSaBytes;
+    static constexpr uint32_t out = stages * stage;
     static constexpr uint32_t sc = out + kEpiWarps * Sub<kSubCols0>::bytes;
-    static constexpr uint32_t bars = sc + kSteps * kScSlot;
-    // full[kStages], empty[kStages], tempty[2], tfull[kSteps], drain
-    static constexpr uint32_t nbars = 2 * kStages + kSteps + 3;
+    static constexpr uint32_t bars = sc + kSteps * slot;
+    // full[stages], empty[stages], tempty[2], tfull[kSteps], drain
+    static constexpr uint32_t nbars = 2 * stages + kSteps + 3;
     static constexpr uint32_t misc = bars + nbars * 8;    // tmem holder, abort flag
     static constexpr uint32_t end = misc + 16;
-    static_assert((bars + 16 * kStages) % 16 == 0, "the two tempty barriers are one bit apart");
+    static constexpr uint32_t smem = end + 1024;          // + slack to align the base to 1024 bytes
+    static_assert((bars + 16 * stages) % 16 == 0, "the two tempty barriers are one bit apart");
+    static_assert(stage % 1024 == 0 && out % 512 == 0 && slot % 16 == 0, "alignment");
+    static_assert(smem <= 232448, "shared memory");
 };
-static_assert(kStageBytes % 1024 == 0 && L::out % 512 == 0 && kScSlot % 16 == 0, "alignment");
-constexpr uint32_t kSmemBytes = L::end + 1024;         // + slack to align the base to 1024 bytes
-static_assert(kSmemBytes <= 232448, "shared memory");
 
 __device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                             uint32_t accumulate) {
@@ -89,6 +96,23 @@ __device__ __forceinline__ void promote(float2 (&acc)[16], const uint32_t (&v)[3
     }
 }
 
+// Two rows with the same columns, sixteen of them: acc[r][j] += P[r][j] * (s[r] * ws[j]) from column 4 J on; the weight
+// scales are loaded once for both.
+template <int OFF, int J>
+__device__ __forceinline__ void promote2(float2* a0, float2* a1, const uint32_t (&v0)[16], const uint32_t (&v1)[16], uint32_t sc,
+                                         float2 s0, float2 s1) {
+    if constexpr (J < 4) {
+        const float4 w4 = lds_f32x4_at<OFF + 16 * J>(sc);
+        const float2 wa = make_float2(w4.x, w4.y), wb = make_float2(w4.z, w4.w);
+        auto p2 = [](const uint32_t (&v)[16], int i) { return make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])); };
+        a0[2 * J] = __ffma2_rn(p2(v0, 4 * J), __fmul2_rn(wa, s0), a0[2 * J]);
+        a1[2 * J] = __ffma2_rn(p2(v1, 4 * J), __fmul2_rn(wa, s1), a1[2 * J]);
+        a0[2 * J + 1] = __ffma2_rn(p2(v0, 4 * J + 2), __fmul2_rn(wb, s0), a0[2 * J + 1]);
+        a1[2 * J + 1] = __ffma2_rn(p2(v1, 4 * J + 2), __fmul2_rn(wb, s1), a1[2 * J + 1]);
+        promote2<OFF, J + 1>(a0, a1, v0, v1, sc, s0, s1);
+    }
+}
+
 // One arrival from lane 0 of the warp on a barrier of the cluster (arrive_pair), predicated inside the asm.
 __device__ __forceinline__ void arrive_pair_lane0(uint32_t bar, int lane) {
     asm volatile(
@@ -99,11 +123,15 @@ __device__ __forceinline__ void arrive_pair_lane0(uint32_t bar, int lane) {
 
 }  // namespace
 
+template <int RB>
 __global__ void __launch_bounds__(kThreads, 1)
     k_linear_fp32(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap, const __grid_constant__ CUtensorMap tmY, const LinearArgs p) {
+    using S = L<RB>;
+    constexpr int kStages = S::stages, kM = RB * kPairM;
+    constexpr int kGroups = RB == 1 ? 2 : 1;           // K groups of a step
     extern __shared__ uint8_t smem_raw[];
-    const int mt = (p.T + kPairM - 1) / kPairM, nt = (p.N + kN - 1) / kN;
+    const int mt = (p.T + kM - 1) / kM, nt = (p.N + kN - 1) / kN;
     const int total_units = mt * nt;
     const int KB = p.K / kTileK;
     const uint32_t rank = cluster_ctarank();
@@ -111,13 +139,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const uint32_t raw_addr = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bars);      // the even CTA's count for both
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::bars);      // the even CTA's count for both
     uint64_t* empty = full + kStages;                                  // one in each CTA
     uint64_t* tempty = empty + kStages;                                // the even CTA's
     uint64_t* tfull = tempty + 2;                                      // in each CTA: a step's MMAs and scales
     uint64_t* drain = tfull + kSteps;
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::misc);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::misc + 4);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + S::misc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::misc + 4);
 
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -152,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int u = pair; u < total_units && ok; u += pairs) {
                 const int nb = u / mt, mb = u - nb * mt;
-                const int row0 = mb * kPairM + static_cast<int>(rank) * kTileM;
+                const int row0 = mb * kM + static_cast<int>(rank) * kTileM;
                 const int brow0 = nb * kN + static_cast<int>(rank) * (kN / 2);
                 for (int kb = 0; kb < KB; ++kb, ++it) {
                     if (!mbar_wait<kProducerSleepNs>(&empty[s], ph, abort_flag, p.status)) {
@@ -161,9 +189,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const uint32_t bar = pair_addr(smem_u32(&full[s]), 0);
                     if (elect_one()) {
-                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
-                        tma_load_2d_pair(smem + s * kStageBytes, &tmA, kb * kTileK, row0, bar);
-                        tma_load_2d_pair(smem + s * kStageBytes + kABytes, &tmB, kb * kTileK, brow0, bar);
+                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * S::stage);
+#pragma unroll
+                        for (int b = 0; b < RB; ++b)
+                            tma_load_2d_pair(smem + s * S::stage + b * kABytes, &tmA, kb * kTileK, row0 + b * kPairM, bar);
+                        tma_load_2d_pair(smem + s * S::stage + RB * kABytes, &tmB, kb * kTileK, brow0, bar);
                     }
                     __syncwarp();
                     if (++s == kStages) {
@@ -190,11 +220,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int u = pair; u < total_units && ok; u += pairs) {
                 const int nb = u / mt, mb = u - nb * mt;
-                const int row0 = mb * kPairM + static_cast<int>(rank) * kTileM;
-                const uint32_t a_bytes = row0 < p.T ? kTileM * 4u : 0u;   // the scale rows reach 132 past T
+                const int row0 = mb * kM + static_cast<int>(rank) * kTileM;
+                uint32_t a_bytes[RB];                  // the scale rows reach 132 past T
+#pragma unroll
+                for (int b = 0; b < RB; ++b) a_bytes[b] = row0 + b * kPairM < p.T ? kSaBytes : 0u;
                 const float* ws_src = static_cast<const float*>(p.w_scale) + nb * kN;
                 const float* sa_src = static_cast<const float*>(p.a_scale) + row0;
-                for (int kb = 0; kb < KB; kb += 2, ++it) {
+                for (int kb = 0; kb < KB; kb += kGroups, ++it) {
                     if (it >= kAhead) {
                         const uint32_t g = it - kAhead;
                         if (!mbar_wait<kProducerSleepNs>(&tfull[g % kSteps], (g / kSteps) & 1, abort_flag, p.status)) {
@@ -202,14 +234,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                             break;
                         }
                     }
-                    const int s = it % kSteps, n = min(2, KB - kb);
+                    const int s = it % kSteps, n = min(kGroups, KB - kb);
                     if (elect_one()) {
-                        mbar_arrive_expect_tx(&tfull[s], static_cast<uint32_t>(n) * (kWsBytes + a_bytes));
+                        mbar_arrive_expect_tx(&tfull[s], static_cast<uint32_t>(n) * (kWsBytes + a_bytes[0] + (RB == 2 ? a_bytes[RB - 1] : 0u)));
                         for (int i = 0; i < n; ++i) {
-                            uint8_t* slot = smem + L::sc + s * kScSlot + i * kGroupScales;
+                            uint8_t* slot = smem + S::sc + s * S::slot + i * S::group_scales;
                             bulk_load(slot, ws_src + static_cast<size_t>(kb + i) * n_pad, kWsBytes, &tfull[s]);
-                            if (a_bytes)
-                                bulk_load(slot + kWsBytes, sa_src + static_cast<size_t>(kb + i) * p.a_pad, a_bytes, &tfull[s]);
+#pragma unroll
+                            for (int b = 0; b < RB; ++b)
+                                if (a_bytes[b])
+                                    bulk_load(slot + kWsBytes + b * kSaBytes,
+                                              sa_src + static_cast<size_t>(kb + i) * p.a_pad + b * kPairM, kSaBytes, &tfull[s]);
                         }
                     }
                     __syncwarp();
@@ -223,23 +258,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             // -------------------------------------------------------------- MMA issuer, for the pair
             const uint32_t idesc = f8_idesc(kPairM, kN);
             const uint64_t a_desc0 = sw128_kmajor_desc(smem_u32(smem));
-            const uint64_t b_desc0 = sw128_kmajor_desc(smem_u32(smem + kABytes));
+            const uint64_t b_desc0 = sw128_kmajor_desc(smem_u32(smem + RB * kABytes));
             uint32_t s = 0, ph = 0, buf = 0, bph = 0, step = 0;
             bool ok = true;
             for (int u = pair; u < total_units && ok; u += pairs) {
                 for (int kb = 0; kb < KB; ++kb) {
-                    if (((kb & 1) == 0 && !mbar_wait<kIssuerSleepNs>(&tempty[buf], bph ^ 1, abort_flag, p.status)) ||
+                    const int half = RB == 1 ? kb & 1 : 0;         // of the step's TMEM
+                    if ((half == 0 && !mbar_wait<kIssuerSleepNs>(&tempty[buf], bph ^ 1, abort_flag, p.status)) ||
                         !mbar_wait<kIssuerSleepNs>(&full[s], ph, abort_flag, p.status)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t ad = a_desc0 + s * (kStageBytes >> 4), bd = b_desc0 + s * (kStageBytes >> 4);
-                    const uint32_t d = tmem_base + buf * kStepCols + (kb & 1) * kN;
-                    const bool last = (kb & 1) || kb == KB - 1;    // the step is complete
+                    const uint64_t ad = a_desc0 + s * (S::stage >> 4), bd = b_desc0 + s * (S::stage >> 4);
+                    const uint32_t d = tmem_base + buf * kStepCols + half * kN;
+                    const bool last = RB == 2 || half || kb == KB - 1;   // the step is complete
                     if (elect_one()) {
 #pragma unroll
-                        for (int m = 0; m < MPG; ++m) mma_f8_pair(d, ad + 2 * m, bd + 2 * m, idesc, m > 0 ? 1u : 0u);
+                        for (int b = 0; b < RB; ++b)
+#pragma unroll
+                            for (int m = 0; m < MPG; ++m)
+                                mma_f8_pair(d + b * kN, ad + b * (kABytes >> 4) + 2 * m, bd + 2 * m, idesc, m > 0 ? 1u : 0u);
                         mma_commit2(&empty[s]);
                         if (last) mma_commit2(&tfull[step]);
                     }
@@ -267,12 +306,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         EpiAt at;
         at.qtr = qtr;
         at.quad = quad;
-        at.quad_sub = smem_u32(smem + L::out) + static_cast<uint32_t>(quad) * Sub<kSubCols0>::bytes;
+        at.quad_sub = smem_u32(smem + S::out) + static_cast<uint32_t>(quad) * Sub<kSubCols0>::bytes;
         at.sub = at.quad_sub + static_cast<uint32_t>(4 * qtr) * Sub<kSubCols0>::bytes;
-        const uint32_t abort_at = smem_u32(smem + L::misc + 4);
+        const uint32_t abort_at = smem_u32(smem + S::misc + 4);
         // the step's barrier, weight scales, TMEM and TMEM barrier (256 columns and 8 bytes apart)
         const uint32_t tf0 = smem_u32(tfull), tf_end = tf0 + 8 * kSteps;
-        const uint32_t sc0 = smem_u32(smem + L::sc) + static_cast<uint32_t>(32 * qtr * 4);
+        const uint32_t sc0 = smem_u32(smem + S::sc) + static_cast<uint32_t>(32 * qtr * 4);
         const uint32_t sa_off = kWsBytes + static_cast<uint32_t>((quad * 32 + lane - 32 * qtr) * 4);   // from there, the row's scale
         uint32_t tf_at = tf0, sc_at = sc0, ph = 0;
         uint32_t t_at = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(32 * qtr);
@@ -280,38 +319,55 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int u = pair; u < total_units && ok; u += pairs) {
             const int nb = u / mt, mb = u - nb * mt;
-            at.t0 = mb * kPairM + static_cast<int>(rank) * kTileM + quad * 32;
+            at.t0 = mb * kM + static_cast<int>(rank) * kTileM + quad * 32;
             at.tile_c0 = nb * kN;
             at.c0 = at.tile_c0 + 32 * qtr;
             uint32_t last;
             epilogue_store_wait();                     // the last tile's store has read the subtile
             epilogue_residual<kSubCols0>(p, at, last);
-            float2 acc2[16];
+            float2 acc2[RB][16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) acc2[i] = make_float2(0.0f, 0.0f);
-            for (int kb = 0; kb < KB; kb += 2) {
+            for (int i = 0; i < 16 * RB; ++i) acc2[i / 16][i % 16] = make_float2(0.0f, 0.0f);
+            for (int kb = 0; kb < KB; kb += kGroups) {
                 if (!mbar_wait_at(tf_at, ph, abort_at, p.status)) {   // the partials and their scales
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const bool two = kb + 1 < KB;
-                uint32_t va[32], vb[32];
-                MOE_TMEM_LD32(t_at, va);
-                if (two) MOE_TMEM_LD32(t_at + kN, vb);
-                const float s0 = ld_shared_f32(sc_at + sa_off), s1 = two ? ld_shared_f32(sc_at + sa_off + kGroupScales) : 0.0f;
-                MOE_TMEM_WAIT_LD(va);
-                if (two) MOE_TMEM_WAIT_LD(vb);
-                // the warp holds its partials: hand the buffers back
-                tc_fence_before();
-                arrive_pair_lane0(te_at, lane);
-                promote<0, 0>(acc2, va, sc_at, make_float2(s0, s0));
-                if (two) promote<kGroupScales, 0>(acc2, vb, sc_at, make_float2(s1, s1));
+                if constexpr (RB == 1) {
+                    const bool two = kb + 1 < KB;
+                    uint32_t va[32], vb[32];
+                    MOE_TMEM_LD32(t_at, va);
+                    if (two) MOE_TMEM_LD32(t_at + kN, vb);
+                    const float s0 = ld_shared_f32(sc_at + sa_off), s1 = two ? ld_shared_f32(sc_at + sa_off + S::group_scales) : 0.0f;
+                    MOE_TMEM_WAIT_LD(va);
+                    if (two) MOE_TMEM_WAIT_LD(vb);
+                    // the warp holds its partials: hand the buffers back
+                    tc_fence_before();
+                    arrive_pair_lane0(te_at, lane);
+                    promote<0, 0>(acc2[0], va, sc_at, make_float2(s0, s0));
+                    if (two) promote<S::group_scales, 0>(acc2[0], vb, sc_at, make_float2(s1, s1));
+                } else {
+                    uint32_t va[16], vb[16];
+                    MOE_TMEM_LD16(t_at, va);
+                    MOE_TMEM_LD16(t_at + kN, vb);
+                    const float s0 = ld_shared_f32(sc_at + sa_off), s1 = ld_shared_f32(sc_at + sa_off + kSaBytes);
+                    MOE_TMEM_WAIT_LD16(va);
+                    MOE_TMEM_WAIT_LD16(vb);
+                    promote2<0, 0>(acc2[0], acc2[RB - 1], va, vb, sc_at, make_float2(s0, s0), make_float2(s1, s1));
+                    MOE_TMEM_LD16(t_at + 16, va);
+                    MOE_TMEM_LD16(t_at + 16 + kN, vb);
+                    MOE_TMEM_WAIT_LD16(va);
+                    MOE_TMEM_WAIT_LD16(vb);
+                    tc_fence_before();
+                    arrive_pair_lane0(te_at, lane);
+                    promote2<64, 0>(acc2[0] + 8, acc2[RB - 1] + 8, va, vb, sc_at, make_float2(s0, s0), make_float2(s1, s1));
+                }
                 // the scales were read through the generic proxy; the next bulk copy into this slot is an
                 // async-proxy write: order the reads before it (the next step's arrival carries that on)
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 tf_at += 8;
-                sc_at += kScSlot;
+                sc_at += S::slot;
                 if (tf_at == tf_end) {
                     tf_at = tf0;
                     sc_at = sc0;
@@ -322,8 +378,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ok = epilogue_residual_wait(p, at, ok);
             if (!ok) break;
-            epilogue_sub<kSubCols0>(p, at, last, reinterpret_cast<float*>(acc2));
+            epilogue_sub<kSubCols0>(p, at, last, reinterpret_cast<float*>(acc2[0]));
             epilogue_store<kSubCols0>(p, &tmY, at);
+            if constexpr (RB == 2) {                   // the second row block through the same subtile
+                at.t0 += kPairM;
+                epilogue_store_wait();
+                epilogue_residual<kSubCols0>(p, at, last);
+                epilogue_residual_wait(p, at, true);
+                epilogue_sub<kSubCols0>(p, at, last, reinterpret_cast<float*>(acc2[RB - 1]));
+                epilogue_store<kSubCols0>(p, &tmY, at);
+            }
         }
         epilogue_drain();
     }
@@ -339,14 +403,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-cudaError_t launch_linear_fp32(const LinearArgs& a, const LinearMaps& m, int num_sms, cudaStream_t s) {
+template <int RB>
+static cudaError_t launch_fp32(const LinearArgs& a, const LinearMaps& m, int num_sms, cudaStream_t s) {
     // The register split above must fit what the block is launched with, or setmaxnreg.inc would
     // wait forever: refuse to launch otherwise.
     cudaFuncAttributes fa;
-    const cudaError_t e = cudaFuncGetAttributes(&fa, k_linear_fp32);
+    const cudaError_t e = cudaFuncGetAttributes(&fa, k_linear_fp32<RB>);
     if (e != cudaSuccess) return e;
     if (fa.numRegs * kThreads < kRegsLow * 128 + kRegsHigh * 512) return cudaErrorInvalidConfiguration;
-    return launch_pair(k_linear_fp32, kThreads, kSmemBytes, a, m, num_sms, s);
+    return launch_pair(k_linear_fp32<RB>, kThreads, L<RB>::smem, a, m, num_sms, s);
+}
+
+// Tiles of 512 tokens where their rounds are estimated to take no longer than those of 256: a round is a time per K
+// group and one for the tile's start and epilogue, 0.58 and 2.5 us against 0.34 and 0.9, fitted to 2048 to 16384
+// tokens with K 512 to 7168.  16384 x 4096 x 4096: 305 us against 320; 16384 x 7168 x 2048: 263 against 321; in 7
+// rounds instead of 13, 4096 x 7168 x 7168: 213 against 232; but in 3 instead of 5, 2560 x 4096 x 4096: 65 against
+// 63, and with four groups, 8192 x 512 x 6144: 53 against 49.
+cudaError_t launch_linear_fp32(const LinearArgs& a, const LinearMaps& m, int num_sms, cudaStream_t s) {
+    const long long pairs = num_sms / 2, nt = (a.N + kN - 1) / kN, KB = a.K / kTileK;
+    auto rounds = [&](int rows) { return ((a.T + rows - 1) / rows * nt + pairs - 1) / pairs; };
+    return rounds(2 * kPairM) * (58 * KB + 250) <= rounds(kPairM) * (34 * KB + 90) ? launch_fp32<2>(a, m, num_sms, s)
+                                                                                  : launch_fp32<1>(a, m, num_sms, s);
 }
 
 // The narrow kernel takes a product when its estimated time is below the pair kernel's.  Both estimates

@@ -48,6 +48,27 @@ def test_against_64_bits(T, K, N, recipe):
     check(y, *linear(dequantize(q[0], q[1], recipe), wd, bias, a, res))
 
 
+# tiles of 512 tokens (from seven K groups on, an even and an odd number of them; the last one's second half empty or
+# ragged; N in eights, even and odd) and of 256
+@pytest.mark.parametrize("T,K,N", [(1024, 256, 4736), (1500, 640, 4738), (900, 384, 4729), (1100, 128, 4800), (2048, 1152, 2304),
+                                   (900, 1152, 4729), (1024, 1024, 4730), (1500, 1408, 4736), (1700, 1280, 4673)])
+def test_long_batches_of_fp32_scales(T, K, N):
+    codes, scales, wd, x, bias, res = problem(T, K, N, 0, T + N)
+    cfg = moe.LinearConfig(T, K, N, 0, N % 5)
+    w = moe.transform_linear_weights(cfg, codes.cuda(), scales.cuda())
+    q = quantize(x, 0)
+    ws = moe.new_linear_workspace(cfg)
+    buf = res.cuda()
+    y = moe.linear(cfg, w, quantized=tuple(t.cuda() for t in q), bias=bias.cuda(), residual=buf, y=buf, workspace=ws)
+    assert moe.read_status(ws) == 0
+    check(y, *linear(dequantize(q[0], q[1], 0), wd, bias, N % 5, res))
+    # the same bits in a batch of few enough rows for the smaller tile
+    part = moe.LinearConfig(256, K, N, 0, N % 5)
+    r = T - 256
+    few = moe.linear(part, w, x=x[r:].cuda(), bias=bias.cuda(), residual=res[r:].contiguous().cuda())
+    assert torch.equal(few, y[r:])
+
+
 @pytest.mark.parametrize("a", range(5))
 @pytest.mark.parametrize("recipe,T,N", [(0, 5, 256), (1, 200, 264), (2, 70, 130)])
 @pytest.mark.parametrize("with_bias,with_res", [(False, False), (True, False), (False, True)])
