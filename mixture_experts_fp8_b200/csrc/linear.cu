@@ -10,12 +10,13 @@
 // CTA pairs (cta_group::2), persistent: a tile is 128 columns of one or two row blocks of 256 tokens; each
 // CTA of the pair holds 128 token rows a block and half of the weight rows, and promotes its own sums.
 // Sums are handed over a step at a time: four 128-column TMEM buffers make two steps, and a step is two
-// groups of one row block (the epilogue waits once, takes both partials into registers, 64 beside 32 sums, hands the
-// buffers back, and only then computes) or one group of two.  What bounds it is shared memory: a group
-// of 128 x 128 sums reads the weight scales once a row (a broadcast to 32 rows a warp, 270 cycles of its
+// groups of one row block (the epilogue waits once, takes both partials into registers, 64 beside 32
+// sums, hands the buffers back, and only then computes) or one group of two.  What bounds it is shared
+// memory: a group of 128 x 128 sums reads the weight scales once a row (broadcasts, 270 cycles of its
 // bandwidth), beside the operands' TMA writes (190) and the MMAs' reads (256).  Two row blocks share the
-// loads of the weight scales (a thread has a row of each) and the weights.  The scales have a ring of their
-// own, and an operand stage is free when its MMAs are done.
+// loads of the weights and of their scales (a thread has a row of each).  The scales have a ring of
+// their own, and an operand stage is free when its MMAs are done.  16384 x 4096 x 4096: 306 us, 1.8
+// PFLOP/s, the tensor core active 46% of the time and the issue slots 55%.
 //
 // Threads (640): warp 0 TMA producer, warp 1 MMA issuer (the even CTA's, for both), warp 2 scales,
 // warp 3 idle, warps 4-19 epilogue (TMEM lanes 32 (w % 4).., 32 columns each).  Units go column block

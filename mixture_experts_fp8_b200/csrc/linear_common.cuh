@@ -313,7 +313,7 @@ __device__ __forceinline__ void arrive_pair(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Tiles of the pair kernels: 256 tokens x 128 columns (fp32 scales) or 192 (block-scaled).
+// Tiles of the pair kernels: 256 tokens (fp32 scales: or two such blocks) x 128 columns (fp32 scales) or 192 (block-scaled).
 constexpr int kPairM = 2 * kTileM;
 constexpr int kPairN0 = 128, kPairNX = 192;
 // Columns of an output subtile.
