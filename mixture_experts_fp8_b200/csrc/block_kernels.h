@@ -74,6 +74,7 @@ struct LinearBoxes {
     uint32_t x, w, y;
     bool pair;                  // the pair kernels' maps are needed too
 };
+int linear_mx_cols(const LinearArgs& a, int num_sms);   // columns of a block-scaled pair kernel's tile
 LinearBoxes linear_boxes(const LinearArgs& a, int num_sms);
 cudaError_t launch_linear(const LinearArgs& a, const LinearMaps& m, int num_sms, cudaStream_t s);
 cudaError_t launch_linear_narrow(const LinearArgs& a, const LinearMaps& m, int num_sms, cudaStream_t s);

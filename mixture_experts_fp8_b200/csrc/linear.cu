@@ -450,7 +450,9 @@ bool linear_is_narrow(int T, int N, int K, int recipe, int num_sms) {
 LinearBoxes linear_boxes(const LinearArgs& a, int num_sms) {
     if (linear_is_narrow(a.T, a.N, a.K, a.recipe, num_sms))
         return {static_cast<uint32_t>(linear_narrow_tokens(a.T)), kTileM, 0, false};
-    return a.recipe == 0 ? LinearBoxes{kTileM, kPairN0 / 2, kSubCols0, true} : LinearBoxes{kTileM, kPairNX / 2, kSubColsX, true};
+    if (a.recipe == 0) return {kTileM, kPairN0 / 2, kSubCols0, true};
+    return linear_mx_cols(a, num_sms) == kPairNW ? LinearBoxes{kTileM, kPairNW / 2, kSubColsW, true}
+                                                 : LinearBoxes{kTileM, kPairNX / 2, kSubColsX, true};
 }
 
 cudaError_t launch_linear(const LinearArgs& a, const LinearMaps& m, int num_sms, cudaStream_t s) {

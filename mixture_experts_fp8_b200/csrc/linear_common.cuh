@@ -313,11 +313,12 @@ __device__ __forceinline__ void arrive_pair(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Tiles of the pair kernels: 256 tokens (fp32 scales: or two such blocks) x 128 columns (fp32 scales) or 192 (block-scaled).
+// Tiles of the pair kernels: 256 tokens, or two such blocks, x 128 columns (fp32 scales); 256 tokens x 192 or
+// 256 columns (block-scaled).
 constexpr int kPairM = 2 * kTileM;
-constexpr int kPairN0 = 128, kPairNX = 192;
+constexpr int kPairN0 = 128, kPairNX = 192, kPairNW = 256;
 // Columns of an output subtile.
-constexpr int kSubCols0 = 32, kSubColsX = 48;
+constexpr int kSubCols0 = 32, kSubColsX = 48, kSubColsW = 32;
 
 // Launch a pair kernel: one CTA an SM, clusters of two.
 template <typename K>

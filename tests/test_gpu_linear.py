@@ -69,6 +69,22 @@ def test_long_batches_of_fp32_scales(T, K, N):
     assert torch.equal(few, y[r:])
 
 
+# tiles of 256 columns: one and several a pair, the last one narrow, N in eights, even and odd
+@pytest.mark.parametrize("recipe", [1, 2])
+@pytest.mark.parametrize("T,K,N", [(512, 1024, 9472), (1500, 896, 4738), (2500, 768, 3594), (2048, 1152, 4096), (1030, 640, 7937), (1500, 1024, 4737)])
+def test_long_batches_of_block_scales(T, K, N, recipe):
+    N += N % 2 if recipe == 2 else 0
+    codes, scales, wd, x, bias, res = problem(T, K, N, recipe, T + N)
+    cfg = moe.LinearConfig(T, K, N, recipe, N % 5)
+    w = moe.transform_linear_weights(cfg, codes.cuda(), scales.cuda())
+    q = quantize(x, recipe)
+    ws = moe.new_linear_workspace(cfg)
+    buf = res.cuda()
+    y = moe.linear(cfg, w, quantized=tuple(t.cuda() for t in q), bias=bias.cuda(), residual=buf, y=buf, workspace=ws)
+    assert moe.read_status(ws) == 0
+    check(y, *linear(dequantize(q[0], q[1], recipe), wd, bias, N % 5, res))
+
+
 @pytest.mark.parametrize("a", range(5))
 @pytest.mark.parametrize("recipe,T,N", [(0, 5, 256), (1, 200, 264), (2, 70, 130)])
 @pytest.mark.parametrize("with_bias,with_res", [(False, False), (True, False), (False, True)])
