@@ -109,3 +109,36 @@ def test_config_numbers_of_other_types():
     n = torch.tensor(T)
     b = moe.add_rms_norm(cfg(num_tokens=n, hidden=n.numpy().dtype.type(H), routed_scaling_factor=1), x, w, n.new_tensor(1e-6, dtype=torch.float64))[1]
     assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_calls_from_two_threads():
+    """Each thread with a stream and a workspace of its own; a refusal in one leaves the other's calls alone."""
+    import threading
+    lin = moe.LinearConfig(T, H, 64)
+    w = moe.transform_linear_weights(lin, torch.full((H, 64), 56, dtype=torch.uint8, device="cuda"), torch.ones((H // 128, 64), device="cuda"))
+    nw = torch.ones(H, device="cuda")
+    xs = [torch.randn(T, H, device="cuda").bfloat16() for _ in range(2)]
+    want = [moe.linear(lin, w, x=moe.add_rms_norm(cfg(), x, nw, 1e-6)[1]) for x in xs]
+    torch.cuda.synchronize()
+    wrong = [0, 0]
+
+    def run(i):
+        s, ws = torch.cuda.Stream(), moe.new_linear_workspace(lin)
+        with torch.cuda.stream(s):
+            for _ in range(200):
+                y = moe.linear(lin, w, x=moe.add_rms_norm(cfg(), xs[i], nw, 1e-6)[1], workspace=ws)
+                try:
+                    moe.linear(lin, w, x=xs[i], workspace=ws[:512])
+                    wrong[i] += 1
+                except moe.MoeError as e:
+                    wrong[i] += "512 bytes" not in str(e)
+            s.synchronize()
+            wrong[i] += not torch.equal(y, want[i])
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert wrong == [0, 0]
