@@ -14,6 +14,9 @@ Entry points (same names as the C ABI):
     Profile (moe_profile_create / read / reset / destroy);
 around the layer:
     add_rms_norm, transform_linear_weights, linear, balance_loss, route_backward.
+
+With `stream`, the operators around the layer allocate what they return from that stream's pool: the
+results are that stream's, and another stream waits for it before it reads them.
 """
 from __future__ import annotations
 
@@ -478,10 +481,14 @@ def _arg(t, name: str, shape, dtype, dev):
 
 
 def _new(like, shape, dtype, stream):
-    """A tensor that the call allocates; on a stream other than the current one the allocator is told."""
-    t = like.new_empty(shape, dtype=dtype)
-    if stream is not None:
-        t.record_stream(stream)
+    """A tensor that the call allocates, from the pool of the stream that it runs on: a block of the current stream's
+    pool may still be in use there.  Once freed it is kept until the current stream, too, has passed."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    current = torch.cuda.current_stream(like.device)
+    with torch.cuda.stream(stream):
+        t = like.new_empty(shape, dtype=dtype)
+    t.record_stream(current)
     return t
 
 

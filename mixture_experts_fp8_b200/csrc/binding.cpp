@@ -8,6 +8,7 @@
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include <cstdint>
@@ -72,7 +73,7 @@ bool tensor(PyObject* o, const char* name, const at::Tensor** out) {
 struct Call {
     int dev = -1;
     cudaStream_t stream = nullptr;
-    c10::optional<c10::Stream> other;                  // the caller's, for the allocator
+    c10::optional<c10::Stream> other, ambient;         // the caller's, and then the current one, for the allocator
 
     bool begin(PyObject* first, const char* name, PyObject* stream_) {
         const at::Tensor* t;
@@ -100,13 +101,19 @@ struct Call {
             return refuse("stream is on cuda:" + std::to_string(v[2]) + ", " + name + " on cuda:" + std::to_string(dev));
         stream = reinterpret_cast<cudaStream_t>(v[0]);
         other = c10::Stream::unpack3(v[1], static_cast<c10::DeviceIndex>(v[2]), static_cast<c10::DeviceType>(v[3]));
+        ambient = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).unwrap();
         return true;
     }
 
-    // A tensor that the call allocates; on a stream other than the current one the allocator is told.
-    at::Tensor make(at::IntArrayRef shape, at::ScalarType type) const {
-        at::Tensor t = at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)), c10::nullopt);
-        if (other) t.record_stream(*other);
+    // A tensor that the call allocates, from the pool of the stream that it runs on: a block of the current stream's
+    // pool may still be in use by kernels pending there, which another stream does not wait for.  A result that the
+    // current stream uses too is kept, once freed, until that stream has passed.
+    at::Tensor make(at::IntArrayRef shape, at::ScalarType type, bool result = true) const {
+        const at::Device device(at::kCUDA, static_cast<c10::DeviceIndex>(dev));
+        if (!other) return at::detail::empty_cuda(shape, type, device, c10::nullopt);
+        const c10::cuda::CUDAStreamGuard guard(*other);
+        at::Tensor t = at::detail::empty_cuda(shape, type, device, c10::nullopt);
+        if (result) t.record_stream(*ambient);
         return t;
     }
 
@@ -131,7 +138,7 @@ struct Call {
     // The caller's workspace, or (None) one of `bytes` bytes for this call, kept alive by `own`.
     bool workspace(PyObject* o, size_t bytes, at::Tensor& own, void** out, size_t* have) const {
         if (o == Py_None) {
-            own = make({static_cast<int64_t>(bytes)}, at::kByte);
+            own = make({static_cast<int64_t>(bytes)}, at::kByte, false);
             *out = own.data_ptr();
             *have = bytes;
             return true;
