@@ -407,7 +407,8 @@ int moe_linear_workspace_size(const moe_linear_config_t *cfg, size_t *bytes);
  *   y              device bf16 [T, N]; out
  *   workspace      device, 256-byte aligned; not shared by calls in flight at the same time
  * Alignment: x, codes, scales, bias, residual, y 16 bytes.  A row's bits depend on num_tokens only
- * through the kernel it selects. */
+ * through the kernel it selects.  Where a bounded wait runs out (MOE_ERR_TIMEOUT in the workspace's
+ * status word), every value of y that was not computed is NaN. */
 int moe_linear(const moe_linear_config_t *cfg, const void *x, const void *codes, const void *scales, const void *w_t,
                const void *ws_t, const void *bias, const void *residual, void *y, void *workspace,
                size_t workspace_bytes, void *stream);
@@ -477,10 +478,11 @@ int moe_selftest_bounded_wait(int32_t *status, uint32_t timeout_us, void *stream
 
 /* Fault injection for failure-detection tests (no counterpart on the pages).  Only the debug
  * library, libmoefp8_debug.so (built with MOE_FAULT_INJECTION), acts on it; the release library
- * returns MOE_ERR_UNSUPPORTED.  MOE_FAULT_SKIP_STAGE arms one fault for the next moe_forward on
- * this host thread: the gate+up GEMM's producer in CTA 0 skips its first K stage (no copies, no
- * arrival), so the MMA role's bounded wait runs out (about 2 s), every role of that CTA leaves
- * cleanly and the status word reads MOE_ERR_TIMEOUT.  Nothing faults or hangs; the context stays
+ * returns MOE_ERR_UNSUPPORTED.  MOE_FAULT_SKIP_STAGE arms one fault for the next moe_forward or
+ * moe_linear on this host thread: the producer in CTA 0 (of the gate+up GEMM; of the product, where
+ * the kernel for few tokens does so in the first CTA of every cluster) skips its first K stage (no
+ * copies, no arrival), so the MMA role's bounded wait runs out (about 2 s), every role of that CTA
+ * leaves cleanly and the status word reads MOE_ERR_TIMEOUT.  Nothing faults or hangs; the context stays
  * usable.  MOE_FAULT_NONE disarms it. */
 #define MOE_FAULT_NONE 0
 #define MOE_FAULT_SKIP_STAGE 1

@@ -452,7 +452,7 @@ def selftest_bounded_wait(status_tensor, timeout_us: int, stream=None) -> None:
 
 
 def debug_inject_fault(fault: int) -> None:
-    """Arm a fault for the next forward on this thread (the debug library only; the release
+    """Arm a fault for the next forward or linear on this thread (the debug library only; the release
     library raises MoeError with MOE_ERR_UNSUPPORTED)."""
     _check(_load().moe_debug_inject_fault(int(fault)))
 
@@ -551,7 +551,8 @@ def new_linear_workspace(cfg: LinearConfig, device="cuda"):
 def linear(cfg: LinearConfig, weights, x=None, quantized=None, bias=None, residual=None, y=None, workspace=None,
            stream=None):
     """y = act(x W + bias) + residual, bf16 [T, N].  Exactly one of x (bf16 [T, K], quantized by the call) and
-    quantized (codes and scale words, as add_rms_norm returns them); weights from transform_linear_weights."""
+    quantized (codes and scale words, as add_rms_norm returns them); weights from transform_linear_weights.
+    read_status on a workspace of the caller's tells whether a wait ran out (what was not computed is NaN then)."""
     return (_bound or _bind()).linear(cfg, weights, x, quantized, bias, residual, y, workspace, stream)
 
 

@@ -50,6 +50,7 @@ struct LinearArgs {
     __nv_bfloat16* y;           // [T, N]
     int32_t* status;
     int clear;                  // the kernel clears the status word (it is the call's first)
+    int fault;                  // MOE_FAULT_* (acted on only in a MOE_FAULT_INJECTION build)
 };
 
 // Output columns are padded to this in the transformed scales.

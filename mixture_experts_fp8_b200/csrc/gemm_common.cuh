@@ -9,12 +9,12 @@ namespace moe {
 constexpr unsigned long long kDrainLimitNs = 100000000ull;
 
 // Bounded wait used only while leaving after an abort: ignores the abort flag.
-__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, unsigned long long limit = kDrainLimitNs) {
     const uint32_t a = smem_u32(bar);
     const unsigned long long t0 = globaltimer_ns();
     while (!mbar_try_wait(a, parity)) {
         __nanosleep(128);
-        if (globaltimer_ns() - t0 > kDrainLimitNs) break;
+        if (globaltimer_ns() - t0 > limit) break;
     }
 }
 

@@ -58,7 +58,8 @@ struct L {
     // full[stages], empty[stages], tempty[2], tfull[kSteps], drain
     static constexpr uint32_t nbars = 2 * stages + kSteps + 3;
     static constexpr uint32_t misc = bars + nbars * 8;    // tmem holder, abort flag
-    static constexpr uint32_t end = misc + 16;
+    static constexpr uint32_t owed = misc + 16;           // units that the epilogue warps gave up on
+    static constexpr uint32_t end = owed + kEpiWarps * 4;
     static constexpr uint32_t smem = end + 1024;          // + slack to align the base to 1024 bytes
     static_assert((bars + 16 * stages) % 16 == 0, "the two tempty barriers are one bit apart");
     static_assert(stage % 1024 == 0 && out % 512 == 0 && slot % 16 == 0, "alignment");
@@ -147,6 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* drain = tfull + kSteps;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + S::misc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::misc + 4);
+    int* owed = reinterpret_cast<int*>(smem + S::owed);
 
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -163,6 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tmap(&tmB);
         if (p.N % 8 == 0) prefetch_tmap(&tmY);
     }
+    if (threadIdx.x < kEpiWarps) owed[threadIdx.x] = INT32_MAX;
     if (warp == 1) tmem_alloc2(tmem_holder, kTmemCols);
     tc_fence_before();
     __syncthreads();
@@ -189,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     }
                     const uint32_t bar = pair_addr(smem_u32(&full[s]), 0);
-                    if (elect_one()) {
+                    if (!fault_skip_stage(p.fault, it) && elect_one()) {   // debug builds: an injected fault
                         if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * S::stage);
 #pragma unroll
                         for (int b = 0; b < RB; ++b)
@@ -203,12 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            // after an abort: the copies already issued land (the even CTA's barriers count both CTAs')
-            // before either CTA passes the cluster barrier below
-            if (!ok && rank == 0) {
-                const uint32_t n = it < static_cast<uint32_t>(kStages) ? it : kStages;
-                for (uint32_t i = it - n; i < it; ++i) drain_wait(&full[i % kStages], (i / kStages) & 1);
-            }
+            pair_copies_land<kStages>(ok, full, empty, it, s, ph, rank, abort_flag, p.status);
         } else if (warp == 2) {
             // -------------------------------------------------------------- scales
             // Step g's scales go to slot g % kSteps and count on that slot's barrier.  The slot was last
@@ -251,10 +249,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                 }
             }
-            if (!ok) {   // let the copies already issued land: their steps' barriers may never complete
-                const unsigned long long t0 = globaltimer_ns();
-                while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
-            }
+            // the last steps' copies land; after an abort their steps' barriers may never complete
+            for (uint32_t g = it < kAhead ? 0 : it - kAhead; g < it && ok; ++g)
+                ok = mbar_wait<kProducerSleepNs>(&tfull[g % kSteps], (g / kSteps) & 1, abort_flag, p.status);
+            if (!ok) pause_for_copies();
         } else if (warp == 1 && rank == 0) {
             // -------------------------------------------------------------- MMA issuer, for the pair
             const uint32_t idesc = f8_idesc(kPairM, kN);
@@ -318,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t t_at = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(32 * qtr);
         uint32_t te_at = pair_addr(smem_u32(tempty), 0);
         bool ok = true;
-        for (int u = pair; u < total_units && ok; u += pairs) {
+        for (int u = pair; u < total_units; u += pairs) {
             const int nb = u / mt, mb = u - nb * mt;
             at.t0 = mb * kM + static_cast<int>(rank) * kTileM + quad * 32;
             at.tile_c0 = nb * kN;
@@ -378,7 +376,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 te_at ^= 8;
             }
             ok = epilogue_residual_wait(p, at, ok);
-            if (!ok) break;
+            if (!ok) {
+                if (lane == 0) owed[warp - kFirstEpiWarp] = u;
+                break;
+            }
             epilogue_sub<kSubCols0>(p, at, last, reinterpret_cast<float*>(acc2[0]));
             epilogue_store<kSubCols0>(p, &tmY, at);
             if constexpr (RB == 2) {                   // the second row block through the same subtile
@@ -402,6 +403,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc2(tmem_base, kTmemCols);
     }
+    if (warp >= kFirstEpiWarp && owed[warp - kFirstEpiWarp] < total_units)
+        epilogue_owed<kSubCols0, kM, kN>(p, owed[warp - kFirstEpiWarp], warp - kFirstEpiWarp, rank);
 }
 
 template <int RB>

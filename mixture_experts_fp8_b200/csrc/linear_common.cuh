@@ -313,6 +313,52 @@ __device__ __forceinline__ void arrive_pair(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// After an abort, for copies whose barriers may never complete: long enough for any that is under way.
+__device__ __forceinline__ void pause_for_copies() {
+    const unsigned long long t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+}
+// The end of a pair kernel's producer warp (it: stages issued; s, ph: the next one's place and parity): no copy is
+// under way when the CTA leaves, whichever role gave up.  The MMAs have read the last stages, or else the even CTA's
+// barriers, which count both CTAs' copies, complete.
+template <int STAGES>
+__device__ __forceinline__ void pair_copies_land(bool ok, uint64_t* full, uint64_t* empty, uint32_t it, uint32_t s, uint32_t ph,
+                                                 uint32_t rank, volatile int* abort, int32_t* status) {
+    for (int i = 0; i < STAGES && ok; ++i) {
+        ok = mbar_wait<kProducerSleepNs>(&empty[s], ph, abort, status);
+        if (++s == STAGES) {
+            s = 0;
+            ph ^= 1;
+        }
+    }
+    if (ok) return;
+    if (rank == 0)
+        for (uint32_t i = it < STAGES ? 0 : it - STAGES; i < it; ++i) drain_wait(&full[i % STAGES], (i / STAGES) & 1);
+    pause_for_copies();
+}
+
+// Where an epilogue warp's waits ran out it leaves the unit in shared memory (owed[warp]; no unit at first), and at the
+// kernel's end, where this takes no registers from the loop, writes NaN to its columns of that unit and of those that
+// its pair owes after it: ROWS x N0 values a unit, the lane's rows one by one.
+template <int C, int ROWS, int N0>
+__device__ __forceinline__ void epilogue_owed(const LinearArgs& p, int u, int epi_warp, uint32_t rank) {
+    const int mt = (p.T + ROWS - 1) / ROWS, total = mt * ((p.N + N0 - 1) / N0);
+    const int quad = epi_warp & 3, qtr = epi_warp >> 2;
+#pragma unroll 1
+    for (; u < total; u += gridDim.x >> 1) {
+        const int nb = u / mt, mb = u - nb * mt;
+#pragma unroll 1
+        for (int t = mb * ROWS + static_cast<int>(rank) * kTileM + quad * 32 + static_cast<int>(threadIdx.x & 31);
+             t < min(p.T, (mb + 1) * ROWS); t += 2 * kTileM) {
+            uint16_t* row = reinterpret_cast<uint16_t*>(p.y) + static_cast<size_t>(t) * p.N;
+#pragma unroll 1
+            for (int c0 = nb * N0 + C * qtr; c0 < (nb + 1) * N0; c0 += 4 * C)
+#pragma unroll 1
+                for (int c = c0; c < min(p.N, c0 + C); ++c) row[c] = 0x7fc0;
+        }
+    }
+}
+
 // Tiles of the pair kernels: 256 tokens, or two such blocks, x 128 columns (fp32 scales); 256 tokens x 192 or
 // 256 columns (block-scaled).
 constexpr int kPairM = 2 * kTileM;

@@ -51,7 +51,8 @@ struct XL {
     static constexpr uint32_t bars = sf + stages * kXSfStage;
     static constexpr uint32_t nbars = 3 * stages + 5;     // full, sfready, empty, tfull[2], tempty[2], drain
     static constexpr uint32_t misc = bars + nbars * 8;
-    static constexpr uint32_t end = misc + 16;
+    static constexpr uint32_t owed = misc + 16;           // units that the epilogue warps gave up on
+    static constexpr uint32_t end = owed + kXEpiWarps * 4;
     static constexpr uint32_t smem = end + 1024;
     static_assert(sf_col0 + stages * 12 <= kXTmemCols, "TMEM");
     static_assert(stage % 1024 == 0 && kXA % 1024 == 0 && out % 1024 == 0, "alignment");
@@ -96,6 +97,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     uint64_t* drain = tempty + 2;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + X::misc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + X::misc + 4);
+    int* owed = reinterpret_cast<int*>(smem + X::owed);
 
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -116,6 +118,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         prefetch_tmap(&tmSf);
         if (p.N % 8 == 0) prefetch_tmap(&tmY);
     }
+    if (threadIdx.x < kXEpiWarps) owed[threadIdx.x] = INT32_MAX;
     if (warp == 1) tmem_alloc2(tmem_holder, kXTmemCols);
     tc_fence_before();
     __syncthreads();
@@ -141,7 +144,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 }
                 uint8_t* st = smem + s * X::stage;
                 const uint32_t bar = pair_addr(smem_u32(&full[s]), 0);
-                if (elect_one()) {
+                if (!fault_skip_stage(p.fault, it) && elect_one()) {   // debug builds: an injected fault
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (kXA + b_bytes + 2 * kXSf));
                     tma_load_2d_pair(st, &tmA, kb * kTileK, row0, bar);
                     tma_load_2d_pair(st + X::b, &tmB, kb * kTileK, brow0, bar);
@@ -154,12 +157,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
                 }
             }
         }
-        // after an abort: the copies already issued land (the even CTA's barriers count both CTAs') before
-        // either CTA passes the cluster barrier below
-        if (!ok && rank == 0) {
-            const uint32_t n = it < static_cast<uint32_t>(kXStages) ? it : kXStages;
-            for (uint32_t i = it - n; i < it; ++i) drain_wait(&full[i % kXStages], (i / kXStages) & 1);
-        }
+        pair_copies_land<kXStages>(ok, full, empty, it, s, ph, rank, abort_flag, p.status);
     } else if (warp == 2) {
         // ---------------------------------------------------------------------- token-scale atoms
         // lane i writes the atom's row i: the scale words of tile rows i, 32+i, 64+i, 96+i (rows past T:
@@ -276,7 +274,10 @@ __global__ void __launch_bounds__(kXThreads, 1)
             epilogue_store_wait();                 // the last tile's stores have read the subtile
             epilogue_residual<C>(p, at, last);
             const bool ok = mbar_wait(&tfull[b], (tile / X::accs) & 1, abort_flag, p.status);
-            if (!epilogue_residual_wait(p, at, ok)) break;
+            if (!epilogue_residual_wait(p, at, ok)) {
+                if (lane == 0) owed[warp - 4] = u;
+                break;
+            }
             tc_fence_after();
             const uint32_t from = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(b * kXN + C * qtr);
             float acc[X::parts][C];
@@ -329,6 +330,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         tc_fence_after();
         tmem_dealloc2(tmem_base, kXTmemCols);
     }
+    if (warp >= 4 && owed[warp - 4] < total_units) epilogue_owed<C, kXM, kXN>(p, owed[warp - 4], warp - 4, rank);
 }
 
 cudaError_t launch_linear_mx(const LinearArgs& a, const LinearMaps& m, int num_sms, cudaStream_t s) {

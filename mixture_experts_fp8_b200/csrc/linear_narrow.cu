@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(kSThreads, 2)
     float acc[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[j] = 0.0f;
+    bool gave_up = false;                              // this role, on a wait that ran out
 
     if (warp == 0) {
         // ---------------------------------------------------------------------- TMA producer
@@ -150,7 +151,7 @@ __global__ void __launch_bounds__(kSThreads, 2)
                 break;
             }
             uint8_t* st = smem + s * S::stage;
-            if (elect_one()) {
+            if (!fault_skip_stage(p.fault, it) && elect_one()) {   // debug builds: an injected fault
                 mbar_arrive_expect_tx(&full[s], a_bytes + S::bytes_b + kSSf + (MX ? 0 : NT * 4));
                 tma_load_2d(st, &tmW, kb * kTileK, n0, &full[s]);
                 tma_load_2d(st + S::b, &tmT, kb * kTileK, t0, &full[s]);
@@ -170,9 +171,17 @@ __global__ void __launch_bounds__(kSThreads, 2)
                 ph ^= 1;
             }
         }
-        if (!ok) {   // let the copies already issued land before the CTA leaves
-            for (int i = it > ST ? it - ST : 0; i < it; ++i) drain_wait(&full[i % ST], (i / ST) & 1);
+        // the copies already issued land before their space is used again: the MMAs have read them, or after an abort
+        for (int i = 0; i < ST && ok; ++i) {
+            ok = mbar_wait(&empty[s], ph, abort_flag, p.status);
+            if (++s == ST) {
+                s = 0;
+                ph ^= 1;
+            }
         }
+        if (!ok)
+            for (int i = it > ST ? it - ST : 0; i < it; ++i) drain_wait(&full[i % ST], (i / ST) & 1);
+        gave_up = !ok;
     } else if (warp == 2) {
         if (MX) {
             // -------------------------------------------------------------------- token-scale atoms
@@ -308,7 +317,8 @@ __global__ void __launch_bounds__(kSThreads, 2)
                 }
             }
         }
-        if (!__all_sync(0xffffffffu, ok)) {
+        gave_up = !__all_sync(0xffffffffu, ok);
+        if (gave_up) {
 #pragma unroll
             for (int j = 0; j < NT; ++j) acc[j] = __int_as_float(0x7fc00000);   // a wait ran out: NaN
         }
@@ -343,7 +353,15 @@ __global__ void __launch_bounds__(kSThreads, 2)
             for (int j = 0; j < NT; ++j) own[j * 128] = acc[j];
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        __syncthreads();
+        if (__syncthreads_or(gave_up)) {               // a copy that came late may have landed on them
+            if (warp >= 4) {
+                float* own = reinterpret_cast<float*>(smem) + row;
+#pragma unroll 1
+                for (int j = 0; j < NT; ++j) own[j * 128] = __int_as_float(0x7fc00000);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+            __syncthreads();
+        }
         cluster_wait();                                // every CTA of the cluster has set its barrier up
         if (warp == 4 && lane < split && t0 + lane * per < p.T) {   // lane r sends rank r its tokens
             const uint32_t bytes = static_cast<uint32_t>(per * 512);
@@ -353,7 +371,11 @@ __global__ void __launch_bounds__(kSThreads, 2)
         }
         __syncwarp();
         bool have = true;
-        if (t0 + rank * per < p.T) have = mbar_wait(xbar, 0, abort_flag, p.status);
+        if (t0 + rank * per < p.T) {
+            have = mbar_wait(xbar, 0, abort_flag, p.status);
+            // the others send theirs all the same, at their own waits' limits: no copy is under way when a CTA leaves
+            if (!have) drain_wait(xbar, 0, 2 * kWaitLimitNs);
+        }
         __syncwarp();
         cluster_arrive();                              // this CTA holds its shares: its senders may leave
         const float* mine = reinterpret_cast<const float*>(smem + S::part) + c2;

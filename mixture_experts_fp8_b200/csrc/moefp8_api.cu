@@ -868,6 +868,7 @@ int moe_linear(const moe_linear_config_t* cfg, const void* x, const void* codes,
     a.y = static_cast<__nv_bfloat16*>(y);
     a.status = static_cast<int32_t*>(workspace);
     a.clear = x == nullptr;
+    a.fault = take_armed_fault();
     moe::LinearMaps m{};
     const moe::LinearBoxes box = moe::linear_boxes(a, di.sms);
     if ((rc = make_kmajor_map(&m.x, x ? ws + q_at : codes, T, K, box.x))) return rc;
