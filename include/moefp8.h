@@ -399,7 +399,8 @@ int moe_transform_linear_weights(const moe_linear_config_t *cfg, const void *w, 
 #define MOE_LINEAR_STATUS_BYTES 1024
 int moe_linear_workspace_size(const moe_linear_config_t *cfg, size_t *bytes);
 
-/*   x              device bf16 [T, K], quantized by the call (two launches), or NULL
+/*   x              device bf16 [T, K], quantized by the call (two launches), or NULL; a row with
+ *                  an infinity or NaN has no finite y
  *   codes, scales  device, quantized rows [T, K] (one launch), or NULL; exactly one of x and codes
  *   w_t, ws_t      device, from moe_transform_linear_weights
  *   bias           device bf16 [N] or NULL

@@ -87,12 +87,14 @@ __device__ __forceinline__ uint2 quant_fp32(const float* v, float amax, float& s
 
 // UE8M0 scales: four lanes hold a 32-column group.  Returns the codes; word = the four scale bytes
 // of the lane's 128-column block, lowest group in the lowest byte (equal in its sixteen lanes).
+// An infinity, which the conversion would make 448, is multiplied by zero: its code is NaN, as with an
+// fp32 scale, and the finite columns of its group are zero.
 __device__ __forceinline__ uint2 quant_mx(const float* v, uint32_t& word) {
     float m = absmax8(v);
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
     const int e = mx_exponent(m);
-    const float inv = exp2_int(-e);
+    const float inv = m < INFINITY ? exp2_int(-e) : 0.0f;
     float q[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) q[i] = v[i] * inv;
