@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // the last steps' copies land; after an abort their steps' barriers may never complete
             for (uint32_t g = it < kAhead ? 0 : it - kAhead; g < it && ok; ++g)
-                ok = mbar_wait<kProducerSleepNs>(&tfull[g % kSteps], (g / kSteps) & 1, abort_flag, p.status);
+                ok = mbar_wait(&tfull[g % kSteps], (g / kSteps) & 1, abort_flag, p.status);
             if (!ok) pause_for_copies();
         } else if (warp == 1 && rank == 0) {
             // -------------------------------------------------------------- MMA issuer, for the pair

@@ -324,8 +324,9 @@ __device__ __forceinline__ void pause_for_copies() {
 template <int STAGES>
 __device__ __forceinline__ void pair_copies_land(bool ok, uint64_t* full, uint64_t* empty, uint32_t it, uint32_t s, uint32_t ph,
                                                  uint32_t rank, volatile int* abort, int32_t* status) {
+    if (it == 0 && ok) return;
     for (int i = 0; i < STAGES && ok; ++i) {
-        ok = mbar_wait<kProducerSleepNs>(&empty[s], ph, abort, status);
+        ok = mbar_wait(&empty[s], ph, abort, status);   // no sleep: the kernel may end with this
         if (++s == STAGES) {
             s = 0;
             ph ^= 1;
