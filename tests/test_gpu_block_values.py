@@ -1,10 +1,12 @@
 """Values at the ends of the operators around the layer: infinities through the quantizers, activations far in
 their tails, gradients that are not a row's."""
+import math
+
 import pytest
 import torch
 
 import mixture_experts_fp8_b200 as moe
-from _block_ref import dequantize, random_weights
+from _block_ref import F64, HALF, U, dequantize, random_weights
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +40,36 @@ def test_a_norm_that_overflows(recipe):
     v = dequantize(q[0], q[1], recipe)
     assert torch.isinf(y[2, 200]) and not torch.isfinite(v[2, 200])
     assert torch.isfinite(v[2, :128]).all() and torch.isfinite(v[2, 256:]).all()
+
+
+@pytest.mark.parametrize("T", [3, 300])
+@pytest.mark.parametrize("a", range(5))
+def test_activations_in_their_tails(T, a):
+    """The sums are zero, so that the activation's argument is the bias; relative to each value."""
+    K, N = 128, 1280
+    v = torch.linspace(-9.5, 9.5, N).bfloat16()
+    lin = moe.LinearConfig(T, K, N, 0, a)
+    w = moe.transform_linear_weights(lin, torch.zeros((K, N), dtype=torch.uint8, device="cuda"), torch.ones((1, N), device="cuda"))
+    y = moe.linear(lin, w, x=torch.zeros((T, K), dtype=torch.bfloat16, device="cuda"), bias=v.cuda()).cpu().to(F64)
+    d = v.to(F64)
+    u2 = 2 * math.sqrt(2 / math.pi) * (d + 0.044715 * d ** 3)
+    want = (d, d.clamp(min=0), d / (1 + torch.exp(-d)), 0.5 * d * torch.special.erfc(-d / math.sqrt(2)), d / (1 + torch.exp(-u2)))[a]
+    # fp32 roundings before the last one: an argument's relative error of up to 8 is worth that times the argument in an
+    # exponential, and times 2 x^2 + 1, x = v / sqrt 2, in erfc; 32 for the functions' own and the products
+    arg = (d * 0, d * 0, d.abs(), d ** 2 + 1, u2.abs())[a]
+    assert torch.all((y - want).abs() <= want.abs() * (HALF[torch.bfloat16] + (8 * arg + 32) * U))
+
+
+@pytest.mark.parametrize("T", [3, 300])
+@pytest.mark.parametrize("a", range(5))
+def test_activations_of_nan_and_infinity(T, a):
+    K, N = 128, 128
+    v = torch.zeros(N)
+    v[5], v[70], v[71], v[72] = float("nan"), float("inf"), 1e30, -1e30
+    lin = moe.LinearConfig(T, K, N, 1, a)
+    w = moe.transform_linear_weights(lin, torch.zeros((K, N), dtype=torch.uint8, device="cuda"),
+                                     torch.full((K // 32, N), 127, dtype=torch.uint8, device="cuda"))
+    v = v.bfloat16()
+    y = moe.linear(lin, w, x=torch.zeros((T, K), dtype=torch.bfloat16, device="cuda"), bias=v.cuda())
+    assert torch.isnan(y[:, 5]).all() and torch.all(y[:, 70] == float("inf")) and torch.all(y[:, 71] == v[71].item())
+    assert torch.all(y[:, 72] == (v[72].item() if a == 0 else 0)) and torch.all(y[:, 73:] == 0)
