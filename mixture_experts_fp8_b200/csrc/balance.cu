@@ -564,17 +564,17 @@ __global__ void __launch_bounds__(kRWarps * 32, NE <= 8 ? 4 : 2) k_route_backwar
         }
         // dp: the balance loss's, and for kDirect the slots' too
         const bool through = bal || (MODE == kDirect && wts);
-        const float on = bal ? 1.0f : 0.0f;
+        auto dp = [&](int i) { return MODE == kDirect ? (bal ? g[i] + x[i] : x[i]) : g[i]; };
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
-            const float d = MODE == kDirect ? fmaf(on, g[i], x[i]) : on * g[i];
+            const float d = dp(i);
             dot = fmaf(p[i], d, dot);
         }
         dot = group_sum<G>(dot) * rz;
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
-            const float d = MODE == kDirect ? fmaf(on, g[i], x[i]) : on * g[i];
-            // a token takes no part of a gradient that it does not have (its row may hold NaN)
+            const float d = dp(i);
+            // a token takes no part of a gradient that it does not have (its row or that gradient may hold NaN)
             if (MODE == kSigmoid) p[i] = slope[i] * ((through ? (d - dot) * rz : 0.0f) + x[i]);
             else p[i] = (MODE == kDirect ? 0.0f : x[i]) + (through ? p[i] * rz * (d - dot) : 0.0f);
             if (MODE == kSigmoid && !bal && !wts) p[i] = 0.0f;

@@ -73,3 +73,28 @@ def test_activations_of_nan_and_infinity(T, a):
     y = moe.linear(lin, w, x=torch.zeros((T, K), dtype=torch.bfloat16, device="cuda"), bias=v.cuda())
     assert torch.isnan(y[:, 5]).all() and torch.all(y[:, 70] == float("inf")) and torch.all(y[:, 71] == v[71].item())
     assert torch.all(y[:, 72] == (v[72].item() if a == 0 else 0)) and torch.all(y[:, 73:] == 0)
+
+
+MODES = [(0, 0), (0, 1), (1, 0)]                          # routing, renormalize
+
+
+@pytest.mark.parametrize("T,E,k", [(75, 16, 4), (60000, 16, 4), (15000, 130, 20)])   # a token a lane group, and several
+@pytest.mark.parametrize("routing,renorm", MODES)
+def test_tokens_outside_the_loss_take_no_part_of_its_gradient(T, E, k, routing, renorm):
+    """A loss whose gradient overflowed: masked tokens, and those of no sequence, keep the gradient of their weights."""
+    g = torch.Generator().manual_seed(4)
+    l = torch.randn((T, E), generator=g).cuda()
+    idx = torch.topk(l, k)[1].int()
+    dw = torch.randn((T, k), generator=g).cuda()
+    mask = torch.rand(T, generator=g).cuda() < 0.5
+    off = torch.tensor([3, T // 2, T - 5], dtype=torch.int32, device="cuda")
+    cfg = moe.Config(T, 128, 128, E, k, routing=routing, renormalize=renorm)
+    _, counts, tokens, _ = moe.balance_loss(cfg, l, idx, 0.1, seq_offsets=off, token_mask=mask)
+    alone, _ = moe.route_backward(cfg, l, idx, d_topk_weights=dw)
+    outside = ~mask
+    outside[:3] = outside[T - 5:] = True
+    for d in (float("inf"), float("nan"), 1e38):
+        both, _ = moe.route_backward(cfg, l, idx, d_topk_weights=dw, d_loss=torch.full((1,), d, device="cuda"), coef=1e3,
+                                     expert_counts=counts, seq_tokens=tokens, seq_offsets=off, token_mask=mask)
+        assert torch.equal(both[outside], alone[outside])
+        assert not torch.isfinite(both[~outside]).all(1).any() or d == 1e38
