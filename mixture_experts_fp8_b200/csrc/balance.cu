@@ -482,9 +482,12 @@ __global__ void __launch_bounds__(kRWarps * 32, NE <= 8 ? 4 : 2) k_route_backwar
         }
         bal = bal && t >= q0 && t < q1;
         const float scale0 = e0 >= 0 && a.pes ? __ldg(a.pes + e0) : 1.0f;
-        bool nz = x0 != 0.0f;                          // NaN counts
+        bool nz = e0 >= 0 && x0 != 0.0f;               // NaN counts; a slot without an expert does not
         if (in && a.dw)
-            for (int j = gl + G; j < a.K; j += G) nz |= __ldg(dw + j) != 0.0f;
+            for (int j = gl + G; j < a.K; j += G) {
+                const int e = __ldg(idx + j);
+                nz |= e >= 0 && e < a.E && __ldg(dw + j) != 0.0f;
+            }
         const bool wts = __ballot_sync(0xffffffffu, nz) & group_mask;
         float z = 0.0f, m = -INFINITY;
         if (MODE == kSigmoid) {

@@ -98,3 +98,30 @@ def test_tokens_outside_the_loss_take_no_part_of_its_gradient(T, E, k, routing, 
                                      expert_counts=counts, seq_tokens=tokens, seq_offsets=off, token_mask=mask)
         assert torch.equal(both[outside], alone[outside])
         assert not torch.isfinite(both[~outside]).all(1).any() or d == 1e38
+
+
+@pytest.mark.parametrize("E,k", [(16, 4), (130, 20)])
+@pytest.mark.parametrize("routing,renorm", MODES)
+def test_slots_without_an_expert(E, k, routing, renorm):
+    """A padded row (ids of -1 or past E; logits and weights' gradients of anything) has a gradient of zero, and such a
+    slot among others adds nothing to its row or to the scales."""
+    T = 60
+    g = torch.Generator().manual_seed(5)
+    l = torch.randn((T, E), generator=g).cuda()
+    idx = torch.topk(l, k)[1].int()
+    dw, pes = torch.randn((T, k), generator=g).cuda(), torch.rand(E, generator=g).cuda()
+    pad, part = list(range(0, T, 7)), list(range(3, T, 7))
+    zeroed = dw.clone()
+    zeroed[pad] = 0
+    zeroed[part, k - 1] = 0
+    l[pad] = float("nan")
+    l[pad[0]] = float("inf")
+    idx[pad] = -1
+    idx[pad[1:3]] = E
+    idx[part, k - 1] = 1 << 30
+    dw[part, k - 1] = float("nan")
+    cfg = moe.Config(T, 128, 128, E, k, routing=routing, renormalize=renorm)
+    dl, dp = moe.route_backward(cfg, l, idx, d_topk_weights=dw, per_expert_scale=pes)
+    dl0, dp0 = moe.route_backward(cfg, l, idx, d_topk_weights=zeroed, per_expert_scale=pes)
+    assert torch.all(dl[pad] == 0) and torch.isfinite(dl).all() and torch.isfinite(dp).all()
+    assert torch.equal(dl, dl0) and torch.equal(dp, dp0)
