@@ -25,8 +25,6 @@ import os
 import threading
 from dataclasses import dataclass
 
-import torch
-
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmoefp8.so")
 
@@ -235,6 +233,7 @@ def _ptr(t):
 
 
 def _stream(stream):
+    import torch
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
@@ -242,6 +241,7 @@ def _stream(stream):
 
 def _raw_stream(stream, dev):
     """The stream's handle; the current stream of dev by default."""
+    import torch
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
 
 
@@ -260,6 +260,7 @@ def transformed_weights_size(cfg: Config):
 
 def transform_weights(cfg: Config, w13, w13_scale, w2, w2_scale, stream=None):
     """Device tensors in the pages' layout -> (w13_t, w13s_t, w2_t, w2s_t) uint8 device tensors."""
+    import torch
     sizes = transformed_weights_size(cfg)
     outs = [torch.empty(n, dtype=torch.uint8, device=w13.device) for n in sizes]
     c = cfg.c()
@@ -283,12 +284,14 @@ def workspace_layout(cfg: Config) -> dict:
 
 
 def new_workspace(cfg: Config, device="cuda"):
+    import torch
     return torch.empty(workspace_size(cfg), dtype=torch.uint8, device=device)
 
 
 def route(cfg: Config, router_logits, per_expert_scale=None, topk_idx=None, topk_weights=None,
           stream=None):
     """-> (topk_idx int32 [T,k], topk_weights fp32 [T,k]) on the logits' device."""
+    import torch
     T, k = cfg.num_tokens, cfg.top_k
     if topk_idx is None:
         topk_idx = torch.empty((T, k), dtype=torch.int32, device=router_logits.device)
@@ -310,6 +313,7 @@ def gate_weights_size(cfg: Config) -> int:
 def transform_gate_weights(cfg: Config, norm_weight, router_weight, stream=None):
     """norm_weight fp32 [H] and router_weight fp32 [E, H] (device) -> the gate's weights: a uint8
     device tensor holding w' = norm_weight * router_weight as three bf16 parts [3, E, H]."""
+    import torch
     out = torch.empty(gate_weights_size(cfg), dtype=torch.uint8, device=router_weight.device)
     c = cfg.c()
     _check(_load().moe_transform_gate_weights(ctypes.byref(c), _ptr(norm_weight), _ptr(router_weight), _ptr(out),
@@ -321,6 +325,7 @@ def gate(cfg: Config, hidden_states, gate_weights, rms_eps: float, per_expert_sc
          topk_idx=None, topk_weights=None, stream=None):
     """RMSNorm + router matmul + router top-k (gate_weights from transform_gate_weights).
     -> (logits fp32 [T, E], topk_idx int32 [T, k], topk_weights fp32 [T, k])."""
+    import torch
     T, E, k = cfg.num_tokens, cfg.num_experts, cfg.top_k
     dev = hidden_states.device
     if logits is None:
@@ -339,6 +344,7 @@ def gate(cfg: Config, hidden_states, gate_weights, rms_eps: float, per_expert_sc
 def ep_dispatch(cfg: Config, ranks: int, hidden_states, topk_idx, workspace, stream=None):
     """Order this rank's routed slots by destination rank (rank r owns experts r*E/R ..) ->
     (send_counts int32 [R], send_x bf16 [T*k, H], send_expert int32 [T*k], slot_pos int32 [T, k])."""
+    import torch
     T, H, k = cfg.num_tokens, cfg.hidden, cfg.top_k
     dev = hidden_states.device
     send_counts = torch.empty(ranks, dtype=torch.int32, device=dev)
@@ -356,6 +362,7 @@ def forward_rows(cfg: Config, rows, expert_of_row, weights, w13_bias=None, w2_bi
                  workspace=None, stream=None):
     """Each row through one local expert with weight 1 (cfg: num_tokens = rows, top_k = 1,
     num_experts = this rank's experts) -> o_rows fp32 [N, H]."""
+    import torch
     N, H = cfg.num_tokens, cfg.hidden
     if o_rows is None:
         o_rows = torch.empty((N, H), dtype=torch.float32, device=rows.device)
@@ -373,6 +380,7 @@ def combine_rows(cfg: Config, o_rows, slot_pos, topk_weights, y=None, status=Non
     """y[t] = bf16(sum_j w[t,j] * o_rows[slot_pos[t,j]]) in slot order -> y bf16 [T, H].  A slot
     whose position is outside o_rows adds nothing and sets `status` (device int32) to
     MOE_ERR_BOUNDS."""
+    import torch
     T, H = cfg.num_tokens, cfg.hidden
     if y is None:
         y = torch.empty((T, H), dtype=torch.bfloat16, device=slot_pos.device)
@@ -388,6 +396,7 @@ def forward(cfg: Config, hidden_states, weights, router_logits=None, per_expert_
             expert_counts=None, workspace=None, stream=None, profile: "Profile | None" = None):
     """The fused layer forward.  `weights` = (w13_t, w13s_t, w2_t, w2s_t) from
     transform_weights.  Returns y (bf16 [T, H])."""
+    import torch
     if y is None:
         y = torch.empty((cfg.num_tokens, cfg.hidden), dtype=torch.bfloat16, device=hidden_states.device)
     if workspace is None:
@@ -410,6 +419,7 @@ def forward_static_workspace(cfg: Config, hidden_states, weights, router_logits=
     """The layer forward with its scratch in the library's fixed device array (no workspace
     argument, nothing allocated by the library).  For callers that may not allocate device
     memory; `y` should be preallocated by such callers."""
+    import torch
     if y is None:
         y = torch.empty((cfg.num_tokens, cfg.hidden), dtype=torch.bfloat16, device=hidden_states.device)
     c = cfg.c()
@@ -430,6 +440,7 @@ def debug_unfused_gate_up(cfg: Config, hidden_states, topk_idx, weights, workspa
     """The gate+up step taken apart (test hook): the GEMM stores the fp32 gate/up sums h, then a
     separate SwiGLU + requantization kernel writes the act codes and scales into `workspace`.
     Returns h [A, 2I] fp32 (columns in the transformed order)."""
+    import torch
     A = cfg.num_tokens * (cfg.top_k + cfg.shared_experts)
     h = torch.empty((A, 2 * cfg.inter), dtype=torch.float32, device=hidden_states.device)
     c = cfg.c()
@@ -464,6 +475,7 @@ def _refuse(msg: str):
 
 def _device_of(t, name: str):
     """The device index of a call's first tensor, which has to be the current one (its stream and kernels)."""
+    import torch
     dev = t.get_device()
     if dev < 0 or dev != torch.cuda.current_device():
         _refuse(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
@@ -483,6 +495,7 @@ def _arg(t, name: str, shape, dtype, dev):
 def _new(like, shape, dtype, stream):
     """A tensor that the call allocates, from the pool of the stream that it runs on: a block of the current stream's
     pool may still be in use there.  Once freed it is kept until the current stream, too, has passed."""
+    import torch
     if stream is None:
         return like.new_empty(shape, dtype=dtype)
     current = torch.cuda.current_stream(like.device)
@@ -501,6 +514,7 @@ def quantized_size(rows: int, cols: int):
 
 def new_quantized(rows: int, cols: int, device="cuda"):
     """Buffers for quantized rows: (codes uint8 [rows, cols], scale words int32 [cols/128, scale_rows])."""
+    import torch
     scale_rows = quantized_size(rows, cols)[2]
     return (torch.empty((rows, cols), dtype=torch.uint8, device=device),
             torch.empty((cols // 128, scale_rows), dtype=torch.int32, device=device))
@@ -525,6 +539,7 @@ def transformed_linear_size(cfg: LinearConfig):
 def transform_linear_weights(cfg: LinearConfig, w, w_scale, stream=None):
     """w [K, N] codes (recipe 2: [K, N/2] bytes of pairs) and w_scale (fp32 [K/128, N], or UE8M0 bytes
     [K/32, N]) -> (w_t, ws_t) uint8 device tensors, for any num_tokens."""
+    import torch
     dev = _device_of(w, "w")
     K, N, g = cfg.in_features, cfg.out_features, 128 if cfg.recipe == 0 else 32
     outs = [_new(w, n, torch.uint8, stream) for n in transformed_linear_size(cfg)]
@@ -545,6 +560,7 @@ def linear_workspace_size(cfg: LinearConfig) -> int:
 
 def new_linear_workspace(cfg: LinearConfig, device="cuda"):
     """A workspace for linear() on bf16 rows (quantized rows need its first MOE_LINEAR_STATUS_BYTES only)."""
+    import torch
     return torch.empty(linear_workspace_size(cfg), dtype=torch.uint8, device=device)
 
 
@@ -564,6 +580,7 @@ def balance_workspace_size(cfg: Config, num_seqs: int = 1) -> int:
 
 
 def new_balance_workspace(cfg: Config, num_seqs: int = 1, device="cuda"):
+    import torch
     return torch.empty(balance_workspace_size(cfg, num_seqs), dtype=torch.uint8, device=device)
 
 

@@ -10,13 +10,15 @@ driver API entry point used for TMA descriptors is fetched at run time, so the l
 link libcuda.
 
 csrc/binding.cpp, the Python module that marshals the operators around the layer, is compiled by the
-host compiler against PyTorch's headers into mixture_experts_fp8_b200/_binding.so.
+host compiler against PyTorch's headers into mixture_experts_fp8_b200/_binding.so.  Where PyTorch is not
+installed the libraries alone are built.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -112,9 +114,13 @@ def build_binding(force: bool = False) -> str:
     return BINDING
 
 
+def _bindings(force: bool) -> list:
+    return [build_binding(force)] if importlib.util.find_spec("torch") else []
+
+
 def build_all(force: bool = False, verbose: bool = False) -> list:
-    """The release library, the fault-injection debug library and the Python module."""
-    return [build(force, verbose), build(force, False, debug=True), build_binding(force)]
+    """The release library, the fault-injection debug library and (where PyTorch is) the Python module."""
+    return [build(force, verbose), build(force, False, debug=True), *_bindings(force)]
 
 
 if __name__ == "__main__":
@@ -124,4 +130,4 @@ if __name__ == "__main__":
     ap.add_argument("--debug", action="store_true", help="also build libmoefp8_debug.so")
     a = ap.parse_args()
     print(build_all(a.force, a.verbose) if a.debug else
-          [build(force=a.force, verbose=a.verbose), build_binding(a.force)])
+          [build(force=a.force, verbose=a.verbose), *_bindings(a.force)])
