@@ -209,10 +209,9 @@ def _bind():
     L = _load()
     with _lock:
         if _bound is None:
-            path = os.path.join(_PKG, "_binding.so")
-            if not os.path.exists(path):
-                from . import build as _build
-                _build.build_binding()
+            from . import build as _build
+            if not _build.binding_matches():
+                _build.build_binding(force=True)
             from . import _binding as m
             m.init(MoeError, *[ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
                 "moe_last_error", "moe_add_rms_norm", "moe_linear", "moe_linear_workspace_size", "moe_balance_loss",

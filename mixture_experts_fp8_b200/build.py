@@ -32,6 +32,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoefp8.so")
 BINDING = os.path.join(PKG, "_binding.so")
+BINDING_FOR = os.path.join(BUILD, "binding.for")   # the PyTorch and Python that it was built for
 # The debug library: the same sources with MOE_FAULT_INJECTION, for failure-detection tests.
 BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libmoefp8_debug.so")
@@ -92,13 +93,28 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     return lib
 
 
+def binding_matches() -> bool:
+    """Whether _binding.so is there and was built for this PyTorch and Python (its C++ interface differs by release)."""
+    try:
+        with open(BINDING_FOR) as f:
+            return os.path.exists(BINDING) and f.read() == _binding_for()
+    except OSError:
+        return False
+
+
+def _binding_for() -> str:
+    import torch
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}\n"
+
+
 def build_binding(force: bool = False) -> str:
     """Build _binding.so (host code only) and return its path."""
     src = os.path.join(CSRC, "binding.cpp")
     deps = [src, os.path.join(INCLUDE, "moefp8.h")]
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, deps)):
+    if not force and binding_matches() and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, deps)):
         return BINDING
     import torch
+    os.makedirs(BUILD, exist_ok=True)
     base = os.path.dirname(torch.__file__)
     includes = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
                 sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
@@ -111,6 +127,9 @@ def build_binding(force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed for {src}:\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(tmp, "w") as f:
+        f.write(_binding_for())
+    os.replace(tmp, BINDING_FOR)
     return BINDING
 
 

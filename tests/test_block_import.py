@@ -28,3 +28,21 @@ print(moe.workspace_size(cfg) > 0, moe.workspace_layout(cfg)["status"], moe.quan
 def test_build_of_the_library():
     out = run("import runpy; sys.argv = ['build']; runpy.run_module('mixture_experts_fp8_b200.build', run_name='__main__')")
     assert "libmoefp8.so" in out and "_binding" not in out
+
+
+def test_a_module_built_for_another_pytorch_is_built_again(monkeypatch, tmp_path):
+    import mixture_experts_fp8_b200 as moe
+    from mixture_experts_fp8_b200 import build
+    build.build_binding()
+    moe._bind()
+    assert build.binding_matches()
+    other = tmp_path / "binding.for"
+    monkeypatch.setattr(build, "BINDING_FOR", str(other))
+    assert not build.binding_matches()
+    other.write_text("torch 1.0.0, cpython-38\n")
+    assert not build.binding_matches()
+    called = []
+    monkeypatch.setattr(build, "build_binding", lambda force=False: called.append(force))
+    monkeypatch.setattr(moe, "_bound", None)
+    moe._bind()
+    assert called == [True]
