@@ -350,7 +350,9 @@ int moe_combine_rows(const moe_config_t *cfg, const float *o_rows, int32_t num_r
  * Quantized rows: E4M3 codes [rows, cols] and K-block-major scales, one 4-byte word per (128-column
  * block, row), [cols/128][scale_rows]: the fp32 scale (recipe 0), or the block's four UE8M0 bytes,
  * lowest 32 columns in the lowest byte (recipes 1, 2).  scale_rows is rows + 132 rounded up to 4;
- * words past `rows` are never written and never affect a result.
+ * words past `rows` are never written and never affect a result.  moe_linear reads them; moe_forward
+ * takes bf16 rows and quantizes them itself.  An fp32 scale is the block's largest magnitude times
+ * fl32(1/448), where moe_forward's own quantizer divides by 448: the two can differ by one ulp.
  *
  * moe_quantized_size: bytes of both buffers, and the row stride (host call; NULL outputs are skipped). */
 int moe_quantized_size(int32_t rows, int32_t cols, size_t *codes_bytes, size_t *scales_bytes, size_t *scale_rows);
@@ -368,7 +370,8 @@ int moe_quantized_size(int32_t rows, int32_t cols, size_t *codes_bytes, size_t *
  * At least one output.  residual_out may be the residual or (bf16) x buffer itself, and y the x
  * buffer or (bf16) the residual buffer; buffers may not overlap in any other way.  Every buffer
  * 16-byte aligned, an fp32 residual and its residual_out 32-byte.  One launch.  Inf or NaN in a row
- * makes y, or the values its codes stand for, non-finite in that row only. */
+ * makes y, or the values its codes stand for, non-finite in that row only.  The sum of squares is
+ * fp32: in a row where it passes 3.4e38 (values of 1e17 and more), finite values have a y of zero. */
 int moe_add_rms_norm(const moe_config_t *cfg, const void *x, const void *residual, int residual_fp32,
                      const float *norm_weight, float rms_eps, void *residual_out, void *y, void *codes,
                      void *scales, void *stream);
@@ -416,11 +419,14 @@ int moe_linear(const moe_linear_config_t *cfg, const void *x, const void *codes,
 
 /* The router's balance loss, from the logits and ids of moe_route or moe_gate.  Sequence s holds the
  * tokens seq_offsets[s] .. seq_offsets[s+1] - 1; a token counts when it lies in a sequence and its
- * token_mask is not zero (the logits and ids of other tokens are not read).  With n_s counted tokens,
+ * token_mask is not zero.  The logits and ids of other tokens are read too, and may hold anything: they
+ * never affect a result.  With n_s counted tokens,
  *   p[t, e] = softmax(logits[t])                              (routing 0)
  *           = sigmoid(logits[t, e]) / sum_j sigmoid(logits[t, j])   (routing 1)
  *   loss = coef / S' * sum_s sum_e  E / (k n_s) counts[s, e] * mean_t p[t, e],  S' sequences have n_s > 0
- * (0 when none has).  cfg: num_tokens, num_experts, top_k and routing are used.
+ * (0 when none has).  A row's scores are fp32: where every logit of a counted token is below about -87 its
+ * sigmoids are zero and its sequence's results NaN (as moe_route's weights are there).
+ * cfg: num_tokens, num_experts, top_k and routing are used.
  *   router_logits  device fp32 [T, E];  topk_idx  device int32 [T, k]
  *   token_mask     device uint8 [T] or NULL (every token counts)
  *   seq_offsets    device int32 [num_seqs + 1], ascending, in [0, T], or NULL: one sequence of all
