@@ -15,8 +15,8 @@ Entry points (same names as the C ABI):
 around the layer:
     add_rms_norm, transform_linear_weights, linear, balance_loss, route_backward.
 
-With `stream`, the operators around the layer allocate what they return from that stream's pool: the
-results are that stream's, and another stream waits for it before it reads them.
+With `stream`, a call allocates what it returns from that stream's pool: the results are that stream's,
+and another stream waits for it before it reads them.
 """
 from __future__ import annotations
 
@@ -244,6 +244,19 @@ def _raw_stream(stream, dev):
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
 
 
+def _new(shape, dtype, device, stream):
+    """A tensor that a call allocates, from the pool of the stream that it runs on: a block of the current stream's
+    pool may still be in use there.  Once freed it is kept until the current stream, too, has passed."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
+
+
 # --------------------------------------------------------------------------------------------
 def check_config(cfg: Config) -> None:
     c = cfg.c()
@@ -261,7 +274,7 @@ def transform_weights(cfg: Config, w13, w13_scale, w2, w2_scale, stream=None):
     """Device tensors in the pages' layout -> (w13_t, w13s_t, w2_t, w2s_t) uint8 device tensors."""
     import torch
     sizes = transformed_weights_size(cfg)
-    outs = [torch.empty(n, dtype=torch.uint8, device=w13.device) for n in sizes]
+    outs = [_new(n, torch.uint8, w13.device, stream) for n in sizes]
     c = cfg.c()
     _check(_load().moe_transform_weights(ctypes.byref(c), _ptr(w13), _ptr(w13_scale), _ptr(w2),
                                          _ptr(w2_scale), *[_ptr(o) for o in outs], _stream(stream)))
@@ -293,9 +306,9 @@ def route(cfg: Config, router_logits, per_expert_scale=None, topk_idx=None, topk
     import torch
     T, k = cfg.num_tokens, cfg.top_k
     if topk_idx is None:
-        topk_idx = torch.empty((T, k), dtype=torch.int32, device=router_logits.device)
+        topk_idx = _new((T, k), torch.int32, router_logits.device, stream)
     if topk_weights is None:
-        topk_weights = torch.empty((T, k), dtype=torch.float32, device=router_logits.device)
+        topk_weights = _new((T, k), torch.float32, router_logits.device, stream)
     c = cfg.c()
     _check(_load().moe_route(ctypes.byref(c), _ptr(router_logits), _ptr(per_expert_scale),
                              _ptr(topk_idx), _ptr(topk_weights), _stream(stream)))
@@ -313,7 +326,7 @@ def transform_gate_weights(cfg: Config, norm_weight, router_weight, stream=None)
     """norm_weight fp32 [H] and router_weight fp32 [E, H] (device) -> the gate's weights: a uint8
     device tensor holding w' = norm_weight * router_weight as three bf16 parts [3, E, H]."""
     import torch
-    out = torch.empty(gate_weights_size(cfg), dtype=torch.uint8, device=router_weight.device)
+    out = _new(gate_weights_size(cfg), torch.uint8, router_weight.device, stream)
     c = cfg.c()
     _check(_load().moe_transform_gate_weights(ctypes.byref(c), _ptr(norm_weight), _ptr(router_weight), _ptr(out),
                                               _stream(stream)))
@@ -328,11 +341,11 @@ def gate(cfg: Config, hidden_states, gate_weights, rms_eps: float, per_expert_sc
     T, E, k = cfg.num_tokens, cfg.num_experts, cfg.top_k
     dev = hidden_states.device
     if logits is None:
-        logits = torch.empty((T, E), dtype=torch.float32, device=dev)
+        logits = _new((T, E), torch.float32, dev, stream)
     if topk_idx is None:
-        topk_idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+        topk_idx = _new((T, k), torch.int32, dev, stream)
     if topk_weights is None:
-        topk_weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+        topk_weights = _new((T, k), torch.float32, dev, stream)
     c = cfg.c()
     _check(_load().moe_gate(ctypes.byref(c), _ptr(hidden_states), _ptr(gate_weights), ctypes.c_float(rms_eps),
                             _ptr(per_expert_scale), _ptr(logits), _ptr(topk_idx), _ptr(topk_weights),
@@ -346,10 +359,10 @@ def ep_dispatch(cfg: Config, ranks: int, hidden_states, topk_idx, workspace, str
     import torch
     T, H, k = cfg.num_tokens, cfg.hidden, cfg.top_k
     dev = hidden_states.device
-    send_counts = torch.empty(ranks, dtype=torch.int32, device=dev)
-    send_x = torch.empty((T * k, H), dtype=torch.bfloat16, device=dev)
-    send_expert = torch.empty(T * k, dtype=torch.int32, device=dev)
-    slot_pos = torch.empty((T, k), dtype=torch.int32, device=dev)
+    send_counts = _new(ranks, torch.int32, dev, stream)
+    send_x = _new((T * k, H), torch.bfloat16, dev, stream)
+    send_expert = _new(T * k, torch.int32, dev, stream)
+    slot_pos = _new((T, k), torch.int32, dev, stream)
     c = cfg.c()
     _check(_load().moe_ep_dispatch(ctypes.byref(c), int(ranks), _ptr(hidden_states), _ptr(topk_idx),
                                    _ptr(send_counts), _ptr(send_x), _ptr(send_expert), _ptr(slot_pos),
@@ -364,9 +377,9 @@ def forward_rows(cfg: Config, rows, expert_of_row, weights, w13_bias=None, w2_bi
     import torch
     N, H = cfg.num_tokens, cfg.hidden
     if o_rows is None:
-        o_rows = torch.empty((N, H), dtype=torch.float32, device=rows.device)
+        o_rows = _new((N, H), torch.float32, rows.device, stream)
     if workspace is None:
-        workspace = new_workspace(cfg, rows.device)
+        workspace = _new(workspace_size(cfg), torch.uint8, rows.device, stream)
     c = cfg.c()
     w13_t, w13s_t, w2_t, w2s_t = weights
     _check(_load().moe_forward_rows(ctypes.byref(c), _ptr(rows), _ptr(expert_of_row), _ptr(w13_t), _ptr(w13s_t),
@@ -382,7 +395,7 @@ def combine_rows(cfg: Config, o_rows, slot_pos, topk_weights, y=None, status=Non
     import torch
     T, H = cfg.num_tokens, cfg.hidden
     if y is None:
-        y = torch.empty((T, H), dtype=torch.bfloat16, device=slot_pos.device)
+        y = _new((T, H), torch.bfloat16, slot_pos.device, stream)
     c = cfg.c()
     n = int(o_rows.shape[0])
     _check(_load().moe_combine_rows(ctypes.byref(c), _ptr(o_rows) if n else None, n, _ptr(slot_pos),
@@ -397,9 +410,9 @@ def forward(cfg: Config, hidden_states, weights, router_logits=None, per_expert_
     transform_weights.  Returns y (bf16 [T, H])."""
     import torch
     if y is None:
-        y = torch.empty((cfg.num_tokens, cfg.hidden), dtype=torch.bfloat16, device=hidden_states.device)
+        y = _new((cfg.num_tokens, cfg.hidden), torch.bfloat16, hidden_states.device, stream)
     if workspace is None:
-        workspace = new_workspace(cfg, hidden_states.device)
+        workspace = _new(workspace_size(cfg), torch.uint8, hidden_states.device, stream)
     c = cfg.c()
     args = [ctypes.byref(c), _ptr(hidden_states), _ptr(router_logits), _ptr(per_expert_scale),
             _ptr(topk_idx), _ptr(topk_weights), *[_ptr(w) for w in weights], _ptr(w13_bias),
@@ -420,7 +433,7 @@ def forward_static_workspace(cfg: Config, hidden_states, weights, router_logits=
     memory; `y` should be preallocated by such callers."""
     import torch
     if y is None:
-        y = torch.empty((cfg.num_tokens, cfg.hidden), dtype=torch.bfloat16, device=hidden_states.device)
+        y = _new((cfg.num_tokens, cfg.hidden), torch.bfloat16, hidden_states.device, stream)
     c = cfg.c()
     _check(_load().moe_forward_static_workspace(
         ctypes.byref(c), _ptr(hidden_states), _ptr(router_logits), _ptr(per_expert_scale),
@@ -441,7 +454,7 @@ def debug_unfused_gate_up(cfg: Config, hidden_states, topk_idx, weights, workspa
     Returns h [A, 2I] fp32 (columns in the transformed order)."""
     import torch
     A = cfg.num_tokens * (cfg.top_k + cfg.shared_experts)
-    h = torch.empty((A, 2 * cfg.inter), dtype=torch.float32, device=hidden_states.device)
+    h = _new((A, 2 * cfg.inter), torch.float32, hidden_states.device, stream)
     c = cfg.c()
     w13_t, w13s_t = weights[0], weights[1]
     _check(_load().moe_debug_unfused_gate_up(ctypes.byref(c), _ptr(hidden_states), _ptr(topk_idx), _ptr(w13_t),
@@ -491,19 +504,6 @@ def _arg(t, name: str, shape, dtype, dev):
             f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
-def _new(like, shape, dtype, stream):
-    """A tensor that the call allocates, from the pool of the stream that it runs on: a block of the current stream's
-    pool may still be in use there.  Once freed it is kept until the current stream, too, has passed."""
-    import torch
-    if stream is None:
-        return like.new_empty(shape, dtype=dtype)
-    current = torch.cuda.current_stream(like.device)
-    with torch.cuda.stream(stream):
-        t = like.new_empty(shape, dtype=dtype)
-    t.record_stream(current)
-    return t
-
-
 def quantized_size(rows: int, cols: int):
     """(bytes of the codes, bytes of the scales, scale_rows) of quantized rows."""
     out = [ctypes.c_size_t() for _ in range(3)]
@@ -541,7 +541,7 @@ def transform_linear_weights(cfg: LinearConfig, w, w_scale, stream=None):
     import torch
     dev = _device_of(w, "w")
     K, N, g = cfg.in_features, cfg.out_features, 128 if cfg.recipe == 0 else 32
-    outs = [_new(w, n, torch.uint8, stream) for n in transformed_linear_size(cfg)]
+    outs = [_new(n, torch.uint8, w.device, stream) for n in transformed_linear_size(cfg)]
     c = cfg.c()
     _check(_load().moe_transform_linear_weights(
         ctypes.byref(c), _arg(w, "w", (K, N // 2 if cfg.recipe == 2 else N), torch.uint8, dev),

@@ -78,3 +78,37 @@ def test_results_that_the_current_stream_still_reads(name):
             held.append([torch.full_like(t, 77) for t in want])
     torch.cuda.synchronize()
     assert all(torch.equal(rows(a), rows(b)) for c in copies for a, b in zip(c, want))
+
+
+def test_the_layer_and_its_gate():
+    """The same of the layer's own calls: what they return, and the workspace of a call that is given none."""
+    import synth
+    prob = synth.make_problem("tiny")
+    d = prob.to("cuda:0")
+    cfg = moe.Config(**prob.shape.cfg())
+    weights = moe.transform_weights(cfg, d.w13, d.w13_scale, d.w2, d.w2_scale)
+    nw, rw, eps = synth.make_gate(prob.shape)
+    nw, rw = nw.cuda(), rw.cuda()
+    gw = moe.transform_gate_weights(cfg, nw, rw)
+    calls = [lambda s: [moe.forward(cfg, d.x, weights, router_logits=d.logits, stream=s)],
+             lambda s: list(moe.route(cfg, d.logits, stream=s)), lambda s: list(moe.gate(cfg, d.x, gw, eps, stream=s)),
+             lambda s: list(moe.transform_weights(cfg, d.w13, d.w13_scale, d.w2, d.w2_scale, stream=s)),
+             lambda s: [moe.transform_gate_weights(cfg, nw, rw, stream=s)]]
+    for call in calls:
+        want = [t.clone() for t in call(None)]
+        sizes = [t.numel() * t.element_size() for t in want] + [moe.workspace_size(cfg)]
+        side = torch.cuda.Stream()
+        for _ in range(3):
+            torch.cuda.synchronize()
+            blocks = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(2)]
+            spans = [(b.data_ptr(), b.data_ptr() + b.numel()) for b in blocks]
+            side.wait_stream(torch.cuda.current_stream())
+            torch.cuda._sleep(20_000_000)
+            for b in blocks:
+                b.fill_(0xFF)
+            del blocks, b
+            got = call(side)
+            assert not any(lo <= t.data_ptr() < hi for t in got for lo, hi in spans)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+            del got
