@@ -15,8 +15,9 @@
 // memory: a group of 128 x 128 sums reads the weight scales once a row (broadcasts, 270 cycles of its
 // bandwidth), beside the operands' TMA writes (190) and the MMAs' reads (256).  Two row blocks share the
 // loads of the weights and of their scales (a thread has a row of each).  The scales have a ring of
-// their own, and an operand stage is free when its MMAs are done.  16384 x 4096 x 4096: 306 us, 1.8
-// PFLOP/s, the tensor core active 46% of the time and the issue slots 55%.
+// their own, and an operand stage is free when its MMAs are done.  16384 x 4096 x 4096, codes of normal
+// data, no epilogue inputs: 321 us, 1.7 PFLOP/s, in a short run at 1.9 GHz, and 375 us in a long one at the
+// power limit (1.4 to 1.5 GHz); the tensor core active 45% of the time and the issue slots 56% (8192 tokens).
 //
 // Threads (640): warp 0 TMA producer, warp 1 MMA issuer (the even CTA's, for both), warp 2 scales,
 // warp 3 idle, warps 4-19 epilogue (TMEM lanes 32 (w % 4).., 32 columns each).  Units go column block
@@ -420,9 +421,10 @@ static cudaError_t launch_fp32(const LinearArgs& a, const LinearMaps& m, int num
 
 // Tiles of 512 tokens where their rounds are estimated to take no longer than those of 256: a round is a time per K
 // group and one for the tile's start and epilogue, 0.58 and 2.5 us against 0.34 and 0.9, fitted to 2048 to 16384
-// tokens with K 512 to 7168.  16384 x 4096 x 4096: 305 us against 320; 16384 x 7168 x 2048: 263 against 321; in 7
-// rounds instead of 13, 4096 x 7168 x 7168: 213 against 232; but in 3 instead of 5, 2560 x 4096 x 4096: 65 against
-// 63, and with four groups, 8192 x 512 x 6144: 53 against 49.
+// tokens with K 512 to 7168.  Normal data, short runs of 12 calls on three sets of buffers: 16384 x 4096 x 4096: 321 us
+// against 335; 16384 x 7168 x 2048: 285 against 346; in 7 rounds instead of 13, 4096 x 7168 x 7168: 224 against 241;
+// but in 3 instead of 5, 2560 x 4096 x 4096: 59 against 58, and with four groups, 8192 x 512 x 6144: 48 against 46.
+// (Long runs, at the power limit: 375 and 380, 340 and 404, 260 and 279; 63 and 64, 51 and 50.)
 cudaError_t launch_linear_fp32(const LinearArgs& a, const LinearMaps& m, int num_sms, cudaStream_t s) {
     const long long pairs = num_sms / 2, nt = (a.N + kN - 1) / kN, KB = a.K / kTileK;
     auto rounds = [&](int rows) { return ((a.T + rows - 1) / rows * nt + pairs - 1) / pairs; };
@@ -432,7 +434,10 @@ cudaError_t launch_linear_fp32(const LinearArgs& a, const LinearMaps& m, int num
 
 // The narrow kernel takes a product when its estimated time is below the pair kernel's.  Both estimates
 // (ns) are a start and a time per K group of the busiest SM, fitted to products of 16 to 2048 tokens with
-// K 512 to 7168 and N 512 to 12288 in a graph: narrow 3.3 us (32 tokens) or 5 us (64) for each round of two
+// K 512 to 7168 and N 512 to 12288 in a graph, the pair kernel's with tiles of 256 tokens and 128 or 192 columns
+// alone (where a larger tile is chosen below, it takes less than this says); two CTAs that share an SM count as two
+// rounds of its K groups.  Of 252 products 9 go to a kernel that is more than 8% slower: 512 x 7168 x 2048 with 4-bit
+// weights to the pair kernel, 17.5 us against 15.4, 16 x 4096 x 12288 likewise, 14.7 against 9.5.  Narrow 3.3 us (32 tokens) or 5 us (64) for each round of two
 // CTAs an SM, 0.32 us a group (block-scaled 0.26); pair 3.2 us and 0.28 us a group (4.2 us, 0.225 us).  At
 // 64 x 2816 x 2816 that is 6.9 against 9.4 us (measured 7.8 and 9.5), at 256 tokens 12 against 9.4 (12.6
 // and 9.8).

@@ -4,14 +4,15 @@
 // 32-deep block itself and accumulates the whole K in TMEM, so nothing is promoted.
 //
 // CTA pairs (cta_group::2), persistent: a tile is 256 tokens x 256 or 192 columns, each CTA of the pair
-// holding 128 token rows and half of the weight rows.  What bounds it is shared memory: the MMAs of a
-// 128-deep stage read the CTA's token rows and all of the tile's weight rows (48 KB at 256 columns, 40 at
+// holding 128 token rows and half of the weight rows.  What is taken to bound it, by a count of bytes (no
+// counter shows the tensor core's operand reads), is shared memory: the MMAs of a 128-deep stage read the CTA's token rows and all of the tile's weight rows (48 KB at 256 columns, 40 at
 // 192: 384 and 320 cycles), beside 32 (28) KB of TMA writes, 640 (544) cycles for MMAs of 512 (384).
 // 192 columns leave TMEM for two accumulators beside the scale factors (12 columns a stage), so that a
 // tile's epilogue overlaps the next tile's MMAs; 256 leave one, whose sums the epilogue takes into
 // registers before it works on them, so that the MMAs wait for that alone.  (With 128 x 128 tiles of one CTA the same
-// loop took 735 cycles a stage for MMAs of 256.)  Measured: 16384 x 4096 x 4096 208 us, 2.6 PFLOP/s (192
-// columns: 243), 4096 x 7168 x 7168 150 us, 2.8 PFLOP/s (161).
+// loop took 735 cycles a stage for MMAs of 256.)  Measured on normal data in short runs: 16384 x 4096 x 4096 211 us,
+// 2.6 PFLOP/s (192 columns: 245), 4096 x 7168 x 7168 150 us, 2.8 PFLOP/s (165); at the power limit 245 (286) and 175
+// (193).
 //
 // Scale factors: a CTA's SFA are its own rows', SFB the whole tile's in both CTAs; word 4i + c of a
 // 512-byte atom = the four scale bytes of row 32c + i.  A 192-column tile's columns start in the middle of
@@ -341,8 +342,9 @@ cudaError_t launch_linear_mx(const LinearArgs& a, const LinearMaps& m, int num_s
 
 // The tile whose rounds are estimated to take less: a round is a time per K group and one for the tile's start and
 // epilogue, 0.32 and 0.7 us with 192 columns, 0.38 and 0.9 with 256, fitted to 300 to 16384 tokens with K 512 to
-// 7168.  16384 x 7168 x 2048 (7 rounds of 256, 10 of 192): 208 against 252 us; 512 x 2048 x 8192 (1 and 2): 12 against
-// 14; but 1024 x 7168 x 2048 (1 and 1): 23 against 20.5, and 1237 x 768 x 4226 (2 and 2): 13 against 11.
+// 7168.  Normal data, short runs: 16384 x 7168 x 2048 (7 rounds of 256, 10 of 192): 206 against 255 us; 512 x 2048 x
+// 8192 (1 and 2): 12 against 14; but 1024 x 7168 x 2048 (1 and 1): 23.6 against 22.8, and 1237 x 768 x 4226 (2 and 2):
+// 12.7 against 10.7.
 int linear_mx_cols(const LinearArgs& a, int num_sms) {
     const long long pairs = num_sms / 2, mt = (a.T + kPairM - 1) / kPairM, KB = a.K / kTileK;
     auto rounds = [&](int cols) { return (mt * ((a.N + cols - 1) / cols) + pairs - 1) / pairs; };

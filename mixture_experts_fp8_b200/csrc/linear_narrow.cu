@@ -12,7 +12,7 @@
 // the token, one bulk copy per owner, which adds them in rank order and runs the epilogue.  (Plain
 // distributed-shared-memory stores of the same sums took 14000 cycles at 64 tokens.)
 // What bounds it: the weight bytes, and at one token the latency of one load, one MMA chain and the
-// exchange.  Back to back: 1 x 7168 x 2048 MXFP8 5.6 us (15 MB, 2.7 TB/s), 64 x 2816 x 2816 with fp32
+// exchange.  In a graph: 1 x 7168 x 2048 MXFP8 5.8 us (15 MB, 2.6 TB/s), 64 x 2816 x 2816 with fp32
 // scales and a residual 8.0 us.  Every wait is bounded.
 #include "linear_common.cuh"
 

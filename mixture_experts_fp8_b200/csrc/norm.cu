@@ -7,8 +7,8 @@
 //   recipes 1, 2: s = 2^e per 32 columns, e the smallest with amax <= 448 * 2^e; q = e4m3(y * 2^-e)
 // Scales are stored as every GEMM of the library reads them: [H/128][scale_rows] 4-byte words.
 //
-// Bound: HBM, each row read once and each output written once.  Back to back: 16384 x 4096 with a bf16 residual and
-// fp32 scales (606 MB) 101 us, 6.0 TB/s; 4096 x 7168 with an fp32 residual and MXFP8 (383 MB) 66 us, 5.8 TB/s; a copy
+// Bound: HBM, each row read once and each output written once.  In a graph: 16384 x 4096 with a bf16 residual and
+// fp32 scales (606 MB) 102 us, 5.9 TB/s; 4096 x 7168 with an fp32 residual and MXFP8 (383 MB) 71 us, 5.4 TB/s; a copy
 // reaches 6.5.  64 x 2816 takes 3 us, the latency of a launch, a load, the sum over the block and a store.
 #include "block_kernels.h"
 #include "moe_common.cuh"
@@ -69,7 +69,7 @@ __device__ __forceinline__ float group16_max(float m) {
 // as a torch program on the GPU computes amax / 448.0, so that its codes are these; the layer's own
 // quantizer divides, which can differ by one ulp of the scale.
 // v / s is v times the reciprocal of s and the reciprocal's own remainder, v ih + v il: within 2^-46 of the
-// quotient before its one rounding, in two instructions where an IEEE division takes about ten.
+// quotient before its one rounding (16384 x 4096: 108 us in calls, 117 with a division).
 __device__ __forceinline__ uint2 quant_fp32(const float* v, float amax, float& s) {
     s = __fmul_rn(amax, 1.0f / 448.0f);
     if (!(s > 0.0f)) s = 1.0f;                         // nothing, or less than the smallest scale: codes of zero
