@@ -112,3 +112,54 @@ def test_the_layer_and_its_gate():
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(got, want))
             del got
+
+
+@pytest.mark.parametrize("name", ["add_rms_norm", "linear", "balance_loss", "route_backward"])
+def test_captured_on_a_side_stream(name):
+    """A graph that forks to another stream for the call and joins it again."""
+    call = problems()[name]
+    want = [t.clone() for t in call(None)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cur = torch.cuda.current_stream()
+        side.wait_stream(cur)
+        first = call(side)
+        second = call(side)
+        cur.wait_stream(side)
+        copies = [t.clone() for t in first]
+    for _ in range(2):
+        for t in (*first, *second, *copies):
+            t.fill_(0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for got in (first, second, copies):
+            assert all(torch.equal(rows(a), rows(b)) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("T,K,N,recipe", [(16, 1024, 512, 0), (64, 1024, 512, 1), (300, 768, 514, 0), (2048, 256, 2304, 0),
+                                          (2048, 1152, 4096, 0), (2048, 1152, 4095, 1), (1500, 256, 2048, 2), (2048, 1152, 4096, 1)])
+def test_a_chain_in_place(T, K, N, recipe):
+    """Products that add to one buffer one after the other, with nothing between them: each reads what the last one
+    wrote, though its blocks start while that one's are still running."""
+    g = torch.Generator().manual_seed(6)
+    codes, scales, _ = (t.cuda() for t in random_weights(g, K, N, recipe))
+    lin = moe.LinearConfig(T, K, N, recipe)
+    w = moe.transform_linear_weights(lin, codes, scales)
+    q = moe.add_rms_norm(moe.Config(T, K, 128, 8, 1, recipe=recipe), torch.randn((T, K), generator=g).bfloat16().cuda(),
+                         torch.ones(K, device="cuda"), 1e-6)[2]
+    ws = moe.new_linear_workspace(lin)
+    start = torch.randn((T, N), generator=g).bfloat16().cuda()
+
+    def chain(wait):
+        y = start.clone()
+        torch.cuda.synchronize()
+        for _ in range(12):
+            moe.linear(lin, w, quantized=q, residual=y, y=y, workspace=ws)
+            if wait:
+                torch.cuda.synchronize()
+        return y
+    want = chain(True)
+    for _ in range(5):
+        assert torch.equal(chain(False), want)
