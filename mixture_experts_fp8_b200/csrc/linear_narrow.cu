@@ -135,7 +135,6 @@ __global__ void __launch_bounds__(kSThreads, 2)
     float acc[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[j] = 0.0f;
-    bool gave_up = false;                              // this role, on a wait that ran out
 
     if (warp == 0) {
         // ---------------------------------------------------------------------- TMA producer
@@ -181,7 +180,6 @@ __global__ void __launch_bounds__(kSThreads, 2)
         }
         if (!ok)
             for (int i = it > ST ? it - ST : 0; i < it; ++i) drain_wait(&full[i % ST], (i / ST) & 1);
-        gave_up = !ok;
     } else if (warp == 2) {
         if (MX) {
             // -------------------------------------------------------------------- token-scale atoms
@@ -317,8 +315,7 @@ __global__ void __launch_bounds__(kSThreads, 2)
                 }
             }
         }
-        gave_up = !__all_sync(0xffffffffu, ok);
-        if (gave_up) {
+        if (!__all_sync(0xffffffffu, ok)) {
 #pragma unroll
             for (int j = 0; j < NT; ++j) acc[j] = __int_as_float(0x7fc00000);   // a wait ran out: NaN
         }
@@ -353,16 +350,15 @@ __global__ void __launch_bounds__(kSThreads, 2)
             for (int j = 0; j < NT; ++j) own[j * 128] = acc[j];
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        if (__syncthreads_or(gave_up)) {               // a copy that came late may have landed on them
-            if (warp >= 4) {
-                float* own = reinterpret_cast<float*>(smem) + row;
-#pragma unroll 1
-                for (int j = 0; j < NT; ++j) own[j * 128] = __int_as_float(0x7fc00000);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            }
-            __syncthreads();
-        }
+        __syncthreads();
         cluster_wait();                                // every CTA of the cluster has set its barrier up
+        if (warp == 4 && __any_sync(0xffffffffu, *abort_flag != 0)) {   // a copy that came late may have landed on them
+            float* own = reinterpret_cast<float*>(smem);
+#pragma unroll 1
+            for (int i = lane; i < NT * 128; i += 32) own[i] = __int_as_float(0x7fc00000);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+        }
         if (warp == 4 && lane < split && t0 + lane * per < p.T) {   // lane r sends rank r its tokens
             const uint32_t bytes = static_cast<uint32_t>(per * 512);
             const uint32_t to = static_cast<uint32_t>(lane);
